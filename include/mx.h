@@ -40,7 +40,7 @@
  *
  * Ownership and execution
  *  - Every pointer argument is a DEVICE pointer owned by the caller, except
- *    `offs` of the grouped calls (host).  The library never allocates, frees or
+ *    `offs` of the grouped calls (host; mx_gemv_grouped takes device offsets).  The library never allocates, frees or
  *    synchronizes; it keeps no state between calls, so every entry point is
  *    reentrant.  Work is enqueued on `stream` (a hipStream_t; NULL = default
  *    stream) and the call returns before it runs.
@@ -76,6 +76,7 @@ typedef enum {
 enum { MX_F32 = 0, MX_BF16 = 1 };   /* element types of unquantized tensors */
 enum { MX_ROW = 0, MX_COL = 1 };    /* 1x32 blocks along cols / 32x1 blocks along rows */
 enum { MX_RNE = 0, MX_SR = 1 };     /* Q_D: nearest, ties to even / Q_S: stochastic */
+enum { MX_I32 = 0, MX_I64 = 1 };    /* types of expert ids */
 
 /* Largest number of groups mx_gemm_grouped accepts. */
 #define MX_MAX_GROUPS 128
@@ -376,6 +377,99 @@ int mx_grouped_linear_bwd(const void* dy, int dtype, const int64_t* offs, int64_
                           const uint8_t* wq_codes, const uint8_t* wq_scales, uint64_t seed,
                           float* dx, float* dw, void* workspace, size_t workspace_bytes,
                           void* stream);
+
+/* ------------------------------------------------------------------ few rows
+ * mx_gemv: y[m][n] = alpha * sum_k x[m][k] * deq(W)[n][k] -- unquantized rows x
+ * (x_dtype MX_F32 or MX_BF16, rows ldx >= K elements apart) times a packed MX_ROW
+ * weight [N, K] (w_codes [N][K/2]; scale rows w_scale_ld >= K/32 bytes apart, as
+ * mx_quantize_ld writes them): the product of a layer whose weights stay packed
+ * while a few tokens are decoded.  y (y_dtype) has rows ldy >= N elements apart.
+ * Any M, N >= 0 below 2^31 (M or N == 0: no-op) and K % 32 == 0 below 2^31 (K == 0:
+ * y = 0, x and the weights may be NULL); the weights are read once per 64 rows, so
+ * many rows cost as many passes.  x is used to its full precision (a float32 x down to bits
+ * of 2^-133): products are exact, sums are float32 in a fixed order, and one
+ * rounding to nearest even gives a bf16 y.  A weight block with scale byte 0xFF makes
+ * its sums NaN; deq(W) is +-Inf where it passes the float32 range (bytes 253 and 254,
+ * which no quantizer writes). */
+int mx_gemv(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_codes,
+            const uint8_t* w_scales, int64_t w_scale_ld, int64_t M, int64_t N, int64_t K,
+            float alpha, void* y, int y_dtype, int64_t ldy, void* stream);
+
+/* mx_gemv_grouped: mx_gemv per expert, without the host: offs is a DEVICE array of
+ * groups+1 non-decreasing row offsets (mx_moe_plan's), offs[0] == 0.  Rows
+ * offs[g] .. offs[g+1]-1 of y use W_g, the g-th [N, K] matrix (w_codes + g*N*K/2,
+ * w_scales + g*N*w_scale_ld).  Row r takes row src[r] / top_k of x [x_rows, K]
+ * (src: mx_moe_plan's slots, so that is the row's token), or row r where src is
+ * NULL.  rows bounds offs[groups] and is the number of rows y and src have room
+ * for; rows of y from offs[groups] on, and rows whose source is outside x, are left
+ * as they were.  1 <= groups <= MX_MAX_GROUPS, top_k >= 1; N, K, alpha, strides
+ * and types as mx_gemv. */
+int mx_gemv_grouped(const void* x, int x_dtype, int64_t ldx, int64_t x_rows, const int32_t* src,
+                    int64_t top_k, const uint8_t* w_codes, const uint8_t* w_scales,
+                    int64_t w_scale_ld, const int64_t* offs, int64_t groups, int64_t rows,
+                    int64_t N, int64_t K, float alpha, void* y, int y_dtype, int64_t ldy,
+                    void* stream);
+
+/* ------------------------------------------------------------------ expert routing
+ * Rows of a mixture-of-experts layer ([ALTO] news paragraph: the MoE model trained
+ * in MXFP4) between token order and the expert order of the grouped products.  Slot
+ * s = token * top_k + j is a token's j-th choice.  top_k >= 1, and tokens * top_k and
+ * rows are below 2^31.
+ *
+ * mx_moe_plan: slots sorted by expert, stably (rows of an expert in slot order).
+ * ids [tokens][top_k] (id_type MX_I32 or MX_I64); an id outside 0 .. experts-1
+ * leaves its slot out (padding tokens).  Writes offs [experts+1] (offs[e] = slots of
+ * the experts before e; offs[experts] = sorted rows R), src [tokens*top_k] (slot of
+ * row r; -1 from row R on) and pos [tokens][top_k] (row of a slot; -1 for one left
+ * out).  1 <= experts <= MX_MAX_GROUPS.  workspace: at least
+ * mx_moe_plan_workspace_size bytes (0: may be NULL), 16-byte aligned.  tokens == 0
+ * writes offs = 0 (ids, src, pos may be NULL).  The grouped products that take host
+ * offsets need offs copied to the host. */
+size_t mx_moe_plan_workspace_size(int64_t tokens, int64_t top_k, int64_t experts);
+int mx_moe_plan(const void* ids, int id_type, int64_t tokens, int64_t top_k, int64_t experts,
+                int64_t* offs, int32_t* src, int32_t* pos, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/* The row calls take pos as mx_moe_plan writes it: entries in 0 .. rows-1, each at
+ * most once; an entry outside that range leaves its slot out.  Rows of an expert-
+ * ordered output that no slot maps to are left as they were.  Row strides (ld*, in
+ * elements) are at least cols.  weights: float32 [tokens][top_k], or NULL for 1; the
+ * weight of a slot left out is not used.
+ *
+ * mx_moe_dispatch: out[pos[t][j]] = weights[t][j] * x[t] for every slot; x [tokens]
+ * [cols] and out [rows][cols] are `dtype`.  Without weights an exact copy (the
+ * gather in front of a grouped product), with weights the gradient of
+ * mx_moe_combine alone.  One read of x. */
+int mx_moe_dispatch(const void* x, int dtype, int64_t ldx, const int32_t* pos,
+                    const float* weights, int64_t tokens, int64_t top_k, int64_t rows,
+                    int64_t cols, void* out, int64_t ldo, void* stream);
+
+/* mx_moe_dispatch_quantize: Q_D of mx_moe_dispatch's copy, the grouped forward's
+ * operand, without the copy: codes [rows][cols/2] and scales (rows scale_ld >=
+ * cols/32 bytes apart) equal, bit for bit, those of mx_quantize_ld (MX_ROW, MX_RNE,
+ * no rotation) on the gathered rows.  cols % 32 == 0. */
+int mx_moe_dispatch_quantize(const void* x, int dtype, int64_t ldx, const int32_t* pos,
+                             int64_t tokens, int64_t top_k, int64_t rows, int64_t cols,
+                             uint8_t* codes, uint8_t* scales, int64_t scale_ld, void* stream);
+
+/* mx_moe_combine: y[t] = sum_j weights[t][j] * z[pos[t][j]] over the token's slots in
+ * order, float32 sums of rounded products, one rounding to y's type; 0 for a token
+ * without slots.  z [rows][cols] (z_dtype), y [tokens][cols] (y_dtype).  Without
+ * weights it is the gradient of mx_moe_dispatch (straight through the quantizer for
+ * mx_moe_dispatch_quantize). */
+int mx_moe_combine(const void* z, int z_dtype, int64_t ldz, int64_t rows, const int32_t* pos,
+                   const float* weights, int64_t tokens, int64_t top_k, int64_t cols, void* y,
+                   int y_dtype, int64_t ldy, void* stream);
+
+/* mx_moe_combine_bwd: gradients of mx_moe_combine, given dy [tokens][cols] (dy_dtype)
+ * and the forward's z, pos and weights:
+ *   dz[pos[t][j]] = weights[t][j] * dy[t]                      (dy_dtype)
+ *   dweights[t][j] = sum_c dy[t][c] * z[pos[t][j]][c]  (float32; 0 for a slot left out)
+ * in one pass over dy and z.  The order of the sums is fixed. */
+int mx_moe_combine_bwd(const void* dy, int dy_dtype, int64_t lddy, const void* z, int z_dtype,
+                       int64_t ldz, int64_t rows, const int32_t* pos, const float* weights,
+                       int64_t tokens, int64_t top_k, int64_t cols, void* dz, int64_t lddz,
+                       float* dweights, void* stream);
 
 /* ------------------------------------------------------------------ de-oscillation
  * Weight de-oscillation as a post-optimizer-step pass ([ALTO] "How does ALTO

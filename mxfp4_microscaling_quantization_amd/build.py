@@ -19,7 +19,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = ROOT / "_build"
 LIB = PKG / "libmx355.so"
-SOURCES = ["quant.hip", "gemm.hip", "linear.hip", "deosc.hip"]
+SOURCES = ["quant.hip", "gemm.hip", "linear.hip", "deosc.hip", "moe.hip", "gemv.hip"]
 # The synthetic optimizer step that drives the de-oscillation workload (a
 # workload generator, not part of the method) lives in a library of its own.
 SYNTH_LIB = PKG / "libmx355_synth.so"

@@ -1,0 +1,557 @@
+// Routing of a mixture-of-experts layer around the grouped products: token
+// slots sorted by expert, rows copied or quantized into expert order, expert
+// rows added up per token with the router's weights, and the gradients.
+//
+// A slot s = token * top_k + j is one of a token's top_k choices.  With pos[s]
+// the sorted row of slot s (-1: the slot takes part in nothing),
+//   dispatch          out[pos[t,j]] = w[t,j] x[t]          (w = 1 without weights)
+//   combine           y[t] = sum_j w[t,j] z[pos[t,j]]
+//   combine gradient  dz[pos[t,j]] = w[t,j] dy[t],  dw[t,j] = <dy[t], z[pos[t,j]]>
+// Dispatch and combine are each other's transposes, so combine without weights
+// is the gradient of a dispatch.  All of them move rows once and compute little:
+// HBM bandwidth bounds them.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_device.h"
+#include "mx_host.h"
+
+namespace mx {
+
+// ============================================================== plan
+// Stable counting sort of the slots by expert; slots without an expert form one
+// more bin behind the last expert, whose rows get src = -1.  Chunks of
+// consecutive slots are counted (k_plan_count), then every chunk places its
+// slots (k_plan_place): rows of bin e start at the total of the bins before it,
+// a chunk's rows of the bin at the sum of the chunks before it, and a slot's
+// place among its own wave's slots of the same bin comes from ballots over the
+// bits of the bin number.  Sums of whole numbers: the result does not depend on
+// the order in which atomics arrive.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kPlanMaxChunks = 256;
+constexpr int kPlanBins = MX_MAX_GROUPS + 1;
+
+struct PlanShape {
+  int64_t slots, chunk;
+  int chunks, experts;
+};
+
+template <typename ID>
+__device__ __forceinline__ int plan_bin(const ID* ids, int64_t s, int experts) {
+  const ID e = ids[s];
+  return e >= 0 && e < (ID)experts ? (int)e : experts;
+}
+
+template <typename ID>
+__global__ __launch_bounds__(kPlanThreads) void k_plan_count(const ID* __restrict__ ids,
+                                                             const PlanShape p,
+                                                             int32_t* __restrict__ counts) {
+  __shared__ int32_t s_cnt[kPlanBins];
+  const int bins = p.experts + 1;
+  for (int e = threadIdx.x; e < bins; e += kPlanThreads) s_cnt[e] = 0;
+  __syncthreads();
+  const int64_t end = min<int64_t>(p.slots, (blockIdx.x + 1) * p.chunk);
+  for (int64_t s = blockIdx.x * p.chunk + threadIdx.x; s < end; s += kPlanThreads)
+    atomicAdd(&s_cnt[plan_bin(ids, s, p.experts)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < bins; e += kPlanThreads)
+    counts[(int64_t)blockIdx.x * bins + e] = s_cnt[e];
+}
+
+template <typename ID>
+__global__ __launch_bounds__(kPlanThreads) void k_plan_place(const ID* __restrict__ ids,
+                                                             const PlanShape p,
+                                                             const int32_t* __restrict__ counts,
+                                                             int64_t* __restrict__ offs,
+                                                             int32_t* __restrict__ src,
+                                                             int32_t* __restrict__ pos) {
+  __shared__ int32_t s_total[kPlanBins];            // slots of each bin
+  __shared__ int32_t s_base[kPlanBins];             // next row of each bin in this chunk
+  __shared__ int32_t s_wave[kPlanWaves][kPlanBins]; // slots of a bin in each wave's 64
+  const int bins = p.experts + 1;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (int e = tid; e < bins; e += kPlanThreads) s_total[e] = s_base[e] = 0;
+  __syncthreads();
+  const int64_t begin = (int64_t)blockIdx.x * p.chunk;
+  const int64_t end = min<int64_t>(p.slots, begin + p.chunk);
+  if (p.chunks == 1) {
+    for (int64_t s = tid; s < end; s += kPlanThreads)
+      atomicAdd(&s_total[plan_bin(ids, s, p.experts)], 1);
+  } else {
+    for (int i = tid; i < p.chunks * bins; i += kPlanThreads) {
+      const int c = i / bins, e = i - c * bins;
+      const int32_t n = counts[i];
+      atomicAdd(&s_total[e], n);
+      if (c < (int)blockIdx.x) atomicAdd(&s_base[e], n);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int32_t row = 0;
+    for (int e = 0; e < bins; ++e) {
+      if (blockIdx.x == 0) offs[e] = row;
+      s_base[e] += row;
+      row += s_total[e];
+    }
+  }
+  for (int64_t s0 = begin; s0 < end; s0 += kPlanThreads) {
+    for (int i = tid; i < kPlanWaves * kPlanBins; i += kPlanThreads) (&s_wave[0][0])[i] = 0;
+    __syncthreads();
+    const int64_t s = s0 + tid;
+    const bool in = s < end;
+    const int bin = in ? plan_bin(ids, s, p.experts) : 0;
+    uint64_t same = __ballot(in);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const uint64_t set = __ballot((bin >> b) & 1);
+      same &= ((bin >> b) & 1) ? set : ~set;
+    }
+    const int before = __popcll(same & ((1ull << lane) - 1));
+    if (in && before == 0) s_wave[wave][bin] = __popcll(same);
+    __syncthreads();
+    for (int e = tid; e < bins; e += kPlanThreads) {
+      int32_t row = s_base[e];
+      for (int w = 0; w < kPlanWaves; ++w) {
+        const int32_t n = s_wave[w][e];
+        s_wave[w][e] = row;
+        row += n;
+      }
+      s_base[e] = row;
+    }
+    __syncthreads();
+    if (in) {
+      const int32_t row = s_wave[wave][bin] + before;
+      const bool real = bin < p.experts;
+      pos[s] = real ? row : -1;
+      src[row] = real ? (int32_t)s : -1;
+    }
+    __syncthreads();
+  }
+}
+
+static PlanShape plan_shape(int64_t slots, int64_t experts) {
+  PlanShape p;
+  p.slots = slots;
+  p.experts = (int)experts;
+  const int64_t per = cdiv(cdiv(slots, kPlanMaxChunks), kPlanThreads);
+  p.chunk = (per > 1 ? per : 1) * kPlanThreads;
+  p.chunks = (int)cdiv(slots, p.chunk);
+  return p;
+}
+
+// ============================================================== rows
+// V consecutive values of a row: V = 8 where every row starts on 16 bytes and
+// the width is a multiple of 8, else one value at a time.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* p, float v[V]);
+template <>
+__device__ __forceinline__ void load_row<float, 1>(const float* p, float v[1]) { v[0] = *p; }
+template <>
+__device__ __forceinline__ void load_row<uint16_t, 1>(const uint16_t* p, float v[1]) {
+  v[0] = bf16_lo(*p);
+}
+template <>
+__device__ __forceinline__ void load_row<float, 8>(const float* p, float v[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load_row<uint16_t, 8>(const uint16_t* p, float v[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x);
+  v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+  v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z);
+  v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T* p, const float v[V]);
+template <>
+__device__ __forceinline__ void store_row<float, 1>(float* p, const float v[1]) { *p = v[0]; }
+template <>
+__device__ __forceinline__ void store_row<uint16_t, 1>(uint16_t* p, const float v[1]) {
+  *p = (uint16_t)f32_to_bf16_rne(v[0]);
+}
+template <>
+__device__ __forceinline__ void store_row<float, 8>(float* p, const float v[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <>
+__device__ __forceinline__ void store_row<uint16_t, 8>(uint16_t* p, const float v[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_rne(v[2 * i]) | f32_to_bf16_rne(v[2 * i + 1]) << 16;
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Position of a thread's run in the flat order (token, run of the row): the
+// workgroup's first index is divided once, the threads' by a 32-bit division.
+struct RowRun {
+  int64_t token;
+  int run;
+};
+__device__ __forceinline__ RowRun row_run(int64_t first, int at, int runs) {
+  const int64_t t0 = first / runs;
+  const uint32_t r = (uint32_t)(first - t0 * runs) + (uint32_t)at;
+  const uint32_t q = r / (uint32_t)runs;
+  return {t0 + q, (int)(r - q * (uint32_t)runs)};
+}
+
+// ============================================================== dispatch
+// One read of a token's run, top_k writes.  The copy moves words of U (as wide as
+// the rows' alignment allows) whatever they hold, so NaN patterns stay as they are.
+template <typename U>
+__global__ __launch_bounds__(256) void k_dispatch_copy(const U* __restrict__ x, int64_t ldx,
+                                                       const int32_t* __restrict__ pos,
+                                                       int64_t tokens, int top_k, int64_t rows,
+                                                       int runs, U* __restrict__ out, int64_t ldo) {
+  const int64_t total = tokens * runs;
+  for (int64_t first = (int64_t)blockIdx.x * 256; first < total; first += (int64_t)gridDim.x * 256) {
+    if (first + threadIdx.x >= total) continue;
+    const RowRun r = row_run(first, threadIdx.x, runs);
+    const U v = x[r.token * ldx + r.run];
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t to = pos[r.token * top_k + j];
+      if (to >= 0 && to < rows) out[to * ldo + r.run] = v;
+    }
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_dispatch_scaled(const T* __restrict__ x, int64_t ldx,
+                                                         const int32_t* __restrict__ pos,
+                                                         int64_t tokens, int top_k, int64_t rows,
+                                                         int runs,
+                                                         const float* __restrict__ weights,
+                                                         T* __restrict__ out, int64_t ldo) {
+  const int64_t total = tokens * runs;
+  for (int64_t first = (int64_t)blockIdx.x * 256; first < total; first += (int64_t)gridDim.x * 256) {
+    if (first + threadIdx.x >= total) continue;
+    const RowRun r = row_run(first, threadIdx.x, runs);
+    float v[V];
+    load_row<T, V>(x + r.token * ldx + (int64_t)r.run * V, v);
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t to = pos[r.token * top_k + j];
+      if (to < 0 || to >= rows) continue;
+      const float w = weights[r.token * top_k + j];
+      float u[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[i] = w * v[i];
+      store_row<T, V>(out + to * ldo + (int64_t)r.run * V, u);
+    }
+  }
+}
+
+// Q_D of a token's 1x32 blocks (a quad of lanes per block, 8 values a lane) once,
+// its codes and scale byte written to the token's top_k rows: the values are the
+// same in each, so one conversion serves them all.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_dispatch_quant(const T* __restrict__ x, int64_t ldx,
+                                                        const int32_t* __restrict__ pos,
+                                                        int64_t tokens, int top_k, int64_t rows,
+                                                        int runs, uint32_t* __restrict__ codes,
+                                                        uint8_t* __restrict__ scales,
+                                                        int64_t scale_ld) {
+  const int64_t total = tokens * runs;  // runs of 8: a multiple of 4 per row
+  for (int64_t first = (int64_t)blockIdx.x * 256; first < total; first += (int64_t)gridDim.x * 256) {
+    if (first + threadIdx.x >= total) continue;  // whole quads: total is a multiple of 4
+    const RowRun r = row_run(first, threadIdx.x, runs);
+    const T* p = x + r.token * ldx + (int64_t)r.run * 8;
+    float v[8];
+    if constexpr (V == 8) {
+      load_row<T, 8>(p, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load_row<T, 1>(p + i, v + i);
+    }
+    const uint32_t byte = scale_byte_of(quad_max_u32(amax_bits<8>(v)));
+    uint32_t w = 0;
+    if (byte != 255u) {
+      const float sc = scale_of(byte);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w |= (cvt_rne_pair(v[2 * i], v[2 * i + 1], sc) & 0xFFu) << (8 * i);
+    }
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t to = pos[r.token * top_k + j];
+      if (to < 0 || to >= rows) continue;
+      codes[(int64_t)to * runs + r.run] = w;
+      if ((r.run & 3) == 0) scales[(int64_t)to * scale_ld + (r.run >> 2)] = (uint8_t)byte;
+    }
+  }
+}
+
+// ============================================================== combine
+// Sums in float32 in slot order, each product rounded first.
+template <typename TZ, typename TY, int V>
+__global__ __launch_bounds__(256) void k_combine(const TZ* __restrict__ z, int64_t ldz, int64_t rows,
+                                                 const int32_t* __restrict__ pos,
+                                                 const float* __restrict__ weights, int64_t tokens,
+                                                 int top_k, int runs, TY* __restrict__ y,
+                                                 int64_t ldy) {
+  const int64_t total = tokens * runs;
+  for (int64_t first = (int64_t)blockIdx.x * 256; first < total; first += (int64_t)gridDim.x * 256) {
+    if (first + threadIdx.x >= total) continue;
+    const RowRun r = row_run(first, threadIdx.x, runs);
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t from = pos[r.token * top_k + j];
+      if (from < 0 || from >= rows) continue;
+      const float w = weights ? weights[r.token * top_k + j] : 1.0f;
+      float v[V];
+      load_row<TZ, V>(z + from * ldz + (int64_t)r.run * V, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += w * v[i];
+    }
+    store_row<TY, V>(y + r.token * ldy + (int64_t)r.run * V, acc);
+  }
+}
+
+// One workgroup per token: dz rows as a weighted dispatch, and each slot's inner
+// product <dy, z> as per-thread sums, then a fixed tree over lanes and waves.
+template <typename TY, typename TZ, int V>
+__global__ __launch_bounds__(256) void k_combine_bwd(
+    const TY* __restrict__ dy, int64_t lddy, const TZ* __restrict__ z, int64_t ldz, int64_t rows,
+    const int32_t* __restrict__ pos, const float* __restrict__ weights, int64_t tokens, int top_k,
+    int runs, TY* __restrict__ dz, int64_t lddz, float* __restrict__ dw) {
+  __shared__ float s_part[4];
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t row = pos[t * top_k + j];
+      const bool real = row >= 0 && row < rows;
+      float part = 0.0f;
+      if (real) {
+        const float w = weights ? weights[t * top_k + j] : 1.0f;
+        for (int r = threadIdx.x; r < runs; r += 256) {
+          float g[V], v[V], u[V];
+          load_row<TY, V>(dy + t * lddy + (int64_t)r * V, g);
+          load_row<TZ, V>(z + row * ldz + (int64_t)r * V, v);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            part += g[i] * v[i];
+            u[i] = w * g[i];
+          }
+          store_row<TY, V>(dz + row * lddz + (int64_t)r * V, u);
+        }
+      }
+#pragma unroll
+      for (int d = 32; d; d >>= 1) part += __shfl_xor(part, d);
+      if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = part;
+      __syncthreads();
+      if (threadIdx.x == 0)
+        dw[t * top_k + j] = real ? (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]) : 0.0f;
+      __syncthreads();
+    }
+  }
+}
+
+// ============================================================== launches
+static unsigned row_grid(int64_t work_items) {
+  return (unsigned)hmin(cdiv(work_items, 256), (int64_t)device_cu_count() * 64);
+}
+
+// Whether rows of `ld` elements of `size` bytes all start on 16 bytes.
+static bool rows16(int64_t ld, int size) { return ld * size % 16 == 0; }
+static int size_of(int dtype) { return dtype == MX_BF16 ? 2 : 4; }
+static bool is_float_type(int t) { return t == MX_F32 || t == MX_BF16; }
+constexpr int64_t kMax31 = (int64_t)1 << 31;
+
+// Sizes every row call shares: tokens * top_k and the output rows fit 32-bit positions.
+static bool routed_shape(int64_t tokens, int64_t top_k, int64_t cols, int64_t rows) {
+  return tokens >= 0 && top_k >= 1 && top_k < kMax31 && cols >= 0 && cols < kMax31 && rows >= 0 &&
+         rows < kMax31 && tokens <= (kMax31 - 1) / top_k;
+}
+
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" size_t mx_moe_plan_workspace_size(int64_t tokens, int64_t top_k, int64_t experts) {
+  if (!routed_shape(tokens, top_k, 0, 0) || experts < 1 || experts > MX_MAX_GROUPS) return 0;
+  const PlanShape p = plan_shape(tokens * top_k, experts);
+  return p.chunks > 1 ? (size_t)p.chunks * (experts + 1) * sizeof(int32_t) : 0;
+}
+
+extern "C" int mx_moe_plan(const void* ids, int id_type, int64_t tokens, int64_t top_k,
+                           int64_t experts, int64_t* offs, int32_t* src, int32_t* pos,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  MX_REQUIRE(routed_shape(tokens, top_k, 0, 0) && experts >= 1 && experts <= MX_MAX_GROUPS,
+             MX_ERR_SHAPE);
+  MX_REQUIRE(id_type == MX_I32 || id_type == MX_I64, MX_ERR_ENUM);
+  MX_REQUIRE(offs, MX_ERR_NULL);
+  const int64_t slots = tokens * top_k;
+  if (slots) MX_REQUIRE(ids && src && pos, MX_ERR_NULL);
+  MX_REQUIRE(aligned16(ids) && aligned16(offs) && aligned16(src) && aligned16(pos), MX_ERR_ALIGN);
+  const PlanShape p = plan_shape(slots, experts);
+  const size_t need = mx_moe_plan_workspace_size(tokens, top_k, experts);
+  if (need) {
+    MX_REQUIRE(workspace && workspace_bytes >= need, MX_ERR_WORKSPACE);
+    MX_REQUIRE(aligned16(workspace), MX_ERR_ALIGN);
+  }
+  const hipStream_t st = as_stream(stream);
+  int32_t* counts = static_cast<int32_t*>(workspace);
+  const unsigned grid = p.chunks ? p.chunks : 1;  // no slots: one workgroup writes offs = 0
+  if (id_type == MX_I32) {
+    const int32_t* e = static_cast<const int32_t*>(ids);
+    if (need) k_plan_count<<<grid, kPlanThreads, 0, st>>>(e, p, counts);
+    k_plan_place<<<grid, kPlanThreads, 0, st>>>(e, p, counts, offs, src, pos);
+  } else {
+    const int64_t* e = static_cast<const int64_t*>(ids);
+    if (need) k_plan_count<<<grid, kPlanThreads, 0, st>>>(e, p, counts);
+    k_plan_place<<<grid, kPlanThreads, 0, st>>>(e, p, counts, offs, src, pos);
+  }
+  return launch_status();
+}
+
+extern "C" int mx_moe_dispatch(const void* x, int dtype, int64_t ldx, const int32_t* pos,
+                               const float* weights, int64_t tokens, int64_t top_k, int64_t rows,
+                               int64_t cols, void* out, int64_t ldo, void* stream) {
+  MX_REQUIRE(is_float_type(dtype), MX_ERR_ENUM);
+  MX_REQUIRE(routed_shape(tokens, top_k, cols, rows) && ldx >= cols && ldo >= cols, MX_ERR_SHAPE);
+  if (tokens == 0 || cols == 0 || rows == 0) return MX_OK;
+  MX_REQUIRE(x && pos && out, MX_ERR_NULL);
+  MX_REQUIRE(aligned16(x) && aligned16(pos) && aligned16(out) && aligned16(weights), MX_ERR_ALIGN);
+  const int64_t sz = size_of(dtype);
+  const hipStream_t st = as_stream(stream);
+  if (!weights) {
+    // the widest word that divides the rows and their strides
+    const int64_t all = cols * sz | ldx * sz | ldo * sz;
+    const int64_t word = all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
+    const int runs = (int)(cols * sz / word);
+    const dim3 grid(row_grid(tokens * runs));
+#define MX_COPY(U)                                                                            \
+  k_dispatch_copy<U><<<grid, 256, 0, st>>>(static_cast<const U*>(x), ldx * sz / word, pos,    \
+                                           tokens, (int)top_k, rows, runs,                    \
+                                           static_cast<U*>(out), ldo * sz / word)
+    if (word == 16) MX_COPY(uint4);
+    else if (word == 8) MX_COPY(uint2);
+    else if (word == 4) MX_COPY(uint32_t);
+    else MX_COPY(uint16_t);
+#undef MX_COPY
+    return launch_status();
+  }
+  const bool wide = cols % 8 == 0 && rows16(ldx, (int)sz) && rows16(ldo, (int)sz);
+  const int runs = (int)(wide ? cols / 8 : cols);
+  const dim3 grid(row_grid(tokens * runs));
+#define MX_DISPATCH(T, V)                                                                        \
+  k_dispatch_scaled<T, V><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, pos, tokens,      \
+                                                (int)top_k, rows, runs, weights,                 \
+                                                static_cast<T*>(out), ldo)
+  if (dtype == MX_F32) {
+    if (wide) MX_DISPATCH(float, 8);
+    else MX_DISPATCH(float, 1);
+  } else {
+    if (wide) MX_DISPATCH(uint16_t, 8);
+    else MX_DISPATCH(uint16_t, 1);
+  }
+#undef MX_DISPATCH
+  return launch_status();
+}
+
+extern "C" int mx_moe_dispatch_quantize(const void* x, int dtype, int64_t ldx, const int32_t* pos,
+                                        int64_t tokens, int64_t top_k, int64_t rows, int64_t cols,
+                                        uint8_t* codes, uint8_t* scales, int64_t scale_ld,
+                                        void* stream) {
+  MX_REQUIRE(is_float_type(dtype), MX_ERR_ENUM);
+  MX_REQUIRE(routed_shape(tokens, top_k, cols, rows) && cols % 32 == 0 && ldx >= cols &&
+                 scale_ld >= cols / 32, MX_ERR_SHAPE);
+  if (tokens == 0 || cols == 0 || rows == 0) return MX_OK;
+  MX_REQUIRE(x && pos && codes && scales, MX_ERR_NULL);
+  MX_REQUIRE(aligned16(x) && aligned16(pos) && aligned16(codes) && aligned16(scales), MX_ERR_ALIGN);
+  const bool wide = rows16(ldx, size_of(dtype));
+  const int runs = (int)(cols / 8);
+  const dim3 grid(row_grid(tokens * runs));
+  const hipStream_t st = as_stream(stream);
+#define MX_DISPATCHQ(T, V)                                                                        \
+  k_dispatch_quant<T, V><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, pos, tokens,         \
+                                               (int)top_k, rows, runs,                             \
+                                               reinterpret_cast<uint32_t*>(codes), scales, scale_ld)
+  if (dtype == MX_F32) {
+    if (wide) MX_DISPATCHQ(float, 8);
+    else MX_DISPATCHQ(float, 1);
+  } else {
+    if (wide) MX_DISPATCHQ(uint16_t, 8);
+    else MX_DISPATCHQ(uint16_t, 1);
+  }
+#undef MX_DISPATCHQ
+  return launch_status();
+}
+
+extern "C" int mx_moe_combine(const void* z, int z_dtype, int64_t ldz, int64_t rows,
+                              const int32_t* pos, const float* weights, int64_t tokens,
+                              int64_t top_k, int64_t cols, void* y, int y_dtype, int64_t ldy,
+                              void* stream) {
+  MX_REQUIRE(is_float_type(z_dtype) && is_float_type(y_dtype), MX_ERR_ENUM);
+  MX_REQUIRE(routed_shape(tokens, top_k, cols, rows) && ldz >= cols && ldy >= cols, MX_ERR_SHAPE);
+  if (tokens == 0 || cols == 0) return MX_OK;
+  MX_REQUIRE(pos && y, MX_ERR_NULL);
+  if (rows) MX_REQUIRE(z, MX_ERR_NULL);  // no rows: y = 0, z is not read
+  MX_REQUIRE(aligned16(z) && aligned16(pos) && aligned16(weights) && aligned16(y), MX_ERR_ALIGN);
+  const bool wide = cols % 8 == 0 && rows16(ldz, size_of(z_dtype)) && rows16(ldy, size_of(y_dtype));
+  const int runs = (int)(wide ? cols / 8 : cols);
+  const dim3 grid(row_grid(tokens * runs));
+  const hipStream_t st = as_stream(stream);
+#define MX_COMBINE(TZ, TY)                                                                       \
+  do {                                                                                           \
+    const TZ* zt = static_cast<const TZ*>(z);                                                    \
+    TY* yt = static_cast<TY*>(y);                                                                \
+    if (wide) k_combine<TZ, TY, 8><<<grid, 256, 0, st>>>(zt, ldz, rows, pos, weights, tokens,    \
+                                                         (int)top_k, runs, yt, ldy);             \
+    else k_combine<TZ, TY, 1><<<grid, 256, 0, st>>>(zt, ldz, rows, pos, weights, tokens,         \
+                                                    (int)top_k, runs, yt, ldy);                  \
+  } while (0)
+  if (z_dtype == MX_F32) {
+    if (y_dtype == MX_F32) MX_COMBINE(float, float);
+    else MX_COMBINE(float, uint16_t);
+  } else {
+    if (y_dtype == MX_F32) MX_COMBINE(uint16_t, float);
+    else MX_COMBINE(uint16_t, uint16_t);
+  }
+#undef MX_COMBINE
+  return launch_status();
+}
+
+extern "C" int mx_moe_combine_bwd(const void* dy, int dy_dtype, int64_t lddy, const void* z,
+                                  int z_dtype, int64_t ldz, int64_t rows, const int32_t* pos,
+                                  const float* weights, int64_t tokens, int64_t top_k,
+                                  int64_t cols, void* dz, int64_t lddz, float* dweights,
+                                  void* stream) {
+  MX_REQUIRE(is_float_type(dy_dtype) && is_float_type(z_dtype), MX_ERR_ENUM);
+  MX_REQUIRE(routed_shape(tokens, top_k, cols, rows) && lddy >= cols && ldz >= cols && lddz >= cols,
+             MX_ERR_SHAPE);
+  if (tokens == 0) return MX_OK;
+  MX_REQUIRE(pos && dweights, MX_ERR_NULL);
+  if (rows && cols) MX_REQUIRE(dy && z && dz, MX_ERR_NULL);
+  MX_REQUIRE(aligned16(dy) && aligned16(z) && aligned16(pos) && aligned16(weights) &&
+                 aligned16(dz) && aligned16(dweights), MX_ERR_ALIGN);
+  const bool wide = cols % 8 == 0 && rows16(lddy, size_of(dy_dtype)) &&
+                    rows16(ldz, size_of(z_dtype)) && rows16(lddz, size_of(dy_dtype));
+  const int runs = (int)(wide ? cols / 8 : cols);
+  const dim3 grid((unsigned)hmin(tokens, (int64_t)device_cu_count() * 64));
+  const hipStream_t st = as_stream(stream);
+#define MX_COMBINE_BWD(TY, TZ)                                                                    \
+  do {                                                                                            \
+    const TY* g = static_cast<const TY*>(dy);                                                     \
+    const TZ* zt = static_cast<const TZ*>(z);                                                     \
+    TY* d = static_cast<TY*>(dz);                                                                 \
+    if (wide) k_combine_bwd<TY, TZ, 8><<<grid, 256, 0, st>>>(g, lddy, zt, ldz, rows, pos, weights, \
+                                                             tokens, (int)top_k, runs, d, lddz,   \
+                                                             dweights);                           \
+    else k_combine_bwd<TY, TZ, 1><<<grid, 256, 0, st>>>(g, lddy, zt, ldz, rows, pos, weights,     \
+                                                        tokens, (int)top_k, runs, d, lddz,        \
+                                                        dweights);                                \
+  } while (0)
+  if (dy_dtype == MX_F32) {
+    if (z_dtype == MX_F32) MX_COMBINE_BWD(float, float);
+    else MX_COMBINE_BWD(float, uint16_t);
+  } else {
+    if (z_dtype == MX_F32) MX_COMBINE_BWD(uint16_t, float);
+    else MX_COMBINE_BWD(uint16_t, uint16_t);
+  }
+#undef MX_COMBINE_BWD
+  return launch_status();
+}

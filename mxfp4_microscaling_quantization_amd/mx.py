@@ -19,6 +19,7 @@ MX_OK, MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_ENUM, MX_ERR_WORKSPACE, M
 MX_F32, MX_BF16 = 0, 1
 MX_ROW, MX_COL = 0, 1
 MX_RNE, MX_SR = 0, 1
+MX_I32, MX_I64 = 0, 1
 MX_MAX_GROUPS = 128
 
 LIB_PATH = Path(__file__).resolve().parent / "libmx355.so"
@@ -59,6 +60,16 @@ SIGNATURES = {
     "mx_linear_fwd_rht": ([_P, _P, _i32, _i64, _i64, _i64, _u32, _P, _P, _P, _P, _P, _P], _i32),
     "mx_linear_bwd_rht": ([_P, _i32, _i64, _i64, _i64, _P, _P, _P, _P, _u64, _u32, _P, _P, _P, _sz,
                            _P], _i32),
+    "mx_gemv": ([_P, _i32, _i64, _P, _P, _i64, _i64, _i64, _i64, _f32, _P, _i32, _i64, _P], _i32),
+    "mx_gemv_grouped": ([_P, _i32, _i64, _i64, _P, _i64, _P, _P, _i64, _P, _i64, _i64, _i64, _i64,
+                         _f32, _P, _i32, _i64, _P], _i32),
+    "mx_moe_plan_workspace_size": ([_i64, _i64, _i64], _sz),
+    "mx_moe_plan": ([_P, _i32, _i64, _i64, _i64, _P, _P, _P, _P, _sz, _P], _i32),
+    "mx_moe_dispatch": ([_P, _i32, _i64, _P, _P, _i64, _i64, _i64, _i64, _P, _i64, _P], _i32),
+    "mx_moe_dispatch_quantize": ([_P, _i32, _i64, _P, _i64, _i64, _i64, _i64, _P, _P, _i64, _P], _i32),
+    "mx_moe_combine": ([_P, _i32, _i64, _i64, _P, _P, _i64, _i64, _i64, _P, _i32, _i64, _P], _i32),
+    "mx_moe_combine_bwd": ([_P, _i32, _i64, _P, _i32, _i64, _i64, _P, _P, _i64, _i64, _i64, _P, _i64,
+                            _P, _P], _i32),
     "mx_deosc_init": ([_P, _i64, _i64, _P, _P, _P, _P], _i32),
     "mx_deosc_step": ([_P, _i64, _i64, _P, _P, _P, _i32, _f32, _P, _P], _i32),
     "mx_deosc_step_quantize": ([_P, _i64, _i64, _P, _P, _P, _i32, _f32, _P, _P, _P, _P], _i32),
@@ -321,6 +332,57 @@ def mx_linear_bwd_rht(dy, dtype, M, N, K, xq_codes, xq_scales, wq_codes, wq_scal
         _stream(stream)))
 
 
+def mx_gemv(x, x_dtype, ldx, w_codes, w_scales, w_scale_ld, M, N, K, alpha, y, y_dtype, ldy,
+            stream=None):
+    _check("mx_gemv", lib().mx_gemv(_ptr(x), x_dtype, ldx, _ptr(w_codes), _ptr(w_scales), w_scale_ld,
+                                    M, N, K, alpha, _ptr(y), y_dtype, ldy, _stream(stream)))
+
+
+def mx_gemv_grouped(x, x_dtype, ldx, x_rows, src, top_k, w_codes, w_scales, w_scale_ld, offs, groups,
+                    rows, N, K, alpha, y, y_dtype, ldy, stream=None):
+    _check("mx_gemv_grouped", lib().mx_gemv_grouped(
+        _ptr(x), x_dtype, ldx, x_rows, _ptr(src), top_k, _ptr(w_codes), _ptr(w_scales), w_scale_ld,
+        _ptr(offs), groups, rows, N, K, alpha, _ptr(y), y_dtype, ldy, _stream(stream)))
+
+
+def mx_moe_plan_workspace_size(tokens, top_k, experts) -> int:
+    return int(lib().mx_moe_plan_workspace_size(tokens, top_k, experts))
+
+
+def mx_moe_plan(ids, id_type, tokens, top_k, experts, offs, src, pos, workspace, workspace_bytes,
+                stream=None):
+    _check("mx_moe_plan", lib().mx_moe_plan(_ptr(ids), id_type, tokens, top_k, experts, _ptr(offs),
+                                            _ptr(src), _ptr(pos), _ptr(workspace), workspace_bytes,
+                                            _stream(stream)))
+
+
+def mx_moe_dispatch(x, dtype, ldx, pos, weights, tokens, top_k, rows, cols, out, ldo, stream=None):
+    _check("mx_moe_dispatch", lib().mx_moe_dispatch(
+        _ptr(x), dtype, ldx, _ptr(pos), _ptr(weights), tokens, top_k, rows, cols, _ptr(out), ldo,
+        _stream(stream)))
+
+
+def mx_moe_dispatch_quantize(x, dtype, ldx, pos, tokens, top_k, rows, cols, codes, scales, scale_ld,
+                             stream=None):
+    _check("mx_moe_dispatch_quantize", lib().mx_moe_dispatch_quantize(
+        _ptr(x), dtype, ldx, _ptr(pos), tokens, top_k, rows, cols, _ptr(codes), _ptr(scales),
+        scale_ld, _stream(stream)))
+
+
+def mx_moe_combine(z, z_dtype, ldz, rows, pos, weights, tokens, top_k, cols, y, y_dtype, ldy,
+                   stream=None):
+    _check("mx_moe_combine", lib().mx_moe_combine(
+        _ptr(z), z_dtype, ldz, rows, _ptr(pos), _ptr(weights), tokens, top_k, cols, _ptr(y), y_dtype,
+        ldy, _stream(stream)))
+
+
+def mx_moe_combine_bwd(dy, dy_dtype, lddy, z, z_dtype, ldz, rows, pos, weights, tokens, top_k, cols,
+                       dz, lddz, dweights, stream=None):
+    _check("mx_moe_combine_bwd", lib().mx_moe_combine_bwd(
+        _ptr(dy), dy_dtype, lddy, _ptr(z), z_dtype, ldz, rows, _ptr(pos), _ptr(weights), tokens,
+        top_k, cols, _ptr(dz), lddz, _ptr(dweights), _stream(stream)))
+
+
 def mx_deosc_init(w, rows, cols, w_prev, d_w, d_q, stream=None):
     _check("mx_deosc_init", lib().mx_deosc_init(_ptr(w), rows, cols, _ptr(w_prev), _ptr(d_w),
                                                 _ptr(d_q), _stream(stream)))
@@ -443,3 +505,189 @@ def linear_bwd(dy: torch.Tensor, xq, wq, M, N, K, seed, workspace=None, stream=N
     mx_linear_bwd(dy, dtype_code(dy), M, N, K, xq[0], xq[1], wq[0], wq[1], seed, dx, dw,
                   workspace, workspace.numel(), stream)
     return dx, dw
+
+
+# The conveniences below check what the C calls cannot see: types, shapes, that
+# every tensor is on the current device and that rows are contiguous (row strides
+# are passed on).  Outputs are allocated on the stream the call runs on.
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_current_device(*tensors) -> None:
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.device.index == dev):
+            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+
+
+def _row_ld(t: torch.Tensor, what: str) -> int:
+    """Row stride in elements of a 2-D tensor with contiguous rows."""
+    rows, cols = t.shape
+    _need(cols <= 1 or t.stride(1) == 1, f"{what}: rows must be contiguous")
+    if rows <= 1:
+        return cols
+    _need(t.stride(0) >= cols, f"{what}: rows must not overlap")
+    return t.stride(0)
+
+
+def _empty(shape, dtype, like, stream, *inputs):
+    """An output of the current device, allocated on the stream the call runs on; the
+    inputs are kept from reuse until that stream is done with them."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _output(out, shape, dtype, like, stream, *inputs):
+    if out is None:
+        return _empty(shape, dtype, like, stream, *inputs)
+    _need(tuple(out.shape) == tuple(shape) and (dtype is None or out.dtype == dtype),
+          f"out must be {tuple(shape)} {dtype}")
+    return out
+
+
+def _packed_weight(w, groups):
+    """(codes, scales, N, K, scale row pitch) of a packed weight [N, K], or of `groups` of them."""
+    codes, scales = w
+    lead = () if groups is None else (groups,)
+    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8, "packed weights are uint8")
+    _need(codes.is_contiguous() and scales.is_contiguous(), "packed weights must be contiguous")
+    _need(codes.dim() == len(lead) + 2 and codes.shape[:-1] == scales.shape[:-1]
+          and tuple(codes.shape[:-2]) == lead, "codes and scales must have the same rows")
+    return codes, scales, codes.shape[-2], 2 * codes.shape[-1], scales.shape[-1]
+
+
+def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, stream=None):
+    """alpha x deq(W)^T of a few rows x [M, K] (float32 or bf16) and a packed weight
+    w = (codes [N, K/2], scales [N, >= K/32]); returns [M, N]."""
+    M, K = x.shape
+    codes, scales, N, wk, pitch = _packed_weight(w, None)
+    _need(wk == K, f"x has {K} columns, the weight {wk}")
+    _on_current_device(x, codes, scales, out)
+    ldx = _row_ld(x, "x")
+    if out is not None:
+        out_dtype = out.dtype
+    y = _output(out, (M, N), out_dtype, x, stream, x, codes, scales)
+    mx_gemv(x, dtype_code(x), ldx, codes, scales, pitch, M, N, K, alpha, y, dtype_code(y),
+            _row_ld(y, "out"), stream)
+    return y
+
+
+def gemv_grouped(x: torch.Tensor, w, offs, src=None, top_k=1, alpha=1.0, out=None,
+                 out_dtype=torch.float32, stream=None):
+    """Each routed row's alpha x deq(W_e)^T, offsets on the device (moe_plan's offs and
+    src): w = (codes [E, N, K/2], scales [E, N, >= K/32]); returns [rows, N], where rows
+    is src's length (without src: x's rows, each its own).  Rows from offs[E] on are
+    left as `out` had them."""
+    xr, K = x.shape
+    groups = offs.numel() - 1
+    codes, scales, N, wk, pitch = _packed_weight(w, groups)
+    _need(wk == K, f"x has {K} columns, the weights {wk}")
+    _need(offs.dtype == torch.int64 and offs.is_contiguous(), "offs must be int64")
+    _need(src is None or (src.dtype == torch.int32 and src.is_contiguous()), "src must be int32")
+    _on_current_device(x, codes, scales, offs, src, out)
+    ldx = _row_ld(x, "x")
+    rows = xr if src is None else src.numel()
+    if out is not None:
+        out_dtype = out.dtype
+    y = _output(out, (rows, N), out_dtype, x, stream, x, codes, scales, offs, src)
+    mx_gemv_grouped(x, dtype_code(x), ldx, xr, src, top_k, codes, scales, pitch, offs, groups, rows,
+                    N, K, alpha, y, dtype_code(y), _row_ld(y, "out"), stream)
+    return y
+
+
+def moe_plan(ids: torch.Tensor, experts: int, workspace=None, stream=None):
+    """(offs [experts + 1] int64, src [tokens * top_k] int32, pos [tokens, top_k] int32) of
+    the expert ids [tokens, top_k] (int32 or int64; out of range: the slot is left out)."""
+    tokens, top_k = ids.shape
+    _need(ids.dtype in (torch.int32, torch.int64), "ids must be int32 or int64")
+    _need(ids.is_contiguous(), "ids must be contiguous")
+    _on_current_device(ids, workspace)
+    need = mx_moe_plan_workspace_size(tokens, top_k, experts)
+    if workspace is None and need:
+        workspace = _empty((need,), torch.uint8, ids, stream)
+    offs = _empty((experts + 1,), torch.int64, ids, stream, ids, workspace)
+    src = _empty((tokens * top_k,), torch.int32, ids, stream)
+    pos = _empty((tokens, top_k), torch.int32, ids, stream)
+    mx_moe_plan(ids, MX_I32 if ids.dtype == torch.int32 else MX_I64, tokens, top_k, experts, offs, src,
+                pos, workspace, 0 if workspace is None else workspace.nbytes, stream)
+    return offs, src, pos
+
+
+def _routing(pos, weights, tokens):
+    _need(pos.dim() == 2 and pos.dtype == torch.int32 and pos.is_contiguous(), "pos must be int32 [tokens, top_k]")
+    _need(pos.shape[0] == tokens, f"pos is for {pos.shape[0]} tokens, not {tokens}")
+    _need(weights is None or (weights.dtype == torch.float32 and weights.shape == pos.shape
+                              and weights.is_contiguous()), "weights must be float32 like pos")
+    return pos.shape[1]
+
+
+def moe_dispatch(x: torch.Tensor, pos, weights=None, rows=None, out=None, stream=None):
+    """Rows of x [tokens, cols] copied (times weights) to out[pos]: [rows, cols], rows = all
+    slots if neither it nor out is given.  Rows no slot maps to are left as `out` had them."""
+    tokens, cols = x.shape
+    top_k = _routing(pos, weights, tokens)
+    _on_current_device(x, pos, weights, out)
+    rows = out.shape[0] if out is not None else pos.numel() if rows is None else rows
+    o = _output(out, (rows, cols), x.dtype, x, stream, x, pos, weights)
+    mx_moe_dispatch(x, dtype_code(x), _row_ld(x, "x"), pos, weights, tokens, top_k, rows, cols, o,
+                    _row_ld(o, "out"), stream)
+    return o
+
+
+def moe_dispatch_quantize(x: torch.Tensor, pos, rows=None, out=None, stream=None):
+    """Packed (codes [rows, cols/2], scales [rows, >= cols/32]) of moe_dispatch(x, pos); the
+    scale row pitch is that of out's scales, cols/32 if out is not given."""
+    tokens, cols = x.shape
+    top_k = _routing(pos, None, tokens)
+    if out is None:
+        rows = pos.numel() if rows is None else rows
+        out = (_empty((rows, cols // 2), torch.uint8, x, stream, x, pos),
+               _empty((rows, cols // 32), torch.uint8, x, stream))
+    codes, scales = out
+    rows = codes.shape[0]
+    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.is_contiguous()
+          and scales.is_contiguous() and codes.dim() == 2 and codes.shape[1] == cols // 2
+          and scales.dim() == 2 and scales.shape[0] == rows, "out must be packed uint8 codes and scales")
+    _on_current_device(x, pos, codes, scales)
+    mx_moe_dispatch_quantize(x, dtype_code(x), _row_ld(x, "x"), pos, tokens, top_k, rows, cols, codes,
+                             scales, scales.shape[1], stream)
+    return codes, scales
+
+
+def moe_combine(z: torch.Tensor, pos, weights=None, out=None, out_dtype=torch.float32, stream=None):
+    """y[t] = sum_j weights[t, j] z[pos[t, j]] [tokens, cols]; without weights the gradient of
+    moe_dispatch."""
+    rows, cols = z.shape
+    tokens = pos.shape[0]
+    top_k = _routing(pos, weights, tokens)
+    _on_current_device(z, pos, weights, out)
+    if out is not None:
+        out_dtype = out.dtype
+    y = _output(out, (tokens, cols), out_dtype, z, stream, z, pos, weights)
+    mx_moe_combine(z, dtype_code(z), _row_ld(z, "z"), rows, pos, weights, tokens, top_k, cols, y,
+                   dtype_code(y), _row_ld(y, "out"), stream)
+    return y
+
+
+def moe_combine_bwd(dy: torch.Tensor, z: torch.Tensor, pos, weights=None, out=None, stream=None):
+    """(dz [rows, cols] of dy's type, dweights [tokens, top_k] float32) of moe_combine(z, pos,
+    weights); dz's rows that no slot maps to are left as `out` had them."""
+    tokens, cols = dy.shape
+    rows = z.shape[0]
+    top_k = _routing(pos, weights, tokens)
+    _need(z.dim() == 2 and z.shape[1] == cols, "z and dy must have the same columns")
+    _on_current_device(dy, z, pos, weights, out)
+    dz = _output(out, (rows, cols), dy.dtype, dy, stream, dy, z, pos, weights)
+    dw = _empty((tokens, top_k), torch.float32, dy, stream)
+    mx_moe_combine_bwd(dy, dtype_code(dy), _row_ld(dy, "dy"), z, dtype_code(z), _row_ld(z, "z"), rows,
+                       pos, weights, tokens, top_k, cols, dz, _row_ld(dz, "out"), dw, stream)
+    return dz, dw
