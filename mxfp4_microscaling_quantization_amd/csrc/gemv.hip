@@ -6,19 +6,17 @@
 //
 // What bounds it: the weights are read once, 17/32 byte each, and every value
 // meets only M rows of x, so for few rows HBM (or the latency of one pass over
-// it) is the bound.  The products run on V_MFMA_F32_16X16X32_BF16 with 16 weight
-// rows as one operand and up to 16 rows of x as the other: E2M1 values times a
-// power of two are exact in bf16 (one conversion instruction per two codes), the
-// products are exact in float32 and the sums are float32.  A bf16 x goes in as it
-// is; a float32 x is split exactly into three bf16 terms (8 significant bits
-// each, by truncation), one MFMA each.
+// it) is the bound.  The products run on V_MFMA_F32_16X16X32_BF16: E2M1 values
+// times a power of two are exact in bf16 (one conversion instruction per two
+// codes), the products are exact in float32 and the sums are float32.  A bf16 x
+// goes in as it is; a float32 x is split exactly into three bf16 terms (8
+// significant bits each, by truncation), one MFMA each.
 //
-// Lane layout of the MFMA operands: lane l holds row l & 15 and the 8 consecutive
-// contraction values 8 (l >> 4) .. + 7.  The contraction may run in any order as
-// long as both operands agree, so in a step of 128 values lane group g = l >> 4
-// takes the step's block g (32 consecutive values): one 16-byte load of codes and
-// one scale byte per lane feed four MFMAs, the j-th with values 8j .. 8j+7 of the
-// block.
+// Lane layout: lane l holds MFMA row l & 15 (a weight row) or column l & 15 (a row of
+// x) and the 8 contraction values of group l >> 4.  The contraction may run in any
+// order as long as both operands agree, so in a step of 128 values group g takes the
+// step's block g (32 values): one 16-byte load of codes and one scale byte a lane feed
+// four MFMAs, the j-th with values 8j .. 8j+7 of the block.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -33,17 +31,18 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 
 struct GemvArgs {
   const void* x;
-  int64_t ldx, x_rows;
+  int64_t ldx;
   const uint8_t* codes;
   const uint8_t* scales;
-  int64_t scale_ld;
+  int64_t scale_ld, scale_end;  // bytes between scale rows; end of the last one
   const int64_t* offs;  // grouped: device offsets [groups + 1]
   const int32_t* src;   // grouped: slot of each row, or NULL
-  int64_t M, N;         // M: rows of y
-  int K, top_k, groups, y_bf16;
-  float alpha;
+  int64_t N;
   void* y;
-  int64_t ldy, ntiles, mtiles;
+  float* partial;  // [slices][M][N] where the contraction is sliced
+  int64_t ldy, ntiles;
+  int M, K, top_k, groups, x_rows, y_bf16, window, rounds, slices;  // M: rows of y
+  float alpha;
 };
 
 // 8 codes (element i in nibble i) under a block scale, as bf16.
@@ -58,50 +57,41 @@ __device__ __forceinline__ v8bf decode8_bf16(uint32_t w, float scale) {
   return v;
 }
 
-// The contraction values a lane feeds one MFMA: 8 values of x as TERMS bf16 operands.
+// x as kTerms bf16 planes: take() gives the next plane of a lane's 8 consecutive values
+// (words of bf16 pairs) and leaves the rest of the values in w.
 template <typename T>
 struct XTerms;
 template <>
 struct XTerms<uint16_t> {
   static constexpr int kTerms = 1;
-  static __device__ __forceinline__ void make(const uint32_t w[4], v8bf t[1]) {
-    t[0] = __builtin_bit_cast(v8bf, make_uint4(w[0], w[1], w[2], w[3]));
+  static __device__ __forceinline__ uint4 take(uint32_t w[4]) {
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <>
 struct XTerms<float> {
   static constexpr int kTerms = 3;
-  // Upper halves of two floats as a bf16 pair.
-  static __device__ __forceinline__ uint32_t tops(float a, float b) {
-    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-  }
-  static __device__ __forceinline__ float top(float a) {
-    return __uint_as_float(__float_as_uint(a) & 0xFFFF0000u);
-  }
-  static __device__ __forceinline__ void make(const uint32_t w[8], v8bf t[3]) {
-    uint32_t o[3][4];
+  // The upper half of a float holds its 8 leading significant bits; the rest is exact.  Inf
+  // has no rest, and a NaN stays one even if only its low bits say so.
+  static __device__ __forceinline__ uint4 take(uint32_t w[8]) {
+    uint32_t t[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      float a[2], b[2], c[2];
+      uint32_t u[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t u = w[2 * p + i];
-        const bool nan = (u & 0x7FFFFFFFu) > 0x7F800000u, inf = (u & 0x7FFFFFFFu) == 0x7F800000u;
-        a[i] = __uint_as_float(nan ? 0x7FC00000u : u);  // a NaN with only low bits stays a NaN
-        b[i] = inf ? 0.0f : a[i] - top(a[i]);           // exact: the low 16 significant bits
-        c[i] = b[i] - top(b[i]);                        // exact: the low 8
+        const uint32_t v = w[2 * p + i], m = v & 0x7FFFFFFFu;
+        u[i] = m > 0x7F800000u ? 0x7FC00000u : v;
+        const float rest = __uint_as_float(v) - __uint_as_float(v & 0xFFFF0000u);
+        w[2 * p + i] = m >= 0x7F800000u ? 0u : __float_as_uint(rest);
       }
-      o[0][p] = tops(a[0], a[1]);
-      o[1][p] = tops(b[0], b[1]);
-      o[2][p] = tops(c[0], c[1]);
+      t[p] = __builtin_amdgcn_perm(u[1], u[0], 0x07060302u);  // the two upper halves
     }
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      t[k] = __builtin_bit_cast(v8bf, make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]));
+    return make_uint4(t[0], t[1], t[2], t[3]);
   }
 };
 
-// 8 values of x, raw; `wide`: on 16 bytes.
+// 8 values of x, raw; WIDE: on 16 bytes.
 template <typename T, bool WIDE>
 __device__ __forceinline__ void load_x8(const T* p, uint32_t* w) {
   constexpr int W = 2 * sizeof(T);
@@ -120,177 +110,421 @@ __device__ __forceinline__ void load_x8(const T* p, uint32_t* w) {
   }
 }
 
-// A workgroup of W waves computes 16 NT columns of y (weight rows) for MT tiles of
-// 16 rows: the waves split the contraction (wave w takes steps w, w + W, ...), their
-// sums meet in LDS and are added in wave order.
-template <typename T, int MT, int NT, int W, bool GROUPED, bool WIDE>
-__global__ __launch_bounds__(64 * W) void k_gemv(const GemvArgs a) {
+// Orders a wave's LDS accesses around an exchange between its lanes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// A workgroup barrier for LDS alone: global loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The row tiles (of R rows) of all groups in one sequence.  Every lane holds two groups:
+// their rows [lo, hi) within [0, rows) and the number of row tiles up to their end.
+template <int R>
+struct GroupTiles {
+  int lo[2], hi[2], end[2];
+
+  __device__ __forceinline__ void load(const int64_t* __restrict__ offs, int groups, int rows) {
+    const int lane = threadIdx.x & 63;
+    int64_t o[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = min(64 * h + lane, groups - 1);
+      o[h][0] = offs[e];
+      o[h][1] = offs[e + 1];
+    }
+    int before = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lo[h] = (int)max<int64_t>(min<int64_t>(o[h][0], rows), 0);
+      hi[h] = (int)max<int64_t>(min<int64_t>(o[h][1], rows), 0);
+      int n = 64 * h + lane < groups && hi[h] > lo[h] ? (hi[h] - lo[h] + R - 1) / R : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(n, d);
+        n += lane >= d ? up : 0;
+      }
+      end[h] = n + before;
+      before = __builtin_amdgcn_readlane(end[h], 63);
+    }
+  }
+  __device__ __forceinline__ int total() const { return __builtin_amdgcn_readlane(end[1], 63); }
+  // Row tile v: its group, first row and rows.
+  __device__ __forceinline__ int find(int v, int& m0, int& mrows) const {
+    const uint64_t low = __ballot(end[0] > v);
+    const int h = low ? 0 : 1;
+    const int l = __ffsll((unsigned long long)(low ? low : __ballot(end[1] > v))) - 1;
+    const int first = __builtin_amdgcn_readlane(h ? lo[1] : lo[0], l);
+    const int last = __builtin_amdgcn_readlane(h ? hi[1] : hi[0], l);
+    const int tiles = __builtin_amdgcn_readlane(h ? end[1] : end[0], l);
+    m0 = first + (v - (tiles - (last - first + R - 1) / R)) * R;
+    mrows = min(R, last - m0);
+    return 64 * h + l;
+  }
+};
+
+// A tile is kGemvTile columns of y (weight rows) for up to R rows of x; a workgroup takes a
+// run of consecutive tiles, column tiles first, so that it keeps its rows of x while the
+// group and row tile stay.  Its waves split the contraction into windows of up to 4 S
+// blocks (wave w takes windows w, w + W, ...): a wave holds a window's x operands in
+// registers and walks the tile's weight rows, 16 at a time, two loads of them ahead of
+// their use -- also across tiles, so that the weight stream does not stop at a tile's
+// end.  Its sums go to LDS, where the waves' are added in wave order.
+//
+// The 16 columns of an MFMA are 16 bf16 rows of x, or the three terms of four float32
+// rows (term p of row q in column 4 p + q): the terms' sums are added at the end.
+constexpr int kMaxWaves = 8, kGemvTile = 64;
+
+template <typename T, int MT, int S, bool GROUPED, bool WIDE>
+__global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   constexpr int X = XTerms<T>::kTerms;
-  constexpr int XW = 2 * sizeof(T);  // words of 8 values of x
-  __shared__ v4f s_part[W][MT * NT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int XW = 2 * sizeof(T);        // words of 8 values of x
+  constexpr int RT = X == 1 ? 16 : 4;      // rows of x in an MFMA's columns
+  constexpr int R = RT * MT;
+  constexpr int Q = MT == 1 && S <= 2 ? 4 : 2;  // subtiles in flight
+  extern __shared__ uint4 s_stage[];       // [waves][4 rows][64 runs], then
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int nblk = a.K / 32, steps = (nblk + 3) / 4;
-  const int64_t kbytes = a.K / 2;
+  const int nblk = a.K / 32, rounds = a.rounds;
+  constexpr int tile_n = kGemvTile, subs = tile_n / 16;
+  constexpr int ldp = tile_n + 4;          // LDS column pitch: columns on different banks
+  const uint32_t kbytes = a.K / 2;
   const T* const x = static_cast<const T*>(a.x);
+  uint4* const stage = s_stage + 256 * wave;
+  uint4* const s_scale = s_stage + 256 * waves;                            // [waves][64 rows] of 16 bytes
+  float* const s_part = reinterpret_cast<float*>(s_scale + 64 * waves);    // [waves][16 MT][ldp]
+  float* const part = s_part + wave * (16 * MT) * ldp;
 
-  for (int64_t tile = blockIdx.x; tile < a.ntiles * a.mtiles; tile += gridDim.x) {
-    const int64_t n0 = (tile % a.ntiles) * (16 * NT);
-    int64_t row0 = tile / a.ntiles, row1;
-    const uint8_t* codes = a.codes;
-    const uint8_t* scales = a.scales;
+  // this workgroup's run of tiles [t, t_end)
+  GroupTiles<R> groups;
+  int64_t row_tiles = (a.M + R - 1) / R;
+  if constexpr (GROUPED) {
+    groups.load(a.offs, a.groups, a.M);
+    row_tiles = groups.total();
+  }
+  const int64_t tiles = row_tiles * a.slices * a.ntiles;
+  const int64_t t0 = tiles * blockIdx.x / gridDim.x, t_end = tiles * (blockIdx.x + 1) / gridDim.x;
+  if (t0 >= t_end) return;
+
+  struct Place {
+    int v, ks, nt;  // row tile, slice of the contraction, column tile
+    int grp, m0, mrows, ncols;
+  };
+  const auto find = [&](Place& p) {
+    p.ncols = (int)min<int64_t>(tile_n, a.N - (int64_t)p.nt * tile_n);
+    p.grp = 0;
     if constexpr (GROUPED) {
-      // row0 counts the groups that hold rows
-      int grp = -1;
-      int64_t left = row0;
-      for (int e = 0; e < a.groups; ++e) {
-        if (a.offs[e + 1] > a.offs[e] && left-- == 0) {
-          grp = e;
-          break;
-        }
-      }
-      if (grp < 0) break;
-      row0 = max<int64_t>(a.offs[grp], 0);
-      row1 = min<int64_t>(a.offs[grp + 1], a.M);
-      codes += grp * a.N * kbytes;
-      scales += grp * a.N * a.scale_ld;
+      p.grp = groups.find(p.v, p.m0, p.mrows);
     } else {
-      row0 *= 16 * MT;
-      row1 = min<int64_t>(row0 + 16 * MT, a.M);
+      p.m0 = p.v * R;
+      p.mrows = min(R, a.M - p.m0);
     }
-    const uint8_t* wc[NT];
-    const uint8_t* ws[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int64_t n = min<int64_t>(n0 + 16 * i + r16, a.N - 1);
-      wc[i] = codes + n * kbytes;
-      ws[i] = scales + n * a.scale_ld;
+  };
+  const auto step_tile = [&](Place& p) {
+    if (++p.nt == a.ntiles) {
+      p.nt = 0;
+      if (++p.ks == a.slices) p.ks = 0, ++p.v;
     }
-    for (int64_t m0 = row0; m0 < row1; m0 += 16 * MT) {
-      const T* xr[MT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        int64_t r = min<int64_t>(m0 + 16 * i + r16, row1 - 1);
-        if constexpr (GROUPED) {
-          if (a.src) r = a.src[r] / a.top_k;
-          if (r < 0 || r >= a.x_rows) r = 0;  // not stored below
-        }
-        xr[i] = x + r * a.ldx;
-      }
-      v4f acc[MT][NT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    find(p);
+  };
+  Place cur;
+  const int64_t strip = t0 / a.ntiles;
+  cur.nt = (int)(t0 - strip * a.ntiles);
+  cur.v = (int)(strip / a.slices);
+  cur.ks = (int)(strip - (int64_t)cur.v * a.slices);
+  find(cur);
 
-      for (int s = wave; s < steps; s += W) {
-        const int blk = 4 * s + g;
-        const bool in = blk < nblk;
-        const int b = in ? blk : 0;  // lanes past the last block read block 0 and put in zeros
-        uint4 c[NT];
-        uint32_t sc[NT];
+  // The weight stream.  Offsets within a tile fit 32 bits (K < 2^26); rows past the last
+  // read the last, lanes past the last block read block 0.  Past the workgroup's last
+  // tile it repeats that tile's last rows.
+  Place ahead = cur;
+  int64_t t_ahead = t0;
+  int round_ahead = 0, sub_ahead = 0;
+  const uint8_t* codes;
+  uint4 scale16;
+  uint32_t c_at, c_end, b_at[S];
+  const auto stream = [&]() {
+    const int64_t row = (GROUPED ? ahead.grp * a.N : 0) + (int64_t)ahead.nt * tile_n;
+    codes = a.codes + row * kbytes;
+    const int b0 = ((ahead.ks * rounds + round_ahead) * waves + wave) * a.window, b1 = min(b0 + a.window, nblk);
+    c_at = min(r16, ahead.ncols - 1) * kbytes;
+    c_end = (ahead.ncols - 1) * kbytes;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          c[i] = *reinterpret_cast<const uint4*>(wc[i] + (int64_t)b * 16);
-          sc[i] = ws[i][b];
-        }
-        uint32_t xw[MT][4][XW];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) load_x8<T, WIDE>(xr[i] + (int64_t)b * 32 + 8 * j, xw[i][j]);
-        if (4 * s + 4 > nblk) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            if (!in) {
-              c[i] = make_uint4(0, 0, 0, 0);
-              sc[i] = 127;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int k = 0; k < XW; ++k) xw[i][j][k] = in ? xw[i][j][k] : 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v8bf xt[MT][X];
-#pragma unroll
-          for (int i = 0; i < MT; ++i) XTerms<T>::make(xw[i][j], xt[i]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint32_t w = j == 0 ? c[n].x : j == 1 ? c[n].y : j == 2 ? c[n].z : c[n].w;
-            const v8bf wv = decode8_bf16(w, scale_of(sc[n]));
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int k = X - 1; k >= 0; --k)
-                acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xt[i][k], acc[i][n], 0, 0, 0);
-          }
-        }
+    for (int s = 0; s < S; ++s) b_at[s] = (b0 + 4 * s + g < b1 ? b0 + 4 * s + g : 0) * 16;
+    // The window's scale bytes of the tile's rows, a row a lane (at most 64): 16 bytes at
+    // any alignment, byte by byte where the array ends within them.
+    const int64_t at = (row + min(lane, ahead.ncols - 1)) * a.scale_ld + b0;
+    if (at + 16 <= a.scale_end) {
+      __builtin_memcpy(&scale16, a.scales + at, 16);
+    } else {
+      uint64_t w[2] = {0, 0};
+#pragma unroll 1
+      for (int i = 0; at + i < a.scale_end; ++i) {
+        const uint64_t byte = (uint64_t)a.scales[at + i] << (8 * (i & 7));
+        w[0] |= i < 8 ? byte : 0;
+        w[1] |= i < 8 ? 0 : byte;
       }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) s_part[wave][i * NT + j][lane] = acc[i][j];
-      __syncthreads();
-      // lane (g, m) of tile (i, j) holds y[m0 + 16 i + m][n0 + 16 j + 4 g .. + 3]
-      for (int o = threadIdx.x; o < MT * NT * 64; o += 64 * W) {
-        const int og = o & 3, oj = (o >> 2) % NT, om = (o >> 2) / NT % 16, oi = o / (64 * NT);
-        v4f sum = s_part[0][oi * NT + oj][og * 16 + om];
-#pragma unroll
-        for (int w = 1; w < W; ++w) sum += s_part[w][oi * NT + oj][og * 16 + om];
-        const int64_t m = m0 + 16 * oi + om, n = n0 + 16 * oj + 4 * og;
-        bool real = m < row1;
-        if constexpr (GROUPED) {
-          if (real) {
-            const int64_t r = a.src ? a.src[m] / a.top_k : m;
-            real = r >= 0 && r < a.x_rows && !(a.src && a.src[m] < 0);
-          }
-        }
-        if (real) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (n + k < a.N) {
-              const float v = a.alpha * sum[k];
-              if (a.y_bf16) static_cast<uint16_t*>(a.y)[m * a.ldy + n + k] = (uint16_t)f32_to_bf16_rne(v);
-              else static_cast<float*>(a.y)[m * a.ldy + n + k] = v;
-            }
-          }
-        }
-      }
-      __syncthreads();
+      scale16 = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
     }
+  };
+  uint4 c[Q][S];
+  const auto fetch = [&](int q) {
+    if (sub_ahead == subs && (round_ahead + 1 < rounds || t_ahead + 1 < t_end)) {
+      sub_ahead = 0;
+      if (++round_ahead == rounds) {
+        round_ahead = 0;
+        ++t_ahead;
+        step_tile(ahead);
+      }
+      stream();
+    }
+    ++sub_ahead;
+#pragma unroll
+    for (int s = 0; s < S; ++s) c[q][s] = *reinterpret_cast<const uint4*>(codes + (c_at + b_at[s]));
+    c_at = min(c_at + 16 * kbytes, c_end);
+  };
+
+  // The x operands.  Rows of x, 8 values a lane, go through the wave's LDS four at a time,
+  // 64 runs of 8 values a row, and are read back by the lanes of their columns: block p's
+  // run j.  Run 4 p + j lies at 4 p + (j ^ p / 4), which spreads the blocks over the banks.
+  constexpr int kFours = R / 4;
+  v8bf xt[MT][S][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xt[i][s][j] = v8bf{};
+  uint32_t xv[4][XW];     // four rows on their way
+  int row_of = 0;         // lane q: the row of x of the tile's row q
+  uint64_t real = ~0ull;  // the tile's rows whose row of x exists
+  const auto x_rows = [&]() {
+    row_of = cur.m0 + min(lane, cur.mrows - 1);
+    if constexpr (GROUPED) {
+      if (a.src) {
+        const int slot = a.src[row_of];
+        row_of = slot < 0 ? -1 : slot / a.top_k;
+      }
+      real = __ballot(row_of >= 0 && row_of < a.x_rows);
+      if (row_of < 0 || row_of >= a.x_rows) row_of = 0;  // not stored below
+    }
+  };
+  const auto x_load = [&](int four, int b0, int b1) {
+    const int k0 = 32 * b0 + 8 * lane;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int k = 0; k < XW; ++k) xv[q][k] = 0;
+      if (4 * four + q < cur.mrows && k0 < 32 * b1) {
+        const int64_t r = __builtin_amdgcn_readlane(row_of, 4 * four + q);
+        load_x8<T, WIDE>(x + (r * a.ldx + k0), xv[q]);
+      }
+    }
+  };
+  const auto x_put = [&](int four, int b0, int b1) {
+    const int row = min(r16 & 3, cur.mrows - 4 * four - 1);  // columns past the last row repeat it
+#pragma unroll
+    for (int k = 0; k < X; ++k) {
+      wave_sync();
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (4 * four + q < cur.mrows)
+          stage[64 * q + (lane ^ lane >> 4)] = XTerms<T>::take(xv[q]);
+      wave_sync();
+      if (k == X - 1 && four + 1 < kFours && 4 * four + 4 < cur.mrows) x_load(four + 1, b0, b1);
+      if (r16 >> 2 == (X == 1 ? four % 4 : k)) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            xt[4 * four / RT][s][j] = __builtin_bit_cast(v8bf, stage[64 * row + 16 * s + 4 * g + (j ^ s)]);
+      }
+    }
+  };
+
+  x_rows();
+  if (nblk) {
+    stream();
+    fetch(0);
+    const int b0 = (cur.ks * rounds * waves + wave) * a.window;
+    x_load(0, b0, min(b0 + a.window, nblk));  // in front of the stream's second half
+#pragma unroll
+    for (int q = 1; q < Q; ++q) fetch(q);
+  }
+  bool fresh = true;
+  for (int64_t t = t0;;) {
+    for (int round = 0; round < rounds; ++round) {
+      const int b0 = ((cur.ks * rounds + round) * waves + wave) * a.window, b1 = min(b0 + a.window, nblk);
+      if (fresh || rounds > 1) {
+        if (t > t0 || round > 0) {
+          x_rows();
+          x_load(0, b0, b1);
+        }
+#pragma unroll
+        for (int four = 0; four < kFours; ++four)
+          if (4 * four < cur.mrows) x_put(four, b0, b1);
+      }
+      if (nblk) {
+        // this round's scale bytes: the stream is at most a tile's subtiles ahead, so it has not
+        // come to the next round's yet
+        wave_sync();
+        s_scale[64 * wave + lane] = scale16;
+        wave_sync();
+        const uint8_t* const sb = reinterpret_cast<const uint8_t*>(s_scale + 64 * wave) + 16 * r16 + g;
+#pragma unroll 1
+        for (int sub = 0; sub < subs; sub += Q) {
+          float f[Q][S];  // block scales; x is 0 past the window's end, but NaN and Inf times 0 are not
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+              const uint32_t byte = sb[256 * (sub + q) + 4 * s];
+              f[q][s] = scale_of(b0 + 4 * s + g < b1 ? byte : 127u);
+            }
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            v4f* const p = reinterpret_cast<v4f*>(part + r16 * ldp + 16 * (sub + q) + 4 * g);
+            v4f acc[MT][2];  // two chains of sums
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              acc[i][0] = acc[i][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+              if (round) acc[i][1] = p[4 * i * ldp];
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint4 u = c[q][s];
+                const v8bf w = decode8_bf16(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, f[q][s]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                  acc[i][j & 1] =
+                      __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xt[i][s][j], acc[i][j & 1], 0, 0, 0);
+              }
+            }
+            fetch(q);
+            // lane 16 g + m holds weight rows 4 g .. 4 g + 3 of column m
+#pragma unroll
+            for (int i = 0; i < MT; ++i) p[4 * i * ldp] = acc[i][0] + acc[i][1];
+          }
+        }
+      }
+    }
+    lds_barrier();
+    for (int o = threadIdx.x; o < cur.mrows * tile_n; o += blockDim.x) {
+      const int m = o / tile_n, n = o % tile_n;
+      if (n >= cur.ncols || !(real >> m & 1)) continue;
+      float sum = 0.0f;
+      if (nblk) {
+        const float* const p = s_part + (16 * (m / RT) + m % RT) * ldp + n;
+        float v[X][kMaxWaves];  // all reads in flight, then the sum in order
+#pragma unroll
+        for (int k = 0; k < X; ++k)
+#pragma unroll
+          for (int w = 0; w < kMaxWaves; ++w) v[k][w] = p[(min(w, waves - 1) * (16 * MT) + 4 * k) * ldp];
+#pragma unroll
+        for (int k = X - 1; k >= 0; --k)
+#pragma unroll
+          for (int w = 0; w < kMaxWaves; ++w) sum += w < waves ? v[k][w] : 0.0f;
+      }
+      const int64_t col = (int64_t)cur.nt * tile_n + n;
+      if (a.slices > 1) {
+        a.partial[((int64_t)cur.ks * a.M + cur.m0 + m) * a.N + col] = sum;
+        continue;
+      }
+      const int64_t at = (int64_t)(cur.m0 + m) * a.ldy + col;
+      sum *= a.alpha;
+      if (a.y_bf16) static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_bf16_rne(sum);
+      else static_cast<float*>(a.y)[at] = sum;
+    }
+    if (++t == t_end) break;
+    lds_barrier();
+    const int grp = cur.grp, m0 = cur.m0, ks = cur.ks;
+    step_tile(cur);
+    fresh = cur.m0 != m0 || cur.grp != grp || cur.ks != ks;
   }
 }
 
-template <typename T, int MT, bool GROUPED, bool WIDE>
-static int gemv_launch(GemvArgs a, int64_t mtiles, hipStream_t st) {
-  constexpr int NT = 4, W = MT == 4 ? 4 : 8;
-  a.ntiles = cdiv(a.N, 16 * NT);
-  a.mtiles = mtiles;
-  const unsigned grid = (unsigned)hmin(a.ntiles * mtiles, 1 << 20);
-  k_gemv<T, MT, NT, W, GROUPED, WIDE><<<grid, 64 * W, 0, st>>>(a);
+// y = alpha times the slices' sums, added in slice order.
+__global__ __launch_bounds__(256) void k_gemv_sum(const float* __restrict__ partial, int slices,
+                                                  int64_t M, int64_t N, float alpha, void* y,
+                                                  int y_bf16, int64_t ldy) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * 256) {
+    float sum = 0.0f;
+    for (int k = 0; k < slices; ++k) sum += partial[k * M * N + i];
+    const int64_t m = i / N, at = m * ldy + (i - m * N);
+    sum *= alpha;
+    if (y_bf16) static_cast<uint16_t*>(y)[at] = (uint16_t)f32_to_bf16_rne(sum);
+    else static_cast<float*>(y)[at] = sum;
+  }
+}
+
+// How a product is cut: MFMA row tiles a workgroup holds, steps of a window, waves, blocks
+// of a wave's window, rounds of windows in one workgroup and slices over workgroups.
+struct GemvPlan {
+  int mt, steps, waves, window, rounds, slices;
+};
+
+static GemvPlan gemv_plan(int x_dtype, int64_t rows, int64_t N, int64_t K, bool grouped) {
+  const int rt = x_dtype == MX_BF16 ? 16 : 4, nblk = (int)(K / 32);
+  GemvPlan p;
+  p.mt = rows <= rt ? 1 : rows <= 2 * rt || rows > 3 * rt ? 2 : 3;
+  p.waves = (int)hmin(cdiv(nblk ? nblk : 1, 4), kMaxWaves);
+  const auto passes = [&](int steps) { return (int)cdiv(nblk ? nblk : 1, 4 * steps * p.waves); };
+  p.steps = 1;
+  while (p.steps < (p.mt == 1 ? 4 : 2) && passes(p.steps) > passes(p.mt == 1 ? 4 : 2)) ++p.steps;
+  const int n = passes(p.steps);
+  const bool slice = !grouped && n > 1;
+  p.rounds = slice ? 1 : n;
+  p.slices = slice ? n : 1;
+  p.window = (int)cdiv(cdiv(nblk ? nblk : 1, (int64_t)n * p.waves), 4) * 4;
+  return p;
+}
+
+template <typename T, int MT, int S, bool GROUPED, bool WIDE>
+static int gemv_launch(GemvArgs a, const GemvPlan& p, int64_t groups, hipStream_t st) {
+  constexpr int R = (sizeof(T) == 2 ? 16 : 4) * MT;
+  constexpr int kBytes = 5120 + 16 * MT * (kGemvTile + 4) * 4;  // LDS of a wave
+  static_assert(kMaxWaves * kBytes <= 160 * 1024, "the sums of all waves fit LDS");
+  a.ntiles = cdiv(a.N, kGemvTile);
+  a.window = p.window;
+  a.rounds = p.rounds;
+  a.slices = p.slices;
+  // a group adds less than one row tile to the rows'
+  const int64_t row_tiles = GROUPED ? cdiv(a.M, R) + groups : cdiv(a.M, R);
+  const unsigned grid = (unsigned)hmin(row_tiles * p.slices * a.ntiles, device_cu_count());
+  k_gemv<T, MT, S, GROUPED, WIDE><<<grid, 64 * p.waves, (size_t)p.waves * kBytes, st>>>(a);
+  if (p.slices > 1)
+    k_gemv_sum<<<(unsigned)hmin(cdiv(a.M * a.N, 256), 4096), 256, 0, st>>>(
+        a.partial, p.slices, a.M, a.N, a.alpha, a.y, a.y_bf16, a.ldy);
   return launch_status();
 }
 
 template <typename T, bool GROUPED, bool WIDE>
-static int gemv_rows(const GemvArgs& a, int64_t tile_rows, int64_t groups, hipStream_t st) {
-  if (tile_rows <= 16) return gemv_launch<T, 1, GROUPED, WIDE>(a, GROUPED ? groups : cdiv(a.M, 16), st);
-  if (tile_rows <= 32) return gemv_launch<T, 2, GROUPED, WIDE>(a, GROUPED ? groups : cdiv(a.M, 32), st);
-  return gemv_launch<T, 4, GROUPED, WIDE>(a, GROUPED ? groups : cdiv(a.M, 64), st);
+static int gemv_rows(const GemvArgs& a, const GemvPlan& p, int64_t groups, hipStream_t st) {
+  if (p.mt == 2) return gemv_launch<T, 2, 2, GROUPED, WIDE>(a, p, groups, st);
+  if (p.mt == 3) return gemv_launch<T, 3, 2, GROUPED, WIDE>(a, p, groups, st);
+  if (p.steps == 1) return gemv_launch<T, 1, 1, GROUPED, WIDE>(a, p, groups, st);
+  if (p.steps == 2) return gemv_launch<T, 1, 2, GROUPED, WIDE>(a, p, groups, st);
+  if (p.steps == 3) return gemv_launch<T, 1, 3, GROUPED, WIDE>(a, p, groups, st);
+  return gemv_launch<T, 1, 4, GROUPED, WIDE>(a, p, groups, st);
 }
 
 template <bool GROUPED>
-static int gemv_any(const GemvArgs& a, int x_dtype, int64_t tile_rows, int64_t groups, hipStream_t st) {
+static int gemv_any(const GemvArgs& a, const GemvPlan& p, int x_dtype, int64_t groups, hipStream_t st) {
   const bool wide = a.ldx * (x_dtype == MX_BF16 ? 2 : 4) % 16 == 0;
   if (x_dtype == MX_BF16)
-    return wide ? gemv_rows<uint16_t, GROUPED, true>(a, tile_rows, groups, st)
-                : gemv_rows<uint16_t, GROUPED, false>(a, tile_rows, groups, st);
-  return wide ? gemv_rows<float, GROUPED, true>(a, tile_rows, groups, st)
-              : gemv_rows<float, GROUPED, false>(a, tile_rows, groups, st);
+    return wide ? gemv_rows<uint16_t, GROUPED, true>(a, p, groups, st)
+                : gemv_rows<uint16_t, GROUPED, false>(a, p, groups, st);
+  return wide ? gemv_rows<float, GROUPED, true>(a, p, groups, st)
+              : gemv_rows<float, GROUPED, false>(a, p, groups, st);
 }
 
 static int gemv_check(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_codes,
@@ -299,8 +533,9 @@ static int gemv_check(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_
   constexpr int64_t kMax31 = (int64_t)1 << 31;
   MX_REQUIRE((x_dtype == MX_F32 || x_dtype == MX_BF16) && (y_dtype == MX_F32 || y_dtype == MX_BF16),
              MX_ERR_ENUM);
-  MX_REQUIRE(M >= 0 && M < kMax31 && N >= 0 && N < kMax31 && K >= 0 && K < kMax31 && K % 32 == 0 &&
-                 ldx >= K && ldy >= N && w_scale_ld >= K / 32, MX_ERR_SHAPE);
+  constexpr int64_t kMaxK = (int64_t)1 << 26;  // a tile's offsets stay within 32 bits
+  MX_REQUIRE(M >= 0 && M < kMax31 && N >= 0 && N < kMax31 && K >= 0 && K < kMaxK && K % 32 == 0 &&
+                 ldx >= K && ldy >= N && w_scale_ld >= K / 32 && w_scale_ld < kMaxK, MX_ERR_SHAPE);
   if (M == 0 || N == 0) return MX_OK;
   MX_REQUIRE(y, MX_ERR_NULL);
   if (K) MX_REQUIRE(x && w_codes && w_scales, MX_ERR_NULL);
@@ -312,14 +547,34 @@ static int gemv_check(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_
 
 using namespace mx;
 
+extern "C" size_t mx_gemv_workspace_size(int x_dtype, int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kMax31 = (int64_t)1 << 31;
+  if ((x_dtype != MX_F32 && x_dtype != MX_BF16) || M <= 0 || N <= 0 || K < 0 || M >= kMax31 ||
+      N >= kMax31 || K >= (int64_t)1 << 26 || K % 32)
+    return 0;
+  const GemvPlan p = gemv_plan(x_dtype, M, N, K, false);
+  return p.slices > 1 ? (size_t)p.slices * M * N * sizeof(float) : 0;
+}
+
 extern "C" int mx_gemv(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_codes,
                        const uint8_t* w_scales, int64_t w_scale_ld, int64_t M, int64_t N, int64_t K,
-                       float alpha, void* y, int y_dtype, int64_t ldy, void* stream) {
+                       float alpha, void* y, int y_dtype, int64_t ldy, void* workspace,
+                       size_t workspace_bytes, void* stream) {
   const int bad = gemv_check(x, x_dtype, ldx, w_codes, w_scales, w_scale_ld, M, N, K, y, y_dtype, ldy);
   if (bad != MX_OK || M == 0 || N == 0) return bad;
-  const GemvArgs a{x,       ldx, M, w_codes, w_scales, w_scale_ld, nullptr, nullptr, M, N,
-                   (int)K,  1,   1, y_dtype == MX_BF16, alpha, y,  ldy,     0,       0};
-  return gemv_any<false>(a, x_dtype, M, 1, as_stream(stream));
+  const size_t need = mx_gemv_workspace_size(x_dtype, M, N, K);
+  if (need) {
+    MX_REQUIRE(workspace && workspace_bytes >= need, MX_ERR_WORKSPACE);
+    MX_REQUIRE(aligned16(workspace), MX_ERR_ALIGN);
+  }
+  const GemvPlan p = gemv_plan(x_dtype, M, N, K, false);
+  GemvArgs a = {};
+  a.x = x; a.ldx = ldx; a.x_rows = (int)M; a.M = (int)M; a.N = N; a.K = (int)K;
+  a.codes = w_codes; a.scales = w_scales; a.scale_ld = w_scale_ld;
+  a.scale_end = (N - 1) * w_scale_ld + K / 32;
+  a.alpha = alpha; a.y = y; a.y_bf16 = y_dtype == MX_BF16; a.ldy = ldy;
+  a.partial = static_cast<float*>(workspace);
+  return gemv_any<false>(a, p, x_dtype, 0, as_stream(stream));
 }
 
 extern "C" int mx_gemv_grouped(const void* x, int x_dtype, int64_t ldx, int64_t x_rows,
@@ -334,9 +589,14 @@ extern "C" int mx_gemv_grouped(const void* x, int x_dtype, int64_t ldx, int64_t 
   if (rows == 0 || N == 0 || x_rows == 0) return MX_OK;
   MX_REQUIRE(offs, MX_ERR_NULL);
   MX_REQUIRE(aligned16(offs) && aligned16(src), MX_ERR_ALIGN);
-  const GemvArgs a{x,      ldx,        x_rows,      w_codes, w_scales, w_scale_ld, offs, src, rows, N,
-                   (int)K, (int)top_k, (int)groups, y_dtype == MX_BF16, alpha, y, ldy, 0, 0};
   // at most `rows` groups hold rows; their average count picks the row tile
   const int64_t held = hmin(groups, rows);
-  return gemv_any<true>(a, x_dtype, cdiv(rows, held), held, as_stream(stream));
+  const GemvPlan p = gemv_plan(x_dtype, cdiv(rows, held), N, K, true);
+  GemvArgs a = {};
+  a.x = x; a.ldx = ldx; a.x_rows = (int)x_rows; a.src = src; a.top_k = (int)top_k;
+  a.M = (int)rows; a.N = N; a.K = (int)K; a.offs = offs; a.groups = (int)groups;
+  a.codes = w_codes; a.scales = w_scales; a.scale_ld = w_scale_ld;
+  a.scale_end = (groups * N - 1) * w_scale_ld + K / 32;
+  a.alpha = alpha; a.y = y; a.y_bf16 = y_dtype == MX_BF16; a.ldy = ldy;
+  return gemv_any<true>(a, p, x_dtype, held, as_stream(stream));
 }

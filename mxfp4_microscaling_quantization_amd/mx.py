@@ -60,7 +60,9 @@ SIGNATURES = {
     "mx_linear_fwd_rht": ([_P, _P, _i32, _i64, _i64, _i64, _u32, _P, _P, _P, _P, _P, _P], _i32),
     "mx_linear_bwd_rht": ([_P, _i32, _i64, _i64, _i64, _P, _P, _P, _P, _u64, _u32, _P, _P, _P, _sz,
                            _P], _i32),
-    "mx_gemv": ([_P, _i32, _i64, _P, _P, _i64, _i64, _i64, _i64, _f32, _P, _i32, _i64, _P], _i32),
+    "mx_gemv_workspace_size": ([_i32, _i64, _i64, _i64], _sz),
+    "mx_gemv": ([_P, _i32, _i64, _P, _P, _i64, _i64, _i64, _i64, _f32, _P, _i32, _i64, _P, _sz, _P],
+                _i32),
     "mx_gemv_grouped": ([_P, _i32, _i64, _i64, _P, _i64, _P, _P, _i64, _P, _i64, _i64, _i64, _i64,
                          _f32, _P, _i32, _i64, _P], _i32),
     "mx_moe_plan_workspace_size": ([_i64, _i64, _i64], _sz),
@@ -332,10 +334,15 @@ def mx_linear_bwd_rht(dy, dtype, M, N, K, xq_codes, xq_scales, wq_codes, wq_scal
         _stream(stream)))
 
 
+def mx_gemv_workspace_size(x_dtype, M, N, K) -> int:
+    return int(lib().mx_gemv_workspace_size(x_dtype, M, N, K))
+
+
 def mx_gemv(x, x_dtype, ldx, w_codes, w_scales, w_scale_ld, M, N, K, alpha, y, y_dtype, ldy,
-            stream=None):
+            workspace=None, workspace_bytes=0, stream=None):
     _check("mx_gemv", lib().mx_gemv(_ptr(x), x_dtype, ldx, _ptr(w_codes), _ptr(w_scales), w_scale_ld,
-                                    M, N, K, alpha, _ptr(y), y_dtype, ldy, _stream(stream)))
+                                    M, N, K, alpha, _ptr(y), y_dtype, ldy, _ptr(workspace),
+                                    workspace_bytes, _stream(stream)))
 
 
 def mx_gemv_grouped(x, x_dtype, ldx, x_rows, src, top_k, w_codes, w_scales, w_scale_ld, offs, groups,
@@ -565,7 +572,8 @@ def _packed_weight(w, groups):
     return codes, scales, codes.shape[-2], 2 * codes.shape[-1], scales.shape[-1]
 
 
-def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, stream=None):
+def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, workspace=None,
+         stream=None):
     """alpha x deq(W)^T of a few rows x [M, K] (float32 or bf16) and a packed weight
     w = (codes [N, K/2], scales [N, >= K/32]); returns [M, N]."""
     M, K = x.shape
@@ -576,8 +584,11 @@ def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, strea
     if out is not None:
         out_dtype = out.dtype
     y = _output(out, (M, N), out_dtype, x, stream, x, codes, scales)
+    need = mx_gemv_workspace_size(dtype_code(x), M, N, K)
+    if workspace is None and need:
+        workspace = _empty((need,), torch.uint8, x, stream)
     mx_gemv(x, dtype_code(x), ldx, codes, scales, pitch, M, N, K, alpha, y, dtype_code(y),
-            _row_ld(y, "out"), stream)
+            _row_ld(y, "out"), workspace, 0 if workspace is None else workspace.nbytes, stream)
     return y
 
 

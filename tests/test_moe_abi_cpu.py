@@ -21,13 +21,14 @@ def L():
 
 
 def test_gemv_validation(L):
-    def call(x=GOOD, xt=1, ldx=64, c=GOOD, s=GOOD, pitch=2, M=1, N=5, K=64, y=GOOD, yt=0, ldy=5):
-        return L.mx_gemv(x, xt, ldx, c, s, pitch, M, N, K, 1.0, y, yt, ldy, None)
+    def call(x=GOOD, xt=1, ldx=64, c=GOOD, s=GOOD, pitch=2, M=1, N=5, K=64, y=GOOD, yt=0, ldy=5,
+             ws=None, n=0):
+        return L.mx_gemv(x, xt, ldx, c, s, pitch, M, N, K, 1.0, y, yt, ldy, ws, n, None)
 
     assert call(xt=2) == mx.MX_ERR_ENUM
     assert call(yt=-1) == mx.MX_ERR_ENUM
     for bad in ({"K": 48}, {"K": -32}, {"ldx": 63}, {"pitch": 1}, {"ldy": 4}, {"M": -1}, {"N": -1},
-                {"M": BIG}, {"N": BIG, "ldy": BIG}, {"K": BIG, "ldx": BIG, "pitch": BIG}):
+                {"M": BIG}, {"N": BIG, "ldy": BIG}, {"K": 1 << 26, "ldx": 1 << 26, "pitch": 1 << 21}, {"pitch": 1 << 26}):
         assert call(**bad) == mx.MX_ERR_SHAPE, bad
     for name in ("x", "c", "s", "y"):
         assert call(**{name: None}) == mx.MX_ERR_NULL, name
@@ -35,6 +36,14 @@ def test_gemv_validation(L):
     assert call(x=None, c=None, s=None, y=None, M=0) == mx.MX_OK
     assert call(x=None, c=None, s=None, y=None, N=0) == mx.MX_OK
     assert call(y=None, K=0) == mx.MX_ERR_NULL
+    size = L.mx_gemv_workspace_size
+    assert size(1, 1, 64, 64) == size(7, 1, 64, 64) == size(1, -1, 64, 64) == size(1, 1, 64, 1 << 26) == 0
+    need = size(1, 40, 4096, 14336)
+    assert need >= 2 * 40 * 4096 * 4
+    long = {"M": 40, "N": 4096, "K": 14336, "ldx": 14336, "pitch": 448, "ldy": 4096}
+    assert call(**long) == mx.MX_ERR_WORKSPACE
+    assert call(**long, ws=GOOD, n=need - 1) == mx.MX_ERR_WORKSPACE
+    assert call(**long, ws=BAD, n=need) == mx.MX_ERR_ALIGN
 
 
 def test_gemv_grouped_validation(L):
