@@ -481,7 +481,12 @@ static GemvPlan gemv_plan(int x_dtype, int64_t rows, int64_t N, int64_t K, bool 
   p.steps = 1;
   while (p.steps < (p.mt == 1 ? 4 : 2) && passes(p.steps) > passes(p.mt == 1 ? 4 : 2)) ++p.steps;
   const int n = passes(p.steps);
-  const bool slice = !grouped && n > 1;
+  // A contraction longer than a workgroup's windows goes in rounds, which fetch x again for
+  // every tile, or in slices over workgroups and one more launch for their sums.  Slices pay
+  // where x is many rows or the tiles are few: 40 rows of 8192 x 8192 25.9 us (rounds: 42.9),
+  // 8 rows of 4096 x 14336 18.2 us (23.8), but one row of 8192 x 8192 17.7 us (13.6).
+  const bool slice = !grouped && n > 1 &&
+                     (p.mt > 1 ? rows <= 1024 : cdiv(N, kGemvTile) * cdiv(rows, rt) <= 64);
   p.rounds = slice ? 1 : n;
   p.slices = slice ? n : 1;
   p.window = (int)cdiv(cdiv(nblk ? nblk : 1, (int64_t)n * p.waves), 4) * 4;

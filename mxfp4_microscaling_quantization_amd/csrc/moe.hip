@@ -87,12 +87,22 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_place(const ID* __restric
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    int32_t row = 0;
-    for (int e = 0; e < bins; ++e) {
-      if (blockIdx.x == 0) offs[e] = row;
-      s_base[e] += row;
-      row += s_total[e];
+  if (wave == 0) {  // rows of the bins before each: lanes hold 64 bins at a time
+    int32_t before = 0;
+    for (int e0 = 0; e0 < bins; e0 += 64) {
+      const int e = e0 + lane;
+      const int32_t n = e < bins ? s_total[e] : 0;
+      int32_t upto = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int32_t up = __shfl_up(upto, d);
+        upto += lane >= d ? up : 0;
+      }
+      if (e < bins) {
+        if (blockIdx.x == 0) offs[e] = before + upto - n;
+        s_base[e] += before + upto - n;
+      }
+      before += __shfl(upto, 63);
     }
   }
   for (int64_t s0 = begin; s0 < end; s0 += kPlanThreads) {
@@ -111,11 +121,13 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_place(const ID* __restric
     if (in && before == 0) s_wave[wave][bin] = __popcll(same);
     __syncthreads();
     for (int e = tid; e < bins; e += kPlanThreads) {
-      int32_t row = s_base[e];
+      int32_t n[kPlanWaves], row = s_base[e];
+#pragma unroll
+      for (int w = 0; w < kPlanWaves; ++w) n[w] = s_wave[w][e];
+#pragma unroll
       for (int w = 0; w < kPlanWaves; ++w) {
-        const int32_t n = s_wave[w][e];
         s_wave[w][e] = row;
-        row += n;
+        row += n[w];
       }
       s_base[e] = row;
     }
@@ -247,7 +259,8 @@ __global__ __launch_bounds__(256) void k_dispatch_scaled(const T* __restrict__ x
 
 // Q_D of a token's 1x32 blocks (a quad of lanes per block, 8 values a lane) once,
 // its codes and scale byte written to the token's top_k rows: the values are the
-// same in each, so one conversion serves them all.
+// same in each, so one conversion serves them all.  Every lane of a quad gets the
+// block's 16 bytes of codes and stores them to one of the rows, four rows at a time.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_dispatch_quant(const T* __restrict__ x, int64_t ldx,
                                                         const int32_t* __restrict__ pos,
@@ -274,11 +287,12 @@ __global__ __launch_bounds__(256) void k_dispatch_quant(const T* __restrict__ x,
 #pragma unroll
       for (int i = 0; i < 4; ++i) w |= (cvt_rne_pair(v[2 * i], v[2 * i + 1], sc) & 0xFFu) << (8 * i);
     }
-    for (int j = 0; j < top_k; ++j) {
+    const uint4 block = make_uint4(dpp_u32<0x00>(w), dpp_u32<0x55>(w), dpp_u32<0xAA>(w), dpp_u32<0xFF>(w));
+    for (int j = r.run & 3; j < top_k; j += 4) {
       const int32_t to = pos[r.token * top_k + j];
       if (to < 0 || to >= rows) continue;
-      codes[(int64_t)to * runs + r.run] = w;
-      if ((r.run & 3) == 0) scales[(int64_t)to * scale_ld + (r.run >> 2)] = (uint8_t)byte;
+      *reinterpret_cast<uint4*>(codes + (int64_t)to * runs + (r.run & ~3)) = block;
+      scales[(int64_t)to * scale_ld + (r.run >> 2)] = (uint8_t)byte;
     }
   }
 }

@@ -137,8 +137,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: a Stream object costs 2.6 us more
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -516,30 +516,35 @@ def linear_bwd(dy: torch.Tensor, xq, wq, M, N, K, seed, workspace=None, stream=N
 
 # The conveniences below check what the C calls cannot see: types, shapes, that
 # every tensor is on the current device and that rows are contiguous (row strides
-# are passed on).  Outputs are allocated on the stream the call runs on.
-def _need(ok, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# are passed on).  Outputs are allocated on the stream the call runs on.  They sit
+# in front of calls of a few microseconds, so the checks are plain conditions and
+# messages are made only for an error.
+def _device_error(tensors):
+    bad = [str(t.device) for t in tensors if t is not None and t.get_device() != torch.cuda.current_device()]
+    return ValueError(f"tensor on {bad[0]}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _on_current_device(*tensors) -> None:
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.device.index == dev):
-            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+        if t is not None and t.get_device() != dev:
+            raise _device_error(tensors)
 
 
 def _row_ld(t: torch.Tensor, what: str) -> int:
     """Row stride in elements of a 2-D tensor with contiguous rows."""
     rows, cols = t.shape
-    _need(cols <= 1 or t.stride(1) == 1, f"{what}: rows must be contiguous")
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{what}: rows must be contiguous")
     if rows <= 1:
         return cols
-    _need(t.stride(0) >= cols, f"{what}: rows must not overlap")
-    return t.stride(0)
+    if ld < cols:
+        raise ValueError(f"{what}: rows must not overlap")
+    return ld
 
 
-def _empty(shape, dtype, like, stream, *inputs):
+def _empty(shape, dtype, like, stream, inputs=()):
     """An output of the current device, allocated on the stream the call runs on; the
     inputs are kept from reuse until that stream is done with them."""
     if stream is None:
@@ -553,42 +558,49 @@ def _empty(shape, dtype, like, stream, *inputs):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _output(out, shape, dtype, like, stream, *inputs):
+def _output(out, shape, dtype, like, stream, inputs):
     if out is None:
-        return _empty(shape, dtype, like, stream, *inputs)
-    _need(tuple(out.shape) == tuple(shape) and (dtype is None or out.dtype == dtype),
-          f"out must be {tuple(shape)} {dtype}")
+        return _empty(shape, dtype, like, stream, inputs)
+    if out.shape != shape or out.dtype != dtype:
+        raise ValueError(f"out must be {tuple(shape)} {dtype}, not {tuple(out.shape)} {out.dtype}")
     return out
 
 
-def _packed_weight(w, groups):
-    """(codes, scales, N, K, scale row pitch) of a packed weight [N, K], or of `groups` of them."""
-    codes, scales = w
-    lead = () if groups is None else (groups,)
-    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8, "packed weights are uint8")
-    _need(codes.is_contiguous() and scales.is_contiguous(), "packed weights must be contiguous")
-    _need(codes.dim() == len(lead) + 2 and codes.shape[:-1] == scales.shape[:-1]
-          and tuple(codes.shape[:-2]) == lead, "codes and scales must have the same rows")
-    return codes, scales, codes.shape[-2], 2 * codes.shape[-1], scales.shape[-1]
+def _workspace(workspace, need, like, stream):
+    return _empty((need,), torch.uint8, like, stream) if workspace is None and need else workspace
+
+
+def _nbytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _check_packed(codes, scales, K):
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError("packed weights are uint8")
+    if codes.shape[:-1] != scales.shape[:-1]:
+        raise ValueError("codes and scales must have the same rows")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("packed weights must be contiguous")
+    if 2 * codes.shape[-1] != K:
+        raise ValueError(f"x has {K} columns, the weight {2 * codes.shape[-1]}")
 
 
 def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, workspace=None,
          stream=None):
     """alpha x deq(W)^T of a few rows x [M, K] (float32 or bf16) and a packed weight
     w = (codes [N, K/2], scales [N, >= K/32]); returns [M, N]."""
+    codes, scales = w
     M, K = x.shape
-    codes, scales, N, wk, pitch = _packed_weight(w, None)
-    _need(wk == K, f"x has {K} columns, the weight {wk}")
-    _on_current_device(x, codes, scales, out)
-    ldx = _row_ld(x, "x")
+    _check_packed(codes, scales, K)
+    N = codes.shape[0]
+    _on_current_device(x, codes, scales, out, workspace)
+    xt, ldx = dtype_code(x), _row_ld(x, "x")
     if out is not None:
         out_dtype = out.dtype
-    y = _output(out, (M, N), out_dtype, x, stream, x, codes, scales)
-    need = mx_gemv_workspace_size(dtype_code(x), M, N, K)
-    if workspace is None and need:
-        workspace = _empty((need,), torch.uint8, x, stream)
-    mx_gemv(x, dtype_code(x), ldx, codes, scales, pitch, M, N, K, alpha, y, dtype_code(y),
-            _row_ld(y, "out"), workspace, 0 if workspace is None else workspace.nbytes, stream)
+    y = _output(out, (M, N), out_dtype, x, stream, (x, codes, scales))
+    workspace = _workspace(workspace, mx_gemv_workspace_size(xt, M, N, K), x, stream)
+    mx_gemv(x, xt, ldx, codes, scales, scales.shape[1], M, N, K, alpha, y, dtype_code(y),
+            _row_ld(y, "out"), workspace, _nbytes(workspace), stream)
     return y
 
 
@@ -598,20 +610,24 @@ def gemv_grouped(x: torch.Tensor, w, offs, src=None, top_k=1, alpha=1.0, out=Non
     src): w = (codes [E, N, K/2], scales [E, N, >= K/32]); returns [rows, N], where rows
     is src's length (without src: x's rows, each its own).  Rows from offs[E] on are
     left as `out` had them."""
+    codes, scales = w
     xr, K = x.shape
     groups = offs.numel() - 1
-    codes, scales, N, wk, pitch = _packed_weight(w, groups)
-    _need(wk == K, f"x has {K} columns, the weights {wk}")
-    _need(offs.dtype == torch.int64 and offs.is_contiguous(), "offs must be int64")
-    _need(src is None or (src.dtype == torch.int32 and src.is_contiguous()), "src must be int32")
+    _check_packed(codes, scales, K)
+    if codes.dim() != 3 or codes.shape[0] != groups:
+        raise ValueError(f"codes and scales must have the same rows, {groups} groups of them")
+    N = codes.shape[1]
+    if offs.dtype != torch.int64 or not offs.is_contiguous():
+        raise ValueError("offs must be int64")
+    if src is not None and (src.dtype != torch.int32 or not src.is_contiguous()):
+        raise ValueError("src must be int32")
     _on_current_device(x, codes, scales, offs, src, out)
-    ldx = _row_ld(x, "x")
     rows = xr if src is None else src.numel()
     if out is not None:
         out_dtype = out.dtype
-    y = _output(out, (rows, N), out_dtype, x, stream, x, codes, scales, offs, src)
-    mx_gemv_grouped(x, dtype_code(x), ldx, xr, src, top_k, codes, scales, pitch, offs, groups, rows,
-                    N, K, alpha, y, dtype_code(y), _row_ld(y, "out"), stream)
+    y = _output(out, (rows, N), out_dtype, x, stream, (x, codes, scales, offs, src))
+    mx_gemv_grouped(x, dtype_code(x), _row_ld(x, "x"), xr, src, top_k, codes, scales, scales.shape[2],
+                    offs, groups, rows, N, K, alpha, y, dtype_code(y), _row_ld(y, "out"), stream)
     return y
 
 
@@ -619,25 +635,30 @@ def moe_plan(ids: torch.Tensor, experts: int, workspace=None, stream=None):
     """(offs [experts + 1] int64, src [tokens * top_k] int32, pos [tokens, top_k] int32) of
     the expert ids [tokens, top_k] (int32 or int64; out of range: the slot is left out)."""
     tokens, top_k = ids.shape
-    _need(ids.dtype in (torch.int32, torch.int64), "ids must be int32 or int64")
-    _need(ids.is_contiguous(), "ids must be contiguous")
+    wide = ids.dtype == torch.int64
+    if not wide and ids.dtype != torch.int32:
+        raise ValueError("ids must be int32 or int64")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
     _on_current_device(ids, workspace)
-    need = mx_moe_plan_workspace_size(tokens, top_k, experts)
-    if workspace is None and need:
-        workspace = _empty((need,), torch.uint8, ids, stream)
-    offs = _empty((experts + 1,), torch.int64, ids, stream, ids, workspace)
+    workspace = _workspace(workspace, mx_moe_plan_workspace_size(tokens, top_k, experts), ids, stream)
+    offs = _empty((experts + 1,), torch.int64, ids, stream, (ids, workspace))
     src = _empty((tokens * top_k,), torch.int32, ids, stream)
     pos = _empty((tokens, top_k), torch.int32, ids, stream)
-    mx_moe_plan(ids, MX_I32 if ids.dtype == torch.int32 else MX_I64, tokens, top_k, experts, offs, src,
-                pos, workspace, 0 if workspace is None else workspace.nbytes, stream)
+    mx_moe_plan(ids, MX_I64 if wide else MX_I32, tokens, top_k, experts, offs, src, pos, workspace,
+                _nbytes(workspace), stream)
     return offs, src, pos
 
 
 def _routing(pos, weights, tokens):
-    _need(pos.dim() == 2 and pos.dtype == torch.int32 and pos.is_contiguous(), "pos must be int32 [tokens, top_k]")
-    _need(pos.shape[0] == tokens, f"pos is for {pos.shape[0]} tokens, not {tokens}")
-    _need(weights is None or (weights.dtype == torch.float32 and weights.shape == pos.shape
-                              and weights.is_contiguous()), "weights must be float32 like pos")
+    """top_k of pos [tokens, top_k]."""
+    if pos.dim() != 2 or pos.dtype != torch.int32 or not pos.is_contiguous():
+        raise ValueError("pos must be int32 [tokens, top_k]")
+    if pos.shape[0] != tokens:
+        raise ValueError(f"pos is for {pos.shape[0]} tokens, not {tokens}")
+    if weights is not None and (weights.dtype != torch.float32 or weights.shape != pos.shape
+                                or not weights.is_contiguous()):
+        raise ValueError("weights must be float32 like pos")
     return pos.shape[1]
 
 
@@ -648,7 +669,7 @@ def moe_dispatch(x: torch.Tensor, pos, weights=None, rows=None, out=None, stream
     top_k = _routing(pos, weights, tokens)
     _on_current_device(x, pos, weights, out)
     rows = out.shape[0] if out is not None else pos.numel() if rows is None else rows
-    o = _output(out, (rows, cols), x.dtype, x, stream, x, pos, weights)
+    o = _output(out, (rows, cols), x.dtype, x, stream, (x, pos, weights))
     mx_moe_dispatch(x, dtype_code(x), _row_ld(x, "x"), pos, weights, tokens, top_k, rows, cols, o,
                     _row_ld(o, "out"), stream)
     return o
@@ -661,13 +682,14 @@ def moe_dispatch_quantize(x: torch.Tensor, pos, rows=None, out=None, stream=None
     top_k = _routing(pos, None, tokens)
     if out is None:
         rows = pos.numel() if rows is None else rows
-        out = (_empty((rows, cols // 2), torch.uint8, x, stream, x, pos),
+        out = (_empty((rows, cols // 2), torch.uint8, x, stream, (x, pos)),
                _empty((rows, cols // 32), torch.uint8, x, stream))
     codes, scales = out
     rows = codes.shape[0]
-    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.is_contiguous()
-          and scales.is_contiguous() and codes.dim() == 2 and codes.shape[1] == cols // 2
-          and scales.dim() == 2 and scales.shape[0] == rows, "out must be packed uint8 codes and scales")
+    if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous()
+            or not scales.is_contiguous() or codes.dim() != 2 or codes.shape[1] != cols // 2
+            or scales.dim() != 2 or scales.shape[0] != rows):
+        raise ValueError("out must be packed uint8 codes and scales")
     _on_current_device(x, pos, codes, scales)
     mx_moe_dispatch_quantize(x, dtype_code(x), _row_ld(x, "x"), pos, tokens, top_k, rows, cols, codes,
                              scales, scales.shape[1], stream)
@@ -683,7 +705,7 @@ def moe_combine(z: torch.Tensor, pos, weights=None, out=None, out_dtype=torch.fl
     _on_current_device(z, pos, weights, out)
     if out is not None:
         out_dtype = out.dtype
-    y = _output(out, (tokens, cols), out_dtype, z, stream, z, pos, weights)
+    y = _output(out, (tokens, cols), out_dtype, z, stream, (z, pos, weights))
     mx_moe_combine(z, dtype_code(z), _row_ld(z, "z"), rows, pos, weights, tokens, top_k, cols, y,
                    dtype_code(y), _row_ld(y, "out"), stream)
     return y
@@ -695,9 +717,10 @@ def moe_combine_bwd(dy: torch.Tensor, z: torch.Tensor, pos, weights=None, out=No
     tokens, cols = dy.shape
     rows = z.shape[0]
     top_k = _routing(pos, weights, tokens)
-    _need(z.dim() == 2 and z.shape[1] == cols, "z and dy must have the same columns")
+    if z.dim() != 2 or z.shape[1] != cols:
+        raise ValueError("z and dy must have the same columns")
     _on_current_device(dy, z, pos, weights, out)
-    dz = _output(out, (rows, cols), dy.dtype, dy, stream, dy, z, pos, weights)
+    dz = _output(out, (rows, cols), dy.dtype, dy, stream, (dy, z, pos, weights))
     dw = _empty((tokens, top_k), torch.float32, dy, stream)
     mx_moe_combine_bwd(dy, dtype_code(dy), _row_ld(dy, "dy"), z, dtype_code(z), _row_ld(z, "z"), rows,
                        pos, weights, tokens, top_k, cols, dz, _row_ld(dz, "out"), dw, stream)
