@@ -91,25 +91,6 @@ struct XTerms<float> {
   }
 };
 
-// 8 values of x, raw; WIDE: on 16 bytes.
-template <typename T, bool WIDE>
-__device__ __forceinline__ void load_x8(const T* p, uint32_t* w) {
-  constexpr int W = 2 * sizeof(T);
-  if constexpr (WIDE) {
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const uint4 u = reinterpret_cast<const uint4*>(p)[i];
-      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
-    }
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(p[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
-  }
-}
-
 // Orders a wave's LDS accesses around an exchange between its lanes.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
@@ -181,7 +162,7 @@ struct GroupTiles {
 // rows (term p of row q in column 4 p + q): the terms' sums are added at the end.
 constexpr int kMaxWaves = 8, kGemvTile = 64;
 
-template <typename T, int MT, int S, bool GROUPED, bool WIDE>
+template <typename T, int MT, int S, bool GROUPED>
 __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   constexpr int X = XTerms<T>::kTerms;
   constexpr int XW = 2 * sizeof(T);        // words of 8 values of x
@@ -324,7 +305,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
       for (int k = 0; k < XW; ++k) xv[q][k] = 0;
       if (4 * four + q < cur.mrows && k0 < 32 * b1) {
         const int64_t r = __builtin_amdgcn_readlane(row_of, 4 * four + q);
-        load_x8<T, WIDE>(x + (r * a.ldx + k0), xv[q]);
+        __builtin_memcpy(xv[q], x + (r * a.ldx + k0), 4 * XW);  // at T's alignment
       }
     }
   };
@@ -493,7 +474,7 @@ static GemvPlan gemv_plan(int x_dtype, int64_t rows, int64_t N, int64_t K, bool 
   return p;
 }
 
-template <typename T, int MT, int S, bool GROUPED, bool WIDE>
+template <typename T, int MT, int S, bool GROUPED>
 static int gemv_launch(GemvArgs a, const GemvPlan& p, int64_t groups, hipStream_t st) {
   constexpr int R = (sizeof(T) == 2 ? 16 : 4) * MT;
   constexpr int kBytes = 5120 + 16 * MT * (kGemvTile + 4) * 4;  // LDS of a wave
@@ -505,31 +486,27 @@ static int gemv_launch(GemvArgs a, const GemvPlan& p, int64_t groups, hipStream_
   // a group adds less than one row tile to the rows'
   const int64_t row_tiles = GROUPED ? cdiv(a.M, R) + groups : cdiv(a.M, R);
   const unsigned grid = (unsigned)hmin(row_tiles * p.slices * a.ntiles, device_cu_count());
-  k_gemv<T, MT, S, GROUPED, WIDE><<<grid, 64 * p.waves, (size_t)p.waves * kBytes, st>>>(a);
+  k_gemv<T, MT, S, GROUPED><<<grid, 64 * p.waves, (size_t)p.waves * kBytes, st>>>(a);
   if (p.slices > 1)
     k_gemv_sum<<<(unsigned)hmin(cdiv(a.M * a.N, 256), 4096), 256, 0, st>>>(
         a.partial, p.slices, a.M, a.N, a.alpha, a.y, a.y_bf16, a.ldy);
   return launch_status();
 }
 
-template <typename T, bool GROUPED, bool WIDE>
+template <typename T, bool GROUPED>
 static int gemv_rows(const GemvArgs& a, const GemvPlan& p, int64_t groups, hipStream_t st) {
-  if (p.mt == 2) return gemv_launch<T, 2, 2, GROUPED, WIDE>(a, p, groups, st);
-  if (p.mt == 3) return gemv_launch<T, 3, 2, GROUPED, WIDE>(a, p, groups, st);
-  if (p.steps == 1) return gemv_launch<T, 1, 1, GROUPED, WIDE>(a, p, groups, st);
-  if (p.steps == 2) return gemv_launch<T, 1, 2, GROUPED, WIDE>(a, p, groups, st);
-  if (p.steps == 3) return gemv_launch<T, 1, 3, GROUPED, WIDE>(a, p, groups, st);
-  return gemv_launch<T, 1, 4, GROUPED, WIDE>(a, p, groups, st);
+  if (p.mt == 2) return gemv_launch<T, 2, 2, GROUPED>(a, p, groups, st);
+  if (p.mt == 3) return gemv_launch<T, 3, 2, GROUPED>(a, p, groups, st);
+  if (p.steps == 1) return gemv_launch<T, 1, 1, GROUPED>(a, p, groups, st);
+  if (p.steps == 2) return gemv_launch<T, 1, 2, GROUPED>(a, p, groups, st);
+  if (p.steps == 3) return gemv_launch<T, 1, 3, GROUPED>(a, p, groups, st);
+  return gemv_launch<T, 1, 4, GROUPED>(a, p, groups, st);
 }
 
 template <bool GROUPED>
 static int gemv_any(const GemvArgs& a, const GemvPlan& p, int x_dtype, int64_t groups, hipStream_t st) {
-  const bool wide = a.ldx * (x_dtype == MX_BF16 ? 2 : 4) % 16 == 0;
-  if (x_dtype == MX_BF16)
-    return wide ? gemv_rows<uint16_t, GROUPED, true>(a, p, groups, st)
-                : gemv_rows<uint16_t, GROUPED, false>(a, p, groups, st);
-  return wide ? gemv_rows<float, GROUPED, true>(a, p, groups, st)
-              : gemv_rows<float, GROUPED, false>(a, p, groups, st);
+  return x_dtype == MX_BF16 ? gemv_rows<uint16_t, GROUPED>(a, p, groups, st)
+                            : gemv_rows<float, GROUPED>(a, p, groups, st);
 }
 
 static int gemv_check(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_codes,

@@ -153,50 +153,50 @@ static PlanShape plan_shape(int64_t slots, int64_t experts) {
 }
 
 // ============================================================== rows
-// V consecutive values of a row: V = 8 where every row starts on 16 bytes and
-// the width is a multiple of 8, else one value at a time.
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* p, float v[V]);
-template <>
-__device__ __forceinline__ void load_row<float, 1>(const float* p, float v[1]) { v[0] = *p; }
-template <>
-__device__ __forceinline__ void load_row<uint16_t, 1>(const uint16_t* p, float v[1]) {
-  v[0] = bf16_lo(*p);
-}
-template <>
-__device__ __forceinline__ void load_row<float, 8>(const float* p, float v[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load_row<uint16_t, 8>(const uint16_t* p, float v[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x);
-  v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-  v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z);
-  v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+// A run is 8 consecutive values of a row.  Rows start at any multiple of their type's
+// size: the vector accesses carry that alignment, which the hardware takes.  Where the
+// width is no multiple of 8 the last run starts early and covers values of the run before
+// it once more (they are stored twice alike, and summed once).  One value a thread took
+// 206 us where such runs take 165 (combine of 2885 columns, float32 to bf16), and a branch
+// for a short last run cost whole ones too (a copy of 2880 bf16 columns 146 us, not 93).
+// NARROW: rows of fewer than 8 values, one run of n of them.
+template <typename T, bool NARROW>
+__device__ __forceinline__ void load_run(const T* p, int n, float v[8]) {
+  if constexpr (!NARROW) {
+    T raw[8];
+    __builtin_memcpy(raw, p, sizeof(raw));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2) v[i] = bf16_lo(raw[i]);
+      else v[i] = raw[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.0f;
+      if (i < n) {
+        if constexpr (sizeof(T) == 2) v[i] = bf16_lo(p[i]);
+        else v[i] = p[i];
+      }
+    }
+  }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_row(T* p, const float v[V]);
-template <>
-__device__ __forceinline__ void store_row<float, 1>(float* p, const float v[1]) { *p = v[0]; }
-template <>
-__device__ __forceinline__ void store_row<uint16_t, 1>(uint16_t* p, const float v[1]) {
-  *p = (uint16_t)f32_to_bf16_rne(v[0]);
-}
-template <>
-__device__ __forceinline__ void store_row<float, 8>(float* p, const float v[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-template <>
-__device__ __forceinline__ void store_row<uint16_t, 8>(uint16_t* p, const float v[8]) {
-  uint32_t w[4];
+template <typename T, bool NARROW>
+__device__ __forceinline__ void store_run(T* p, int n, const float v[8]) {
+  T raw[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_rne(v[2 * i]) | f32_to_bf16_rne(v[2 * i + 1]) << 16;
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 2) raw[i] = (T)f32_to_bf16_rne(v[i]);
+    else raw[i] = v[i];
+  }
+  if constexpr (!NARROW) {
+    __builtin_memcpy(p, raw, sizeof(raw));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = raw[i];
+  }
 }
 
 // Position of a thread's run in the flat order (token, run of the row): the
@@ -213,46 +213,66 @@ __device__ __forceinline__ RowRun row_run(int64_t first, int at, int runs) {
 }
 
 // ============================================================== dispatch
-// One read of a token's run, top_k writes.  The copy moves words of U (as wide as
-// the rows' alignment allows) whatever they hold, so NaN patterns stay as they are.
-template <typename U>
-__global__ __launch_bounds__(256) void k_dispatch_copy(const U* __restrict__ x, int64_t ldx,
+// One read of a token's run, top_k writes.  The copy moves 16-byte runs of elements of
+// `size` bytes whatever they hold, so NaN patterns stay as they are.
+template <typename T, bool NARROW>
+__global__ __launch_bounds__(256) void k_dispatch_copy(const T* __restrict__ x, int64_t ldx,
                                                        const int32_t* __restrict__ pos,
                                                        int64_t tokens, int top_k, int64_t rows,
-                                                       int runs, U* __restrict__ out, int64_t ldo) {
+                                                       int cols, int runs, T* __restrict__ out,
+                                                       int64_t ldo) {
+  constexpr int E = 16 / sizeof(T);
   const int64_t total = tokens * runs;
   for (int64_t first = (int64_t)blockIdx.x * 256; first < total; first += (int64_t)gridDim.x * 256) {
     if (first + threadIdx.x >= total) continue;
     const RowRun r = row_run(first, threadIdx.x, runs);
-    const U v = x[r.token * ldx + r.run];
+    const int n = min(E, cols), col = min(r.run * E, cols - n);
+    const T* p = x + r.token * ldx + col;
+    T v[E];
+    if constexpr (!NARROW) {
+      __builtin_memcpy(v, p, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i < n) v[i] = p[i];
+    }
     for (int j = 0; j < top_k; ++j) {
       const int32_t to = pos[r.token * top_k + j];
-      if (to >= 0 && to < rows) out[to * ldo + r.run] = v;
+      if (to < 0 || to >= rows) continue;
+      T* o = out + to * ldo + col;
+      if constexpr (!NARROW) {
+        __builtin_memcpy(o, v, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (i < n) o[i] = v[i];
+      }
     }
   }
 }
 
-template <typename T, int V>
+template <typename T, bool NARROW>
 __global__ __launch_bounds__(256) void k_dispatch_scaled(const T* __restrict__ x, int64_t ldx,
                                                          const int32_t* __restrict__ pos,
                                                          int64_t tokens, int top_k, int64_t rows,
-                                                         int runs,
+                                                         int cols, int runs,
                                                          const float* __restrict__ weights,
                                                          T* __restrict__ out, int64_t ldo) {
   const int64_t total = tokens * runs;
   for (int64_t first = (int64_t)blockIdx.x * 256; first < total; first += (int64_t)gridDim.x * 256) {
     if (first + threadIdx.x >= total) continue;
     const RowRun r = row_run(first, threadIdx.x, runs);
-    float v[V];
-    load_row<T, V>(x + r.token * ldx + (int64_t)r.run * V, v);
+    const int n = min(8, cols), col = min(r.run * 8, cols - n);
+    float v[8];
+    load_run<T, NARROW>(x + r.token * ldx + col, n, v);
     for (int j = 0; j < top_k; ++j) {
       const int32_t to = pos[r.token * top_k + j];
       if (to < 0 || to >= rows) continue;
       const float w = weights[r.token * top_k + j];
-      float u[V];
+      float u[8];
 #pragma unroll
-      for (int i = 0; i < V; ++i) u[i] = w * v[i];
-      store_row<T, V>(out + to * ldo + (int64_t)r.run * V, u);
+      for (int i = 0; i < 8; ++i) u[i] = w * v[i];
+      store_run<T, NARROW>(out + to * ldo + col, n, u);
     }
   }
 }
@@ -261,7 +281,7 @@ __global__ __launch_bounds__(256) void k_dispatch_scaled(const T* __restrict__ x
 // its codes and scale byte written to the token's top_k rows: the values are the
 // same in each, so one conversion serves them all.  Every lane of a quad gets the
 // block's 16 bytes of codes and stores them to one of the rows, four rows at a time.
-template <typename T, int V>
+template <typename T>
 __global__ __launch_bounds__(256) void k_dispatch_quant(const T* __restrict__ x, int64_t ldx,
                                                         const int32_t* __restrict__ pos,
                                                         int64_t tokens, int top_k, int64_t rows,
@@ -272,14 +292,8 @@ __global__ __launch_bounds__(256) void k_dispatch_quant(const T* __restrict__ x,
   for (int64_t first = (int64_t)blockIdx.x * 256; first < total; first += (int64_t)gridDim.x * 256) {
     if (first + threadIdx.x >= total) continue;  // whole quads: total is a multiple of 4
     const RowRun r = row_run(first, threadIdx.x, runs);
-    const T* p = x + r.token * ldx + (int64_t)r.run * 8;
     float v[8];
-    if constexpr (V == 8) {
-      load_row<T, 8>(p, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) load_row<T, 1>(p + i, v + i);
-    }
+    load_run<T, false>(x + r.token * ldx + (int64_t)r.run * 8, 8, v);
     const uint32_t byte = scale_byte_of(quad_max_u32(amax_bits<8>(v)));
     uint32_t w = 0;
     if (byte != 255u) {
@@ -298,67 +312,108 @@ __global__ __launch_bounds__(256) void k_dispatch_quant(const T* __restrict__ x,
 }
 
 // ============================================================== combine
+// A token's slots are taken four at a time, so that four rows of z are on their way
+// together.  A slot left out loads row 0 and adds nothing.
+constexpr int kSlots = 4;
+
+struct Slots {
+  int32_t row[kSlots];
+  float w[kSlots];
+  bool real[kSlots];
+};
+__device__ __forceinline__ Slots load_slots(const int32_t* __restrict__ pos,
+                                            const float* __restrict__ weights, int64_t first,
+                                            int left, int64_t rows) {
+  Slots s;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int64_t at = first + min(i, left - 1);
+    s.row[i] = pos[at];
+    s.w[i] = weights ? weights[at] : 1.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    s.real[i] = i < left && s.row[i] >= 0 && s.row[i] < rows;
+    s.row[i] = s.real[i] ? s.row[i] : 0;
+  }
+  return s;
+}
+
 // Sums in float32 in slot order, each product rounded first.
-template <typename TZ, typename TY, int V>
+template <typename TZ, typename TY, bool NARROW>
 __global__ __launch_bounds__(256) void k_combine(const TZ* __restrict__ z, int64_t ldz, int64_t rows,
                                                  const int32_t* __restrict__ pos,
                                                  const float* __restrict__ weights, int64_t tokens,
-                                                 int top_k, int runs, TY* __restrict__ y,
-                                                 int64_t ldy) {
+                                                 int top_k, int cols, int runs,
+                                                 TY* __restrict__ y, int64_t ldy) {
   const int64_t total = tokens * runs;
   for (int64_t first = (int64_t)blockIdx.x * 256; first < total; first += (int64_t)gridDim.x * 256) {
     if (first + threadIdx.x >= total) continue;
     const RowRun r = row_run(first, threadIdx.x, runs);
-    float acc[V];
+    const int n = min(8, cols), col = min(r.run * 8, cols - n);
+    float acc[8] = {};
+    for (int j = 0; j < top_k && rows; j += kSlots) {
+      const Slots s = load_slots(pos, weights, r.token * top_k + j, top_k - j, rows);
+      float v[kSlots][8];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    for (int j = 0; j < top_k; ++j) {
-      const int32_t from = pos[r.token * top_k + j];
-      if (from < 0 || from >= rows) continue;
-      const float w = weights ? weights[r.token * top_k + j] : 1.0f;
-      float v[V];
-      load_row<TZ, V>(z + from * ldz + (int64_t)r.run * V, v);
+      for (int k = 0; k < kSlots; ++k) load_run<TZ, NARROW>(z + s.row[k] * ldz + col, n, v[k]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += w * v[i];
+      for (int k = 0; k < kSlots; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = s.real[k] ? acc[i] + s.w[k] * v[k][i] : acc[i];
     }
-    store_row<TY, V>(y + r.token * ldy + (int64_t)r.run * V, acc);
+    store_run<TY, NARROW>(y + r.token * ldy + col, n, acc);
   }
 }
 
 // One workgroup per token: dz rows as a weighted dispatch, and each slot's inner
 // product <dy, z> as per-thread sums, then a fixed tree over lanes and waves.
-template <typename TY, typename TZ, int V>
+template <typename TY, typename TZ, bool NARROW>
 __global__ __launch_bounds__(256) void k_combine_bwd(
     const TY* __restrict__ dy, int64_t lddy, const TZ* __restrict__ z, int64_t ldz, int64_t rows,
     const int32_t* __restrict__ pos, const float* __restrict__ weights, int64_t tokens, int top_k,
-    int runs, TY* __restrict__ dz, int64_t lddz, float* __restrict__ dw) {
-  __shared__ float s_part[4];
+    int cols, int runs, TY* __restrict__ dz, int64_t lddz, float* __restrict__ dw) {
+  __shared__ float s_part[2][4][kSlots];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  int turn = 0;  // the two halves of s_part alternate: one barrier a turn
   for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
-    for (int j = 0; j < top_k; ++j) {
-      const int32_t row = pos[t * top_k + j];
-      const bool real = row >= 0 && row < rows;
-      float part = 0.0f;
-      if (real) {
-        const float w = weights ? weights[t * top_k + j] : 1.0f;
-        for (int r = threadIdx.x; r < runs; r += 256) {
-          float g[V], v[V], u[V];
-          load_row<TY, V>(dy + t * lddy + (int64_t)r * V, g);
-          load_row<TZ, V>(z + row * ldz + (int64_t)r * V, v);
+    for (int j = 0; j < top_k; j += kSlots, turn ^= 1) {
+      const Slots s = load_slots(pos, weights, t * top_k + j, top_k - j, rows);
+      float part[kSlots] = {};
+      if (rows) {
+        for (int r = threadIdx.x; r < runs; r += blockDim.x) {
+          const int n = min(8, cols), col = min(r * 8, cols - n);
+          const int again = r * 8 - col;  // values that the run before has
+          float g[8], v[kSlots][8], u[8];
+          load_run<TY, NARROW>(dy + t * lddy + col, n, g);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            part += g[i] * v[i];
-            u[i] = w * g[i];
+          for (int k = 0; k < kSlots; ++k) load_run<TZ, NARROW>(z + s.row[k] * ldz + col, n, v[k]);
+#pragma unroll
+          for (int k = 0; k < kSlots; ++k) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              part[k] = i < again ? part[k] : part[k] + g[i] * v[k][i];
+              u[i] = s.w[k] * g[i];
+            }
+            if (s.real[k]) store_run<TY, NARROW>(dz + s.row[k] * lddz + col, n, u);
           }
-          store_row<TY, V>(dz + row * lddz + (int64_t)r * V, u);
         }
       }
 #pragma unroll
-      for (int d = 32; d; d >>= 1) part += __shfl_xor(part, d);
-      if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = part;
+      for (int k = 0; k < kSlots; ++k) {
+#pragma unroll
+        for (int d = 32; d; d >>= 1) part[k] += __shfl_xor(part[k], d);
+        if (lane == 0) s_part[turn][wave][k] = part[k];
+      }
       __syncthreads();
-      if (threadIdx.x == 0)
-        dw[t * top_k + j] = real ? (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]) : 0.0f;
-      __syncthreads();
+      if (threadIdx.x < kSlots && j + (int)threadIdx.x < top_k) {
+        float sum = 0.0f;
+        for (int w = 0; w < waves; ++w) sum += s_part[turn][w][threadIdx.x];
+        bool real = false;
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) real = (int)threadIdx.x == k ? s.real[k] : real;
+        dw[t * top_k + j + threadIdx.x] = real ? sum : 0.0f;
+      }
     }
   }
 }
@@ -368,9 +423,6 @@ static unsigned row_grid(int64_t work_items) {
   return (unsigned)hmin(cdiv(work_items, 256), (int64_t)device_cu_count() * 64);
 }
 
-// Whether rows of `ld` elements of `size` bytes all start on 16 bytes.
-static bool rows16(int64_t ld, int size) { return ld * size % 16 == 0; }
-static int size_of(int dtype) { return dtype == MX_BF16 ? 2 : 4; }
 static bool is_float_type(int t) { return t == MX_F32 || t == MX_BF16; }
 constexpr int64_t kMax31 = (int64_t)1 << 31;
 
@@ -429,40 +481,30 @@ extern "C" int mx_moe_dispatch(const void* x, int dtype, int64_t ldx, const int3
   if (tokens == 0 || cols == 0 || rows == 0) return MX_OK;
   MX_REQUIRE(x && pos && out, MX_ERR_NULL);
   MX_REQUIRE(aligned16(x) && aligned16(pos) && aligned16(out) && aligned16(weights), MX_ERR_ALIGN);
-  const int64_t sz = size_of(dtype);
-  const hipStream_t st = as_stream(stream);
-  if (!weights) {
-    // the widest word that divides the rows and their strides
-    const int64_t all = cols * sz | ldx * sz | ldo * sz;
-    const int64_t word = all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
-    const int runs = (int)(cols * sz / word);
-    const dim3 grid(row_grid(tokens * runs));
-#define MX_COPY(U)                                                                            \
-  k_dispatch_copy<U><<<grid, 256, 0, st>>>(static_cast<const U*>(x), ldx * sz / word, pos,    \
-                                           tokens, (int)top_k, rows, runs,                    \
-                                           static_cast<U*>(out), ldo * sz / word)
-    if (word == 16) MX_COPY(uint4);
-    else if (word == 8) MX_COPY(uint2);
-    else if (word == 4) MX_COPY(uint32_t);
-    else MX_COPY(uint16_t);
-#undef MX_COPY
-    return launch_status();
-  }
-  const bool wide = cols % 8 == 0 && rows16(ldx, (int)sz) && rows16(ldo, (int)sz);
-  const int runs = (int)(wide ? cols / 8 : cols);
+  const int run = weights || dtype == MX_BF16 ? 8 : 4;
+  const int runs = (int)cdiv(cols, run);
   const dim3 grid(row_grid(tokens * runs));
-#define MX_DISPATCH(T, V)                                                                        \
-  k_dispatch_scaled<T, V><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, pos, tokens,      \
-                                                (int)top_k, rows, runs, weights,                 \
-                                                static_cast<T*>(out), ldo)
-  if (dtype == MX_F32) {
-    if (wide) MX_DISPATCH(float, 8);
-    else MX_DISPATCH(float, 1);
-  } else {
-    if (wide) MX_DISPATCH(uint16_t, 8);
-    else MX_DISPATCH(uint16_t, 1);
-  }
+  const hipStream_t st = as_stream(stream);
+#define MX_DISPATCH_WIDTH(T, NARROW)                                                          \
+  do {                                                                                       \
+    const T* xt = static_cast<const T*>(x);                                                  \
+    T* o = static_cast<T*>(out);                                                             \
+    if (weights)                                                                             \
+      k_dispatch_scaled<T, NARROW><<<grid, 256, 0, st>>>(xt, ldx, pos, tokens, (int)top_k, rows, \
+                                                       (int)cols, runs, weights, o, ldo);    \
+    else                                                                                     \
+      k_dispatch_copy<T, NARROW><<<grid, 256, 0, st>>>(xt, ldx, pos, tokens, (int)top_k, rows, \
+                                                     (int)cols, runs, o, ldo);               \
+  } while (0)
+#define MX_DISPATCH(T)                            \
+  do {                                             \
+    if (cols < run) MX_DISPATCH_WIDTH(T, true);    \
+    else MX_DISPATCH_WIDTH(T, false);              \
+  } while (0)
+  if (dtype == MX_F32) MX_DISPATCH(float);
+  else MX_DISPATCH(uint16_t);
 #undef MX_DISPATCH
+#undef MX_DISPATCH_WIDTH
   return launch_status();
 }
 
@@ -476,21 +518,15 @@ extern "C" int mx_moe_dispatch_quantize(const void* x, int dtype, int64_t ldx, c
   if (tokens == 0 || cols == 0 || rows == 0) return MX_OK;
   MX_REQUIRE(x && pos && codes && scales, MX_ERR_NULL);
   MX_REQUIRE(aligned16(x) && aligned16(pos) && aligned16(codes) && aligned16(scales), MX_ERR_ALIGN);
-  const bool wide = rows16(ldx, size_of(dtype));
   const int runs = (int)(cols / 8);
   const dim3 grid(row_grid(tokens * runs));
   const hipStream_t st = as_stream(stream);
-#define MX_DISPATCHQ(T, V)                                                                        \
-  k_dispatch_quant<T, V><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, pos, tokens,         \
-                                               (int)top_k, rows, runs,                             \
-                                               reinterpret_cast<uint32_t*>(codes), scales, scale_ld)
-  if (dtype == MX_F32) {
-    if (wide) MX_DISPATCHQ(float, 8);
-    else MX_DISPATCHQ(float, 1);
-  } else {
-    if (wide) MX_DISPATCHQ(uint16_t, 8);
-    else MX_DISPATCHQ(uint16_t, 1);
-  }
+#define MX_DISPATCHQ(T)                                                                        \
+  k_dispatch_quant<T><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, pos, tokens,         \
+                                            (int)top_k, rows, runs,                             \
+                                            reinterpret_cast<uint32_t*>(codes), scales, scale_ld)
+  if (dtype == MX_F32) MX_DISPATCHQ(float);
+  else MX_DISPATCHQ(uint16_t);
 #undef MX_DISPATCHQ
   return launch_status();
 }
@@ -505,18 +541,17 @@ extern "C" int mx_moe_combine(const void* z, int z_dtype, int64_t ldz, int64_t r
   MX_REQUIRE(pos && y, MX_ERR_NULL);
   if (rows) MX_REQUIRE(z, MX_ERR_NULL);  // no rows: y = 0, z is not read
   MX_REQUIRE(aligned16(z) && aligned16(pos) && aligned16(weights) && aligned16(y), MX_ERR_ALIGN);
-  const bool wide = cols % 8 == 0 && rows16(ldz, size_of(z_dtype)) && rows16(ldy, size_of(y_dtype));
-  const int runs = (int)(wide ? cols / 8 : cols);
+  const int runs = (int)cdiv(cols, 8);
   const dim3 grid(row_grid(tokens * runs));
   const hipStream_t st = as_stream(stream);
-#define MX_COMBINE(TZ, TY)                                                                       \
-  do {                                                                                           \
-    const TZ* zt = static_cast<const TZ*>(z);                                                    \
-    TY* yt = static_cast<TY*>(y);                                                                \
-    if (wide) k_combine<TZ, TY, 8><<<grid, 256, 0, st>>>(zt, ldz, rows, pos, weights, tokens,    \
-                                                         (int)top_k, runs, yt, ldy);             \
-    else k_combine<TZ, TY, 1><<<grid, 256, 0, st>>>(zt, ldz, rows, pos, weights, tokens,         \
-                                                    (int)top_k, runs, yt, ldy);                  \
+#define MX_COMBINE_WIDTH(TZ, TY, NARROW)                                                      \
+  k_combine<TZ, TY, NARROW><<<grid, 256, 0, st>>>(static_cast<const TZ*>(z), ldz, rows, pos, \
+                                                weights, tokens, (int)top_k, (int)cols, runs, \
+                                                static_cast<TY*>(y), ldy)
+#define MX_COMBINE(TZ, TY)                            \
+  do {                                                 \
+    if (cols < 8) MX_COMBINE_WIDTH(TZ, TY, true);      \
+    else MX_COMBINE_WIDTH(TZ, TY, false);              \
   } while (0)
   if (z_dtype == MX_F32) {
     if (y_dtype == MX_F32) MX_COMBINE(float, float);
@@ -526,6 +561,7 @@ extern "C" int mx_moe_combine(const void* z, int z_dtype, int64_t ldz, int64_t r
     else MX_COMBINE(uint16_t, uint16_t);
   }
 #undef MX_COMBINE
+#undef MX_COMBINE_WIDTH
   return launch_status();
 }
 
@@ -542,22 +578,21 @@ extern "C" int mx_moe_combine_bwd(const void* dy, int dy_dtype, int64_t lddy, co
   if (rows && cols) MX_REQUIRE(dy && z && dz, MX_ERR_NULL);
   MX_REQUIRE(aligned16(dy) && aligned16(z) && aligned16(pos) && aligned16(weights) &&
                  aligned16(dz) && aligned16(dweights), MX_ERR_ALIGN);
-  const bool wide = cols % 8 == 0 && rows16(lddy, size_of(dy_dtype)) &&
-                    rows16(ldz, size_of(z_dtype)) && rows16(lddz, size_of(dy_dtype));
-  const int runs = (int)(wide ? cols / 8 : cols);
+  const int runs = (int)cdiv(cols, 8);
   const dim3 grid((unsigned)hmin(tokens, (int64_t)device_cu_count() * 64));
+  // the workgroup whose last pass over the row leaves the fewest threads idle
+  int threads = 256;
+  for (int n = 192; n >= 64; n -= 64)
+    if (cdiv(runs, n) * n < cdiv(runs, threads) * threads) threads = n;
   const hipStream_t st = as_stream(stream);
-#define MX_COMBINE_BWD(TY, TZ)                                                                    \
-  do {                                                                                            \
-    const TY* g = static_cast<const TY*>(dy);                                                     \
-    const TZ* zt = static_cast<const TZ*>(z);                                                     \
-    TY* d = static_cast<TY*>(dz);                                                                 \
-    if (wide) k_combine_bwd<TY, TZ, 8><<<grid, 256, 0, st>>>(g, lddy, zt, ldz, rows, pos, weights, \
-                                                             tokens, (int)top_k, runs, d, lddz,   \
-                                                             dweights);                           \
-    else k_combine_bwd<TY, TZ, 1><<<grid, 256, 0, st>>>(g, lddy, zt, ldz, rows, pos, weights,     \
-                                                        tokens, (int)top_k, runs, d, lddz,        \
-                                                        dweights);                                \
+#define MX_COMBINE_BWD_WIDTH(TY, TZ, NARROW)                                                   \
+  k_combine_bwd<TY, TZ, NARROW><<<grid, threads, 0, st>>>(                                    \
+      static_cast<const TY*>(dy), lddy, static_cast<const TZ*>(z), ldz, rows, pos, weights,  \
+      tokens, (int)top_k, (int)cols, runs, static_cast<TY*>(dz), lddz, dweights)
+#define MX_COMBINE_BWD(TY, TZ)                            \
+  do {                                                     \
+    if (cols < 8) MX_COMBINE_BWD_WIDTH(TY, TZ, true);      \
+    else MX_COMBINE_BWD_WIDTH(TY, TZ, false);              \
   } while (0)
   if (dy_dtype == MX_F32) {
     if (z_dtype == MX_F32) MX_COMBINE_BWD(float, float);
@@ -567,5 +602,6 @@ extern "C" int mx_moe_combine_bwd(const void* dy, int dy_dtype, int64_t lddy, co
     else MX_COMBINE_BWD(uint16_t, uint16_t);
   }
 #undef MX_COMBINE_BWD
+#undef MX_COMBINE_BWD_WIDTH
   return launch_status();
 }
