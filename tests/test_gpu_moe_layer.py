@@ -1,0 +1,212 @@
+"""The routing operators and the products together, as a mixture-of-experts layer uses them:
+a training step (plan, quantizing dispatch, grouped product, combine and the way back through
+the gradients) and a decode step (plan, grouped few-row products, combine), the latter captured
+into HIP graphs and replayed with other inputs; streams other than the current one."""
+import numpy as np
+import pytest
+import torch
+
+from mxfp4_microscaling_quantization_amd import mx
+from tests.gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+T, TOP_K, E, H, F = 70, 3, 6, 96, 160
+
+
+def packed_experts(seed, N, K, std=0.05):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    w = torch.randn((E * N, K), generator=g, device=DEV) * std
+    c, s = mx.quantize(w)
+    return (c.reshape(E, N, -1), s.reshape(E, N, -1)), mx.dequantize(c, s, E * N, K).double().reshape(E, N, K)
+
+
+def batch(seed, tokens=T, padding=5):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((tokens, H), generator=g, device=DEV).to(torch.bfloat16)
+    p, ids = torch.softmax(torch.rand((tokens, E), generator=g, device=DEV), 1).topk(TOP_K, 1)
+    ids[tokens - padding:] = -1
+    return x, ids, p.contiguous()
+
+
+def test_training_step():
+    """y = combine(grouped product of the quantized rows); every part against float64 on the
+    operands that the step itself quantized."""
+    x, ids, p = batch(1)
+    (wc, ws), w64 = packed_experts(2, F, H)
+    offs, src, pos = mx.moe_plan(ids, E)
+    ends = offs.tolist()                                    # the grouped product takes host offsets
+    R, rows = ends[-1], pos.numel()
+    assert R == (T - 5) * TOP_K
+    xq = mx.moe_dispatch_quantize(x, pos)
+    z = torch.zeros((rows, F), device=DEV)
+    mx.mx_gemm_grouped(xq[0], xq[1], wc, ws, ends, E, F, H, 1.0, z)
+    y = mx.moe_combine(z, pos, p)
+
+    xr = mx.dequantize(*mx.quantize(x), T, H).double()
+    want_z = torch.zeros((rows, F), dtype=torch.float64, device=DEV)
+    for e in range(E):
+        tok = src[ends[e]:ends[e + 1]].long() // TOP_K
+        want_z[ends[e]:ends[e + 1]] = xr[tok] @ w64[e].T
+    want_y = torch.zeros((T, F), dtype=torch.float64, device=DEV)
+    for t, j in np.ndindex(T, TOP_K):
+        if pos[t, j] >= 0:
+            want_y[t] += p[t, j].double() * want_z[pos[t, j].long()]
+    # the product's own bound is 1e-5 of the magnitudes' sum; the combination adds (top_k + 1) 2^-24
+    mag = (xr.abs().amax() * w64.abs().amax() * H * TOP_K).item()
+    assert (y.double() - want_y).abs().max() <= (1e-5 + (TOP_K + 1) * 2.0 ** -24) * mag
+    assert torch.all(y[T - 5:] == 0)
+
+    dy = (torch.randn((T, F), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV) * 1e-2).to(torch.bfloat16)
+    dz, dp = mx.moe_combine_bwd(dy, z, pos, p, out=torch.zeros((rows, F), dtype=torch.bfloat16, device=DEV))
+    xq_rows = (xq[0][:R].contiguous(), xq[1][:R].contiguous())
+    dxr, dw = mx.grouped_linear_bwd(dz[:R], xq_rows, (wc.reshape(E * F, -1), ws.reshape(E * F, -1)), ends, F, H, 7)
+    dx = mx.moe_combine(dxr, pos)                           # the dispatch's gradient
+
+    want_dp = torch.zeros((T, TOP_K), dtype=torch.float64, device=DEV)
+    want_dx = torch.zeros((T, H), dtype=torch.float64, device=DEV)
+    mag_dp = torch.zeros_like(want_dp)
+    for t, j in np.ndindex(T, TOP_K):
+        r = int(pos[t, j])
+        if r >= 0:
+            terms = dy[t].double() * z[r].double()
+            want_dp[t, j], mag_dp[t, j] = terms.sum(), terms.abs().sum()
+            assert (dz[r].double() - p[t, j].double() * dy[t].double()).abs().max() <= \
+                (2.0 ** -8 + 2.0 ** -24) * (p[t, j] * dy[t].float().abs().max()).item()
+            want_dx[t] += dxr[r].double()
+    assert torch.all((dp - want_dp).abs() <= (F + 1) * 2.0 ** -24 * mag_dp)
+    assert (dx.double() - want_dx).abs().max() <= (TOP_K + 1) * 2.0 ** -24 * TOP_K * dxr.abs().max().item()
+    assert dw.shape == (E, F, H) and torch.isfinite(dw).all()
+
+
+class Decode:
+    """One mixture-of-experts block on unquantized activations: gated up-projection, down-projection."""
+
+    def __init__(self):
+        self.up, self.up64 = packed_experts(11, 2 * F, H)
+        self.down, self.down64 = packed_experts(12, H, F)
+
+    def run(self, x, ids, p):
+        offs, src, pos = mx.moe_plan(ids, E)
+        h = mx.gemv_grouped(x, self.up, offs, src, TOP_K)
+        a = torch.nn.functional.silu(h[:, :F]) * h[:, F:]
+        z = mx.gemv_grouped(a, self.down, offs)
+        return mx.moe_combine(z, pos, p)
+
+    def want(self, x, ids, p):
+        y = torch.zeros((len(x), H), dtype=torch.float64, device=DEV)
+        for t, j in np.ndindex(*ids.shape):
+            e = int(ids[t, j])
+            if 0 <= e < E:
+                h = self.up64[e] @ x[t].double()
+                a = torch.nn.functional.silu(h[:F]) * h[F:]
+                y[t] += p[t, j].double() * (self.down64[e] @ a)
+        return y
+
+
+def close(y, want):
+    """Two float32 products of lengths H and F, an activation and a combination: their roundings,
+    counted as chains of at most 64 + 3 K / 32 steps of 2^-23 of the terms, stay below 1e-4 of the
+    largest result for these sizes and distributions (terms' magnitudes are below 20 results)."""
+    assert (y.double() - want).abs().max() <= 1e-4 * want.abs().max()
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 17, 70])
+def test_decode_step(tokens):
+    block = Decode()
+    x, ids, p = batch(20 + tokens, tokens, padding=tokens // 10)
+    close(block.run(x, ids, p), block.want(x, ids, p))
+
+
+def test_decode_step_captured_and_replayed():
+    """Two graphs of different batches, replayed in turn with eager calls and new inputs between:
+    every replay equals the eager result on its inputs bit for bit."""
+    block = Decode()
+    graphs = []
+    side = torch.cuda.Stream()
+    for tokens in (3, 24):
+        static = [t.clone() for t in batch(30, tokens, padding=1)]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            block.run(*static)                              # warm up off the capture
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = block.run(*static)
+        graphs.append((g, static, y, tokens))
+    for seed in range(40, 44):
+        for g, static, y, tokens in graphs:
+            fresh = batch(seed, tokens, padding=seed % 3)
+            for a, b in zip(static, fresh):
+                a.copy_(b)
+            eager = block.run(*fresh)
+            torch.cuda.synchronize()
+            g.replay()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, eager)
+            close(y, block.want(*fresh))
+
+
+def test_plan_and_dense_product_with_workspaces_replayed():
+    """The calls that keep partial results in a workspace, captured with the same workspace."""
+    ids = torch.randint(-1, E, (3000, 2), device=DEV)
+    K, N = 8192, 200
+    wc = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)
+    ws = torch.randint(115, 128, (N, K // 32), dtype=torch.uint8, device=DEV)
+    x = torch.randn((20, K), device=DEV)
+    need = mx.mx_gemv_workspace_size(mx.MX_F32, 20, N, K), mx.mx_moe_plan_workspace_size(3000, 2, E)
+    assert min(need) > 0
+    work = torch.empty(max(need), dtype=torch.uint8, device=DEV)
+    run = lambda: (mx.gemv(x, (wc, ws), workspace=work), *mx.moe_plan(ids, E, workspace=work))  # noqa: E731
+    run()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run()
+    for seed in range(4):
+        torch.manual_seed(seed)
+        x.copy_(torch.randn_like(x))
+        ids.copy_(torch.randint(-1, E, ids.shape, device=DEV))
+        work.fill_(0xEE)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, run()):
+            assert torch.equal(a, b)
+
+
+def test_calls_on_another_stream():
+    """Outputs of a call on a given stream belong to that stream; the result is the same."""
+    block = Decode()
+    x, ids, p = batch(50)
+    want = block.run(x, ids, p)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (s, s.cuda_stream):
+        offs, src, pos = mx.moe_plan(ids, E, stream=stream)
+        h = mx.gemv_grouped(x, block.up, offs, src, TOP_K, stream=stream)
+        with torch.cuda.stream(s):
+            a = torch.nn.functional.silu(h[:, :F]) * h[:, F:]
+        z = mx.gemv_grouped(a, block.down, offs, stream=stream)
+        y = mx.moe_combine(z, pos, p, stream=stream)
+        s.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_cpu_tensors_are_refused():
+    pos = torch.zeros((2, 2), dtype=torch.int32)
+    with pytest.raises(ValueError, match="current device"):
+        mx.moe_combine(torch.zeros(4, 8), pos)
+    with pytest.raises(ValueError, match="current device"):
+        mx.moe_plan(torch.zeros((2, 2), dtype=torch.int64), 4)
+
+
+@pytest.mark.parametrize("x_type", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(200, 70, 64), (1100, 65, 2304), (513, 300, 96)])
+def test_gemv_of_many_rows(x_type, M, N, K):
+    """Row counts past one tile: each row equals the one-row call to the bound of two orders."""
+    x = torch.randn((M, K), generator=torch.Generator(device=DEV).manual_seed(M), device=DEV).to(x_type)
+    w = mx.quantize(torch.randn((N, K), generator=torch.Generator(device=DEV).manual_seed(N), device=DEV))
+    y = mx.gemv(x, w)
+    w64 = mx.dequantize(*w, N, K).double()
+    want, mag = x.double() @ w64.T, x.double().abs() @ w64.abs().T
+    assert torch.all((y - want).abs() <= (3 * K / 32 + 64) * 2.0 ** -23 * mag)
