@@ -162,13 +162,12 @@ struct GroupTiles {
 // rows (term p of row q in column 4 p + q): the terms' sums are added at the end.
 constexpr int kMaxWaves = 8, kGemvTile = 64;
 
-template <typename T, int MT, int S, bool GROUPED>
+template <typename T, int S, bool GROUPED>
 __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   constexpr int X = XTerms<T>::kTerms;
   constexpr int XW = 2 * sizeof(T);        // words of 8 values of x
-  constexpr int RT = X == 1 ? 16 : 4;      // rows of x in an MFMA's columns
-  constexpr int R = RT * MT;
-  constexpr int Q = MT == 1 && S <= 2 ? 4 : 2;  // subtiles in flight
+  constexpr int R = X == 1 ? 16 : 4;       // rows of x in an MFMA's columns
+  constexpr int Q = S <= 2 ? 4 : 2;        // subtiles in flight
   extern __shared__ uint4 s_stage[];       // [waves][4 rows][64 runs], then
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -180,8 +179,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   const T* const x = static_cast<const T*>(a.x);
   uint4* const stage = s_stage + 256 * wave;
   uint4* const s_scale = s_stage + 256 * waves;                            // [waves][64 rows] of 16 bytes
-  float* const s_part = reinterpret_cast<float*>(s_scale + 64 * waves);    // [waves][16 MT][ldp]
-  float* const part = s_part + wave * (16 * MT) * ldp;
+  float* const s_part = reinterpret_cast<float*>(s_scale + 64 * waves);    // [waves][16][ldp]
+  float* const part = s_part + wave * 16 * ldp;
 
   // this workgroup's run of tiles [t, t_end)
   GroupTiles<R> groups;
@@ -276,13 +275,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   // 64 runs of 8 values a row, and are read back by the lanes of their columns: block p's
   // run j.  Run 4 p + j lies at 4 p + (j ^ p / 4), which spreads the blocks over the banks.
   constexpr int kFours = R / 4;
-  v8bf xt[MT][S][4];
+  v8bf xt[S][4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xt[i][s][j] = v8bf{};
+    for (int j = 0; j < 4; ++j) xt[s][j] = v8bf{};
   uint32_t xv[4][XW];     // four rows on their way
   int row_of = 0;         // lane q: the row of x of the tile's row q
   uint64_t real = ~0ull;  // the tile's rows whose row of x exists
@@ -320,12 +317,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
           stage[64 * q + (lane ^ lane >> 4)] = XTerms<T>::take(xv[q]);
       wave_sync();
       if (k == X - 1 && four + 1 < kFours && 4 * four + 4 < cur.mrows) x_load(four + 1, b0, b1);
-      if (r16 >> 2 == (X == 1 ? four % 4 : k)) {
+      if (r16 >> 2 == (X == 1 ? four : k)) {
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            xt[4 * four / RT][s][j] = __builtin_bit_cast(v8bf, stage[64 * row + 16 * s + 4 * g + (j ^ s)]);
+            xt[s][j] = __builtin_bit_cast(v8bf, stage[64 * row + 16 * s + 4 * g + (j ^ s)]);
       }
     }
   };
@@ -372,28 +369,20 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
             v4f* const p = reinterpret_cast<v4f*>(part + r16 * ldp + 16 * (sub + q) + 4 * g);
-            v4f acc[MT][2];  // two chains of sums
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              acc[i][0] = acc[i][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-              if (round) acc[i][1] = p[4 * i * ldp];
-            }
+            v4f acc[2] = {};  // two chains of sums
+            if (round) acc[1] = *p;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint4 u = c[q][s];
                 const v8bf w = decode8_bf16(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, f[q][s]);
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                  acc[i][j & 1] =
-                      __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xt[i][s][j], acc[i][j & 1], 0, 0, 0);
+                acc[j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xt[s][j], acc[j & 1], 0, 0, 0);
               }
             }
             fetch(q);
             // lane 16 g + m holds weight rows 4 g .. 4 g + 3 of column m
-#pragma unroll
-            for (int i = 0; i < MT; ++i) p[4 * i * ldp] = acc[i][0] + acc[i][1];
+            *p = acc[0] + acc[1];
           }
         }
       }
@@ -404,12 +393,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
       if (n >= cur.ncols || !(real >> m & 1)) continue;
       float sum = 0.0f;
       if (nblk) {
-        const float* const p = s_part + (16 * (m / RT) + m % RT) * ldp + n;
+        const float* const p = s_part + m * ldp + n;
         float v[X][kMaxWaves];  // all reads in flight, then the sum in order
 #pragma unroll
         for (int k = 0; k < X; ++k)
 #pragma unroll
-          for (int w = 0; w < kMaxWaves; ++w) v[k][w] = p[(min(w, waves - 1) * (16 * MT) + 4 * k) * ldp];
+          for (int w = 0; w < kMaxWaves; ++w) v[k][w] = p[(min(w, waves - 1) * 16 + 4 * k) * ldp];
 #pragma unroll
         for (int k = X - 1; k >= 0; --k)
 #pragma unroll
@@ -447,37 +436,41 @@ __global__ __launch_bounds__(256) void k_gemv_sum(const float* __restrict__ part
   }
 }
 
-// How a product is cut: MFMA row tiles a workgroup holds, steps of a window, waves, blocks
-// of a wave's window, rounds of windows in one workgroup and slices over workgroups.
+// How a product is cut: steps of a window, waves, blocks of a wave's window, rounds of
+// windows in one workgroup and slices over workgroups.
 struct GemvPlan {
-  int mt, steps, waves, window, rounds, slices;
+  int steps, waves, window, rounds, slices;
 };
 
+static constexpr int rows_per_tile(int x_dtype) { return x_dtype == MX_BF16 ? 16 : 4; }
+
 static GemvPlan gemv_plan(int x_dtype, int64_t rows, int64_t N, int64_t K, bool grouped) {
-  const int rt = x_dtype == MX_BF16 ? 16 : 4, nblk = (int)(K / 32);
+  const int nblk = K ? (int)(K / 32) : 1;
   GemvPlan p;
-  p.mt = rows <= rt ? 1 : rows <= 2 * rt || rows > 3 * rt ? 2 : 3;
-  p.waves = (int)hmin(cdiv(nblk ? nblk : 1, 4), kMaxWaves);
-  const auto passes = [&](int steps) { return (int)cdiv(nblk ? nblk : 1, 4 * steps * p.waves); };
+  p.waves = (int)hmin(cdiv(nblk, 4), kMaxWaves);
+  const auto passes = [&](int steps) { return (int)cdiv(nblk, 4 * steps * p.waves); };
+  const int n = passes(4);
   p.steps = 1;
-  while (p.steps < (p.mt == 1 ? 4 : 2) && passes(p.steps) > passes(p.mt == 1 ? 4 : 2)) ++p.steps;
-  const int n = passes(p.steps);
-  // A contraction longer than a workgroup's windows goes in rounds, which fetch x again for
-  // every tile, or in slices over workgroups and one more launch for their sums.  Slices pay
-  // where x is many rows or the tiles are few: 40 rows of 8192 x 8192 25.9 us (rounds: 42.9),
-  // 8 rows of 4096 x 14336 18.2 us (23.8), but one row of 8192 x 8192 17.7 us (13.6).
-  const bool slice = !grouped && n > 1 &&
-                     (p.mt > 1 ? rows <= 1024 : cdiv(N, kGemvTile) * cdiv(rows, rt) <= 64);
+  while (passes(p.steps) > n) ++p.steps;
+  // A contraction longer than a workgroup's windows goes in n rounds, which fetch x again
+  // for every tile, or in n slices over workgroups and one more launch for their sums.
+  // Slices pay where x is many rows or the tiles leave compute units idle.  Sliced and in
+  // rounds, us: bf16 8192 x 8192 (n = 2) one row 14.1 and 11.3, 8 rows 14.4 and 14.6, 16
+  // rows 15.1 and 18.5; 14336 x 14336 (n = 4) 8 rows 31.9 and 30.0, 40 rows 73.7 and 91.4;
+  // one row of 4096 x 14336 (64 tiles) 13.9 and 18.8; float32 14336 x 14336 2 rows 30.5 and
+  // 29.1, 4 rows 32.7 and 35.1.
+  const bool slice = !grouped && n > 1 && rows <= 1024 &&
+                     (rows > rows_per_tile(x_dtype) / 2 || (n > 2 && cdiv(N, kGemvTile) <= 64));
   p.rounds = slice ? 1 : n;
   p.slices = slice ? n : 1;
-  p.window = (int)cdiv(cdiv(nblk ? nblk : 1, (int64_t)n * p.waves), 4) * 4;
+  p.window = (int)cdiv(cdiv(nblk, (int64_t)n * p.waves), 4) * 4;
   return p;
 }
 
-template <typename T, int MT, int S, bool GROUPED>
+template <typename T, int S, bool GROUPED>
 static int gemv_launch(GemvArgs a, const GemvPlan& p, int64_t groups, hipStream_t st) {
-  constexpr int R = (sizeof(T) == 2 ? 16 : 4) * MT;
-  constexpr int kBytes = 5120 + 16 * MT * (kGemvTile + 4) * 4;  // LDS of a wave
+  constexpr int R = rows_per_tile(sizeof(T) == 2 ? MX_BF16 : MX_F32);
+  constexpr int kBytes = 5120 + 16 * (kGemvTile + 4) * 4;  // LDS of a wave
   static_assert(kMaxWaves * kBytes <= 160 * 1024, "the sums of all waves fit LDS");
   a.ntiles = cdiv(a.N, kGemvTile);
   a.window = p.window;
@@ -486,7 +479,7 @@ static int gemv_launch(GemvArgs a, const GemvPlan& p, int64_t groups, hipStream_
   // a group adds less than one row tile to the rows'
   const int64_t row_tiles = GROUPED ? cdiv(a.M, R) + groups : cdiv(a.M, R);
   const unsigned grid = (unsigned)hmin(row_tiles * p.slices * a.ntiles, device_cu_count());
-  k_gemv<T, MT, S, GROUPED><<<grid, 64 * p.waves, (size_t)p.waves * kBytes, st>>>(a);
+  k_gemv<T, S, GROUPED><<<grid, 64 * p.waves, (size_t)p.waves * kBytes, st>>>(a);
   if (p.slices > 1)
     k_gemv_sum<<<(unsigned)hmin(cdiv(a.M * a.N, 256), 4096), 256, 0, st>>>(
         a.partial, p.slices, a.M, a.N, a.alpha, a.y, a.y_bf16, a.ldy);
@@ -494,19 +487,17 @@ static int gemv_launch(GemvArgs a, const GemvPlan& p, int64_t groups, hipStream_
 }
 
 template <typename T, bool GROUPED>
-static int gemv_rows(const GemvArgs& a, const GemvPlan& p, int64_t groups, hipStream_t st) {
-  if (p.mt == 2) return gemv_launch<T, 2, 2, GROUPED>(a, p, groups, st);
-  if (p.mt == 3) return gemv_launch<T, 3, 2, GROUPED>(a, p, groups, st);
-  if (p.steps == 1) return gemv_launch<T, 1, 1, GROUPED>(a, p, groups, st);
-  if (p.steps == 2) return gemv_launch<T, 1, 2, GROUPED>(a, p, groups, st);
-  if (p.steps == 3) return gemv_launch<T, 1, 3, GROUPED>(a, p, groups, st);
-  return gemv_launch<T, 1, 4, GROUPED>(a, p, groups, st);
+static int gemv_steps(const GemvArgs& a, const GemvPlan& p, int64_t groups, hipStream_t st) {
+  if (p.steps == 1) return gemv_launch<T, 1, GROUPED>(a, p, groups, st);
+  if (p.steps == 2) return gemv_launch<T, 2, GROUPED>(a, p, groups, st);
+  if (p.steps == 3) return gemv_launch<T, 3, GROUPED>(a, p, groups, st);
+  return gemv_launch<T, 4, GROUPED>(a, p, groups, st);
 }
 
 template <bool GROUPED>
 static int gemv_any(const GemvArgs& a, const GemvPlan& p, int x_dtype, int64_t groups, hipStream_t st) {
-  return x_dtype == MX_BF16 ? gemv_rows<uint16_t, GROUPED>(a, p, groups, st)
-                            : gemv_rows<float, GROUPED>(a, p, groups, st);
+  return x_dtype == MX_BF16 ? gemv_steps<uint16_t, GROUPED>(a, p, groups, st)
+                            : gemv_steps<float, GROUPED>(a, p, groups, st);
 }
 
 static int gemv_check(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_codes,
