@@ -179,8 +179,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   const T* const x = static_cast<const T*>(a.x);
   uint4* const stage = s_stage + 256 * wave;
   uint4* const s_scale = s_stage + 256 * waves;                            // [waves][64 rows] of 16 bytes
-  float* const s_part = reinterpret_cast<float*>(s_scale + 64 * waves);    // [waves][16][ldp]
-  float* const part = s_part + wave * 16 * ldp;
+  float* const s_part = reinterpret_cast<float*>(s_scale + 64 * waves);    // [2][waves][16][ldp]
+  int turn = 0;  // the sums of consecutive tiles alternate: one barrier a tile
 
   // this workgroup's run of tiles [t, t_end)
   GroupTiles<R> groups;
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
             }
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
-            v4f* const p = reinterpret_cast<v4f*>(part + r16 * ldp + 16 * (sub + q) + 4 * g);
+            v4f* const p = reinterpret_cast<v4f*>(s_part + ((turn * waves + wave) * 16 + r16) * ldp + 16 * (sub + q) + 4 * g);
             v4f acc[2] = {};  // two chains of sums
             if (round) acc[1] = *p;
 #pragma unroll
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
       if (n >= cur.ncols || !(real >> m & 1)) continue;
       float sum = 0.0f;
       if (nblk) {
-        const float* const p = s_part + m * ldp + n;
+        const float* const p = s_part + (turn * waves * 16 + m) * ldp + n;
         float v[X][kMaxWaves];  // all reads in flight, then the sum in order
 #pragma unroll
         for (int k = 0; k < X; ++k)
@@ -415,7 +415,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
       else static_cast<float*>(a.y)[at] = sum;
     }
     if (++t == t_end) break;
-    lds_barrier();
+    turn ^= 1;
     const int grp = cur.grp, m0 = cur.m0, ks = cur.ks;
     step_tile(cur);
     fresh = cur.m0 != m0 || cur.grp != grp || cur.ks != ks;
@@ -470,7 +470,7 @@ static GemvPlan gemv_plan(int x_dtype, int64_t rows, int64_t N, int64_t K, bool 
 template <typename T, int S, bool GROUPED>
 static int gemv_launch(GemvArgs a, const GemvPlan& p, int64_t groups, hipStream_t st) {
   constexpr int R = rows_per_tile(sizeof(T) == 2 ? MX_BF16 : MX_F32);
-  constexpr int kBytes = 5120 + 16 * (kGemvTile + 4) * 4;  // LDS of a wave
+  constexpr int kBytes = 5120 + 2 * 16 * (kGemvTile + 4) * 4;  // LDS of a wave
   static_assert(kMaxWaves * kBytes <= 160 * 1024, "the sums of all waves fit LDS");
   a.ntiles = cdiv(a.N, kGemvTile);
   a.window = p.window;
