@@ -44,7 +44,9 @@
  *    synchronizes; it keeps no state between calls, so every entry point is
  *    reentrant.  Work is enqueued on `stream` (a hipStream_t; NULL = default
  *    stream) and the call returns before it runs.
- *  - Input and output buffers must not overlap unless stated.
+ *  - Input and output buffers must not overlap unless stated.  A workspace is in use
+ *    until the call's work has run: calls that share one must be ordered (one stream,
+ *    or captured graphs that are never replayed at the same time).
  *
  * Errors
  *  - Every entry point returns an mx_status.  Arguments are validated before
@@ -384,15 +386,15 @@ int mx_grouped_linear_bwd(const void* dy, int dtype, const int64_t* offs, int64_
  * weight [N, K] (w_codes [N][K/2]; scale rows w_scale_ld >= K/32 bytes apart, as
  * mx_quantize_ld writes them): the product of a layer whose weights stay packed
  * while a few tokens are decoded.  y (y_dtype) has rows ldy >= N elements apart.
- * Any M, N >= 0 below 2^31 (M or N == 0: no-op), K % 32 == 0 and K, w_scale_ld
- * below 2^26 (K == 0:
- * y = 0, x and the weights may be NULL); the weights are read once per 64 rows, so
- * many rows cost as many passes.  x is used to its full precision (a float32 x down to bits
- * of 2^-133): products are exact, sums are float32 in a fixed order, and one
- * rounding to nearest even gives a bf16 y.  A weight block with scale byte 0xFF makes
- * its sums NaN; deq(W) is +-Inf where it passes the float32 range (bytes 253 and 254,
- * which no quantizer writes).  workspace: at least mx_gemv_workspace_size bytes (the
- * partial sums of a long contraction; 0: may be NULL), 16-byte aligned. */
+ * Any M, N >= 0 below 2^31 (M or N == 0: no-op), K % 32 == 0, K and w_scale_ld
+ * below 2^26 (K == 0: y = 0, x and the weights may be NULL).  The weights are read
+ * once per 16 rows of a bf16 x and per 4 of a float32 x.  x is used to its full
+ * precision (a float32 x down to bits of 2^-133): products are exact, sums are float32
+ * in a fixed order, and one rounding to nearest even gives a bf16 y.  A weight block
+ * with scale byte 0xFF makes its sums NaN; sums over values past the float32 range
+ * (scale bytes 253 and 254, which no quantizer writes) are not finite.  workspace: at
+ * least mx_gemv_workspace_size bytes (the partial sums of a long contraction; 0: may be
+ * NULL), 16-byte aligned. */
 size_t mx_gemv_workspace_size(int x_dtype, int64_t M, int64_t N, int64_t K);
 int mx_gemv(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_codes,
             const uint8_t* w_scales, int64_t w_scale_ld, int64_t M, int64_t N, int64_t K,

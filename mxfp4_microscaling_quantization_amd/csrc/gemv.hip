@@ -562,9 +562,8 @@ extern "C" int mx_gemv_grouped(const void* x, int x_dtype, int64_t ldx, int64_t 
   if (rows == 0 || N == 0 || x_rows == 0) return MX_OK;
   MX_REQUIRE(offs, MX_ERR_NULL);
   MX_REQUIRE(aligned16(offs) && aligned16(src), MX_ERR_ALIGN);
-  // at most `rows` groups hold rows; their average count picks the row tile
-  const int64_t held = hmin(groups, rows);
-  const GemvPlan p = gemv_plan(x_dtype, cdiv(rows, held), N, K, true);
+  const int64_t held = hmin(groups, rows);  // at most `rows` groups hold rows
+  const GemvPlan p = gemv_plan(x_dtype, rows, N, K, true);
   GemvArgs a = {};
   a.x = x; a.ldx = ldx; a.x_rows = (int)x_rows; a.src = src; a.top_k = (int)top_k;
   a.M = (int)rows; a.N = N; a.K = (int)K; a.offs = offs; a.groups = (int)groups;

@@ -544,23 +544,30 @@ def _row_ld(t: torch.Tensor, what: str) -> int:
     return ld
 
 
-def _empty(shape, dtype, like, stream, inputs=()):
-    """An output of the current device, allocated on the stream the call runs on; the
-    inputs are kept from reuse until that stream is done with them."""
+def _torch_stream(stream):
+    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+
+
+def _empty(shape, dtype, like, stream):
+    """A tensor of the current device, allocated on the stream the call runs on."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    for t in inputs:
-        if t is not None:
-            t.record_stream(stream)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream)):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _output(out, shape, dtype, like, stream, inputs):
+def _keep(stream, *tensors) -> None:
+    """Keeps the memory of tensors from reuse until the given stream is done with them."""
+    if stream is not None:
+        stream = _torch_stream(stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _output(out, shape, dtype, like, stream):
     if out is None:
-        return _empty(shape, dtype, like, stream, inputs)
+        return _empty(shape, dtype, like, stream)
     if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"out must be {tuple(shape)} {dtype}, not {tuple(out.shape)} {out.dtype}")
     return out
@@ -597,7 +604,8 @@ def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, works
     xt, ldx = dtype_code(x), _row_ld(x, "x")
     if out is not None:
         out_dtype = out.dtype
-    y = _output(out, (M, N), out_dtype, x, stream, (x, codes, scales))
+    y = _output(out, (M, N), out_dtype, x, stream)
+    _keep(stream, x, codes, scales, out, workspace)
     workspace = _workspace(workspace, mx_gemv_workspace_size(xt, M, N, K), x, stream)
     mx_gemv(x, xt, ldx, codes, scales, scales.shape[1], M, N, K, alpha, y, dtype_code(y),
             _row_ld(y, "out"), workspace, _nbytes(workspace), stream)
@@ -625,7 +633,8 @@ def gemv_grouped(x: torch.Tensor, w, offs, src=None, top_k=1, alpha=1.0, out=Non
     rows = xr if src is None else src.numel()
     if out is not None:
         out_dtype = out.dtype
-    y = _output(out, (rows, N), out_dtype, x, stream, (x, codes, scales, offs, src))
+    y = _output(out, (rows, N), out_dtype, x, stream)
+    _keep(stream, x, codes, scales, offs, src, out)
     mx_gemv_grouped(x, dtype_code(x), _row_ld(x, "x"), xr, src, top_k, codes, scales, scales.shape[2],
                     offs, groups, rows, N, K, alpha, y, dtype_code(y), _row_ld(y, "out"), stream)
     return y
@@ -641,8 +650,9 @@ def moe_plan(ids: torch.Tensor, experts: int, workspace=None, stream=None):
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
     _on_current_device(ids, workspace)
+    _keep(stream, ids, workspace)
     workspace = _workspace(workspace, mx_moe_plan_workspace_size(tokens, top_k, experts), ids, stream)
-    offs = _empty((experts + 1,), torch.int64, ids, stream, (ids, workspace))
+    offs = _empty((experts + 1,), torch.int64, ids, stream)
     src = _empty((tokens * top_k,), torch.int32, ids, stream)
     pos = _empty((tokens, top_k), torch.int32, ids, stream)
     mx_moe_plan(ids, MX_I64 if wide else MX_I32, tokens, top_k, experts, offs, src, pos, workspace,
@@ -669,7 +679,8 @@ def moe_dispatch(x: torch.Tensor, pos, weights=None, rows=None, out=None, stream
     top_k = _routing(pos, weights, tokens)
     _on_current_device(x, pos, weights, out)
     rows = out.shape[0] if out is not None else pos.numel() if rows is None else rows
-    o = _output(out, (rows, cols), x.dtype, x, stream, (x, pos, weights))
+    o = _output(out, (rows, cols), x.dtype, x, stream)
+    _keep(stream, x, pos, weights, out)
     mx_moe_dispatch(x, dtype_code(x), _row_ld(x, "x"), pos, weights, tokens, top_k, rows, cols, o,
                     _row_ld(o, "out"), stream)
     return o
@@ -682,7 +693,7 @@ def moe_dispatch_quantize(x: torch.Tensor, pos, rows=None, out=None, stream=None
     top_k = _routing(pos, None, tokens)
     if out is None:
         rows = pos.numel() if rows is None else rows
-        out = (_empty((rows, cols // 2), torch.uint8, x, stream, (x, pos)),
+        out = (_empty((rows, cols // 2), torch.uint8, x, stream),
                _empty((rows, cols // 32), torch.uint8, x, stream))
     codes, scales = out
     rows = codes.shape[0]
@@ -691,6 +702,7 @@ def moe_dispatch_quantize(x: torch.Tensor, pos, rows=None, out=None, stream=None
             or scales.dim() != 2 or scales.shape[0] != rows):
         raise ValueError("out must be packed uint8 codes and scales")
     _on_current_device(x, pos, codes, scales)
+    _keep(stream, x, pos, codes, scales)
     mx_moe_dispatch_quantize(x, dtype_code(x), _row_ld(x, "x"), pos, tokens, top_k, rows, cols, codes,
                              scales, scales.shape[1], stream)
     return codes, scales
@@ -705,7 +717,8 @@ def moe_combine(z: torch.Tensor, pos, weights=None, out=None, out_dtype=torch.fl
     _on_current_device(z, pos, weights, out)
     if out is not None:
         out_dtype = out.dtype
-    y = _output(out, (tokens, cols), out_dtype, z, stream, (z, pos, weights))
+    y = _output(out, (tokens, cols), out_dtype, z, stream)
+    _keep(stream, z, pos, weights, out)
     mx_moe_combine(z, dtype_code(z), _row_ld(z, "z"), rows, pos, weights, tokens, top_k, cols, y,
                    dtype_code(y), _row_ld(y, "out"), stream)
     return y
@@ -720,7 +733,8 @@ def moe_combine_bwd(dy: torch.Tensor, z: torch.Tensor, pos, weights=None, out=No
     if z.dim() != 2 or z.shape[1] != cols:
         raise ValueError("z and dy must have the same columns")
     _on_current_device(dy, z, pos, weights, out)
-    dz = _output(out, (rows, cols), dy.dtype, dy, stream, (dy, z, pos, weights))
+    dz = _output(out, (rows, cols), dy.dtype, dy, stream)
+    _keep(stream, dy, z, pos, weights, out)
     dw = _empty((tokens, top_k), torch.float32, dy, stream)
     mx_moe_combine_bwd(dy, dtype_code(dy), _row_ld(dy, "dy"), z, dtype_code(z), _row_ld(z, "z"), rows,
                        pos, weights, tokens, top_k, cols, dz, _row_ld(dz, "out"), dw, stream)
