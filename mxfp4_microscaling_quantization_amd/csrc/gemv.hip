@@ -125,7 +125,7 @@ struct GroupTiles {
     for (int h = 0; h < 2; ++h) {
       lo[h] = (int)max<int64_t>(min<int64_t>(o[h][0], rows), 0);
       hi[h] = (int)max<int64_t>(min<int64_t>(o[h][1], rows), 0);
-      int n = 64 * h + lane < groups && hi[h] > lo[h] ? (hi[h] - lo[h] + R - 1) / R : 0;
+      int n = 64 * h + lane < groups && hi[h] > lo[h] ? (hi[h] - lo[h] - 1) / R + 1 : 0;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const int up = __shfl_up(n, d);
@@ -144,7 +144,7 @@ struct GroupTiles {
     const int first = __builtin_amdgcn_readlane(h ? lo[1] : lo[0], l);
     const int last = __builtin_amdgcn_readlane(h ? hi[1] : hi[0], l);
     const int tiles = __builtin_amdgcn_readlane(h ? end[1] : end[0], l);
-    m0 = first + (v - (tiles - (last - first + R - 1) / R)) * R;
+    m0 = first + (v - (tiles - ((last - first - 1) / R + 1))) * R;
     mrows = min(R, last - m0);
     return 64 * h + l;
   }
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
 
   // this workgroup's run of tiles [t, t_end)
   GroupTiles<R> groups;
-  int64_t row_tiles = (a.M + R - 1) / R;
+  int64_t row_tiles = ((int64_t)a.M + R - 1) / R;
   if constexpr (GROUPED) {
     groups.load(a.offs, a.groups, a.M);
     row_tiles = groups.total();

@@ -164,6 +164,20 @@ def test_gemv_weights_past_two_to_the_31_bytes():
     assert int((y != 0).sum()) == 4
 
 
+def test_gemv_of_the_most_rows():
+    """2^31 - 1 rows, dense and of one expert, with nothing to sum: y is 0 in every row."""
+    M = 2**31 - 1
+    x = torch.empty((M, 0), dtype=torch.bfloat16, device=DEV)
+    codes = torch.empty((1, 1, 0), dtype=torch.uint8, device=DEV)
+    y = torch.ones((M, 1), dtype=torch.bfloat16, device=DEV)
+    mx.gemv(x, (codes[0], codes[0]), out=y)
+    assert torch.equal(y.amax(), y.amin()) and float(y[0]) == 0
+    y.fill_(1)
+    offs = torch.tensor([0, M], device=DEV)
+    mx.gemv_grouped(x, (codes, codes), offs, out=y)
+    assert torch.equal(y.amax(), y.amin()) and float(y[0]) == 0
+
+
 # ------------------------------------------------------------------ grouped
 @pytest.mark.parametrize("x_type", ["f32", "bf16"])
 @pytest.mark.parametrize("tokens,top_k,experts,N,K,left_out", [
