@@ -599,6 +599,8 @@ def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, works
     codes, scales = w
     M, K = x.shape
     _check_packed(codes, scales, K)
+    if codes.dim() != 2:
+        raise ValueError("one packed weight has codes [N, K/2] and scales [N, >= K/32]")
     N = codes.shape[0]
     _on_current_device(x, codes, scales, out, workspace)
     xt, ldx = dtype_code(x), _row_ld(x, "x")

@@ -135,6 +135,8 @@ def test_conveniences_refuse_what_the_library_cannot_see():
         mx.gemv(x, (w[0], u8(4, 2)))
     with pytest.raises(ValueError, match="contiguous"):
         mx.gemv(x, (w[0], u8(2, 5).t()))
+    with pytest.raises(ValueError, match="one packed weight"):
+        mx.gemv(x, (u8(3, 5, 32), u8(3, 5, 2)))
     offs = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="offs must be int64"):
         mx.gemv_grouped(x, (w[0][None], w[1][None]), offs)
