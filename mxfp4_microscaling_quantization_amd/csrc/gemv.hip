@@ -444,6 +444,8 @@ struct GemvPlan {
 
 static constexpr int rows_per_tile(int x_dtype) { return x_dtype == MX_BF16 ? 16 : 4; }
 
+constexpr int64_t kMaxPartial = (int64_t)1 << 26;  // floats of the slices' sums
+
 static GemvPlan gemv_plan(int x_dtype, int64_t rows, int64_t N, int64_t K, bool grouped) {
   const int nblk = K ? (int)(K / 32) : 1;
   GemvPlan p;
@@ -458,8 +460,9 @@ static GemvPlan gemv_plan(int x_dtype, int64_t rows, int64_t N, int64_t K, bool 
   // rounds, us: bf16 8192 x 8192 (n = 2) one row 14.1 and 11.3, 8 rows 14.4 and 14.6, 16
   // rows 15.1 and 18.5; 14336 x 14336 (n = 4) 8 rows 31.9 and 30.0, 40 rows 73.7 and 91.4;
   // one row of 4096 x 14336 (64 tiles) 13.9 and 18.8; float32 14336 x 14336 2 rows 30.5 and
-  // 29.1, 4 rows 32.7 and 35.1.
-  const bool slice = !grouped && n > 1 && rows <= 1024 &&
+  // 29.1, 4 rows 32.7 and 35.1; bf16 4096 x 14336 64 rows 32.6 and 34.8, 2048 rows 654 and
+  // 854.  The sums take at most 256 MiB: past that it is rounds, for the workspace's sake.
+  const bool slice = !grouped && n > 1 && rows * N <= kMaxPartial / n &&
                      (rows > rows_per_tile(x_dtype) / 2 || (n > 2 && cdiv(N, kGemvTile) <= 64));
   p.rounds = slice ? 1 : n;
   p.slices = slice ? n : 1;

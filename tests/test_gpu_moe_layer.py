@@ -201,7 +201,8 @@ def test_cpu_tensors_are_refused():
 
 
 @pytest.mark.parametrize("x_type", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("M,N,K", [(200, 70, 64), (1100, 65, 2304), (513, 300, 96)])
+@pytest.mark.parametrize("M,N,K", [(200, 70, 64), (1100, 65, 2304), (513, 300, 96), (1100, 65, 4128),
+                                   (4200, 8003, 4128)])  # sums of slices past what a workspace holds
 def test_gemv_of_many_rows(x_type, M, N, K):
     """Row counts past one tile: each row equals the one-row call to the bound of two orders."""
     x = torch.randn((M, K), generator=torch.Generator(device=DEV).manual_seed(M), device=DEV).to(x_type)
