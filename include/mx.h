@@ -394,8 +394,7 @@ int mx_grouped_linear_bwd(const void* dy, int dtype, const int64_t* offs, int64_
  * with scale byte 0xFF makes its sums NaN; sums over values past the float32 range
  * (scale bytes 253 and 254, which no quantizer writes) are not finite.  workspace: at
  * least mx_gemv_workspace_size bytes (the partial sums of a long contraction, up to
- *  256 MiB; 0: may be
- * NULL), 16-byte aligned. */
+ * 256 MiB; 0: may be NULL), 16-byte aligned. */
 size_t mx_gemv_workspace_size(int x_dtype, int64_t M, int64_t N, int64_t K);
 int mx_gemv(const void* x, int x_dtype, int64_t ldx, const uint8_t* w_codes,
             const uint8_t* w_scales, int64_t w_scale_ld, int64_t M, int64_t N, int64_t K,
