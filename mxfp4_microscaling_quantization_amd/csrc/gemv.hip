@@ -150,6 +150,19 @@ struct GroupTiles {
   }
 };
 
+// Measured (one launch): one bf16 row of 14336 x 4096, 31 MB of weights, 8.3 us (3.8 TB/s,
+// its start and end in it); 61 tokens x 4 of 32 experts 5760 x 2880, 285 MB, 62.5 us (4.6
+// TB/s); 16 float32 tokens x 4 of 32, 2880 x 2880, 32.5 us; 47 bf16 rows of 4096 x 14336
+// 26.6 us.  Of the 61 tokens' time the loads alone take 53 us and the rest alone 44 us; the
+// 47 rows are bound by the rest (25 us), each of their three row tiles decoding the weights.
+//
+// One workgroup per compute unit: two of them, with smaller windows, took 68 us for the 61
+// tokens where one takes 63, and several row tiles per workgroup, decoded once, 36 us for the
+// 47 rows where one each takes 30 (more x to stage, registers for it, fewer loads ahead).
+// The alternative of x in LDS and whole rows of weights per wave, without sums across
+// waves, computes faster but reads 64-byte pieces of 128 rows at once: 73 us for the 61
+// tokens.
+//
 // A tile is kGemvTile columns of y (weight rows) for up to R rows of x; a workgroup takes a
 // run of consecutive tiles, column tiles first, so that it keeps its rows of x while the
 // group and row tile stay.  Its waves split the contraction into windows of up to 4 S
@@ -167,7 +180,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   constexpr int X = XTerms<T>::kTerms;
   constexpr int XW = 2 * sizeof(T);        // words of 8 values of x
   constexpr int R = X == 1 ? 16 : 4;       // rows of x in an MFMA's columns
-  constexpr int Q = S <= 2 ? 4 : 2;        // subtiles in flight
+  constexpr int Q = S <= 2 ? 4 : 2;        // subtiles in flight (61 tokens, S = 3: 4 took 66.7 us, 2 63.4)
   extern __shared__ uint4 s_stage[];       // [waves][4 rows][64 runs], then
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -178,8 +191,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   const uint32_t kbytes = a.K / 2;
   const T* const x = static_cast<const T*>(a.x);
   uint4* const stage = s_stage + 256 * wave;
-  uint4* const s_scale = s_stage + 256 * waves;                            // [waves][64 rows] of 16 bytes
-  float* const s_part = reinterpret_cast<float*>(s_scale + 64 * waves);    // [2][waves][16][ldp]
+  uint4* const s_scale = s_stage + 256 * waves;                          // [waves][64 rows] of 16 bytes
+  float* const s_part = reinterpret_cast<float*>(s_scale + 64 * waves);  // [2][waves][16][ldp]
   int turn = 0;  // the sums of consecutive tiles alternate: one barrier a tile
 
   // this workgroup's run of tiles [t, t_end)
@@ -233,13 +246,16 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   const auto stream = [&]() {
     const int64_t row = (GROUPED ? ahead.grp * a.N : 0) + (int64_t)ahead.nt * tile_n;
     codes = a.codes + row * kbytes;
-    const int b0 = ((ahead.ks * rounds + round_ahead) * waves + wave) * a.window, b1 = min(b0 + a.window, nblk);
+    const int b0 = ((ahead.ks * rounds + round_ahead) * waves + wave) * a.window;
+    const int b1 = min(b0 + a.window, nblk);
     c_at = min(r16, ahead.ncols - 1) * kbytes;
     c_end = (ahead.ncols - 1) * kbytes;
 #pragma unroll
     for (int s = 0; s < S; ++s) b_at[s] = (b0 + 4 * s + g < b1 ? b0 + 4 * s + g : 0) * 16;
     // The window's scale bytes of the tile's rows, a row a lane (at most 64): 16 bytes at
-    // any alignment, byte by byte where the array ends within them.
+    // any alignment, byte by byte where the array ends within them.  Loaded with the codes,
+    // a byte a lane, they touch as many cache lines as those: a kernel that only reads 265 MB
+    // of weights took 70 us that way and 46 us without.
     const int64_t at = (row + min(lane, ahead.ncols - 1)) * a.scale_ld + b0;
     if (at + 16 <= a.scale_end) {
       __builtin_memcpy(&scale16, a.scales + at, 16);
@@ -251,7 +267,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
         w[0] |= i < 8 ? byte : 0;
         w[1] |= i < 8 ? 0 : byte;
       }
-      scale16 = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
+      scale16 = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1],
+                           (uint32_t)(w[1] >> 32));
     }
   };
   uint4 c[Q][S];
@@ -267,7 +284,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
     }
     ++sub_ahead;
 #pragma unroll
-    for (int s = 0; s < S; ++s) c[q][s] = *reinterpret_cast<const uint4*>(codes + (c_at + b_at[s]));
+    for (int s = 0; s < S; ++s)  // kept in the caches (non-temporal: 80 us for 63)
+      c[q][s] = *reinterpret_cast<const uint4*>(codes + (c_at + b_at[s]));
     c_at = min(c_at + 16 * kbytes, c_end);
   };
 
@@ -339,7 +357,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   bool fresh = true;
   for (int64_t t = t0;;) {
     for (int round = 0; round < rounds; ++round) {
-      const int b0 = ((cur.ks * rounds + round) * waves + wave) * a.window, b1 = min(b0 + a.window, nblk);
+      const int b0 = ((cur.ks * rounds + round) * waves + wave) * a.window;
+      const int b1 = min(b0 + a.window, nblk);
       if (fresh || rounds > 1) {
         if (t > t0 || round > 0) {
           x_rows();
@@ -368,7 +387,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
             }
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
-            v4f* const p = reinterpret_cast<v4f*>(s_part + ((turn * waves + wave) * 16 + r16) * ldp + 16 * (sub + q) + 4 * g);
+            v4f* const p = reinterpret_cast<v4f*>(s_part + ((turn * waves + wave) * 16 + r16) * ldp +
+                                                  16 * (sub + q) + 4 * g);
             v4f acc[2] = {};  // two chains of sums
             if (round) acc[1] = *p;
 #pragma unroll
@@ -376,8 +396,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint4 u = c[q][s];
-                const v8bf w = decode8_bf16(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, f[q][s]);
-                acc[j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xt[s][j], acc[j & 1], 0, 0, 0);
+                const uint32_t eight = j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w;
+                acc[j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    decode8_bf16(eight, f[q][s]), xt[s][j], acc[j & 1], 0, 0, 0);
               }
             }
             fetch(q);
@@ -422,7 +443,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
   }
 }
 
-// y = alpha times the slices' sums, added in slice order.
+// y = alpha times the slices' sums, added in slice order.  Latency bound: 4.1 us for 47
+// rows of 4096 in four slices (3.9 MB).
 __global__ __launch_bounds__(256) void k_gemv_sum(const float* __restrict__ partial, int slices,
                                                   int64_t M, int64_t N, float alpha, void* y,
                                                   int y_bf16, int64_t ldy) {

@@ -27,6 +27,9 @@ namespace mx {
 // place among its own wave's slots of the same bin comes from ballots over the
 // bits of the bin number.  Sums of whole numbers: the result does not depend on
 // the order in which atomics arrive.
+// Latency bound: 16384 x 4 slots of 32 experts (1 MB in all) take 2.4 us to count
+// and 4.7 us to place in 64 chunks, a chunk alone (24 x 4 slots) 2.8 us without the
+// count's launch.  Chunks of one slot a thread keep the ranks a single pass.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanMaxChunks = 256;
@@ -213,8 +216,9 @@ __device__ __forceinline__ RowRun row_run(int64_t first, int at, int runs) {
 }
 
 // ============================================================== dispatch
-// One read of a token's run, top_k writes.  The copy moves 16-byte runs of elements of
-// `size` bytes whatever they hold, so NaN patterns stay as they are.
+// One read of a token's run, top_k writes: bound by the writes.  The copy moves 16-byte
+// runs of elements whatever they hold, so NaN patterns stay as they are.  16384 x 2880
+// bf16 to 4 rows each: 93 us, 5.1 TB/s; the weighted form 113 us of 2885 columns.
 template <typename T, bool NARROW>
 __global__ __launch_bounds__(256) void k_dispatch_copy(const T* __restrict__ x, int64_t ldx,
                                                        const int32_t* __restrict__ pos,
@@ -280,7 +284,9 @@ __global__ __launch_bounds__(256) void k_dispatch_scaled(const T* __restrict__ x
 // Q_D of a token's 1x32 blocks (a quad of lanes per block, 8 values a lane) once,
 // its codes and scale byte written to the token's top_k rows: the values are the
 // same in each, so one conversion serves them all.  Every lane of a quad gets the
-// block's 16 bytes of codes and stores them to one of the rows, four rows at a time.
+// block's 16 bytes of codes and stores them to one of the rows, four rows at a time
+// (4 bytes a lane to every row took 51 us for 16384 x 2880 to 4 rows each, this 44.7 us,
+// 4.4 TB/s; two or four runs of x a thread 48 us).
 template <typename T>
 __global__ __launch_bounds__(256) void k_dispatch_quant(const T* __restrict__ x, int64_t ldx,
                                                         const int32_t* __restrict__ pos,
@@ -339,7 +345,8 @@ __device__ __forceinline__ Slots load_slots(const int32_t* __restrict__ pos,
   return s;
 }
 
-// Sums in float32 in slot order, each product rounded first.
+// Sums in float32 in slot order, each product rounded first.  HBM bound: 16384 x 4 rows of
+// 2880 float32 into bf16 161 us, 5.3 TB/s (164 us one row at a time).
 template <typename TZ, typename TY, bool NARROW>
 __global__ __launch_bounds__(256) void k_combine(const TZ* __restrict__ z, int64_t ldz, int64_t rows,
                                                  const int32_t* __restrict__ pos,
@@ -367,7 +374,8 @@ __global__ __launch_bounds__(256) void k_combine(const TZ* __restrict__ z, int64
 }
 
 // One workgroup per token: dz rows as a weighted dispatch, and each slot's inner
-// product <dy, z> as per-thread sums, then a fixed tree over lanes and waves.
+// product <dy, z> as per-thread sums, then a fixed tree over lanes and waves.  HBM bound:
+// 240 us for 16384 x 4 rows of 2880 (bf16 dy and dz, float32 z), 5.1 TB/s.
 template <typename TY, typename TZ, bool NARROW>
 __global__ __launch_bounds__(256) void k_combine_bwd(
     const TY* __restrict__ dy, int64_t lddy, const TZ* __restrict__ z, int64_t ldz, int64_t rows,
