@@ -20,6 +20,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mx_device.h"
 #include "mx_host.h"
 
@@ -103,6 +105,24 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The first `left` of V neighbouring sums, at T's alignment.
+template <int V, typename T>
+__device__ __forceinline__ void store_sums(T* p, const float (&sum)[V], int left) {
+  T v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if constexpr (sizeof(T) == 2) v[i] = (T)f32_to_bf16_rne(sum[i]);
+    else v[i] = sum[i];
+  }
+  if (left >= V) {
+    __builtin_memcpy(p, v, sizeof(v));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < left) p[i] = v[i];
+  }
 }
 
 // The row tiles (of R rows) of all groups in one sequence.  Every lane holds two groups:
@@ -345,6 +365,42 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
     }
   };
 
+  // The waves' sums of a tile, cols() neighbouring columns a thread.
+  const auto join = [&](auto cols) {
+    constexpr int V = decltype(cols)::value;
+    for (int o = threadIdx.x; o < cur.mrows * (tile_n / V); o += blockDim.x) {
+      const int m = o / (tile_n / V), n = V * (o % (tile_n / V)), left = cur.ncols - n;
+      if (left <= 0 || !(real >> m & 1)) continue;
+      float sum[V] = {};
+      if (nblk) {
+        const float* const p = s_part + (turn * waves * 16 + m) * ldp + n;
+        float v[X][kMaxWaves][V];  // all reads in flight, then the sum in order
+#pragma unroll
+        for (int k = 0; k < X; ++k)
+#pragma unroll
+          for (int w = 0; w < kMaxWaves; ++w)
+            __builtin_memcpy(v[k][w], __builtin_assume_aligned(p + (min(w, waves - 1) * 16 + 4 * k) * ldp, 4 * V),
+                             4 * V);
+#pragma unroll
+        for (int k = X - 1; k >= 0; --k)
+#pragma unroll
+          for (int w = 0; w < kMaxWaves; ++w)
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] += w < waves ? v[k][w][i] : 0.0f;
+      }
+      const int64_t col = (int64_t)cur.nt * tile_n + n;
+      if (a.slices > 1) {
+        store_sums<V>(a.partial + ((int64_t)cur.ks * a.M + cur.m0 + m) * a.N + col, sum, left);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] *= a.alpha;
+      const int64_t at = (int64_t)(cur.m0 + m) * a.ldy + col;
+      if (a.y_bf16) store_sums<V>(static_cast<uint16_t*>(a.y) + at, sum, left);
+      else store_sums<V>(static_cast<float*>(a.y) + at, sum, left);
+    }
+  };
+
   x_rows();
   if (nblk) {
     stream();
@@ -409,32 +465,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
       }
     }
     lds_barrier();
-    for (int o = threadIdx.x; o < cur.mrows * tile_n; o += blockDim.x) {
-      const int m = o / tile_n, n = o % tile_n;
-      if (n >= cur.ncols || !(real >> m & 1)) continue;
-      float sum = 0.0f;
-      if (nblk) {
-        const float* const p = s_part + (turn * waves * 16 + m) * ldp + n;
-        float v[X][kMaxWaves];  // all reads in flight, then the sum in order
-#pragma unroll
-        for (int k = 0; k < X; ++k)
-#pragma unroll
-          for (int w = 0; w < kMaxWaves; ++w) v[k][w] = p[(min(w, waves - 1) * 16 + 4 * k) * ldp];
-#pragma unroll
-        for (int k = X - 1; k >= 0; --k)
-#pragma unroll
-          for (int w = 0; w < kMaxWaves; ++w) sum += w < waves ? v[k][w] : 0.0f;
-      }
-      const int64_t col = (int64_t)cur.nt * tile_n + n;
-      if (a.slices > 1) {
-        a.partial[((int64_t)cur.ks * a.M + cur.m0 + m) * a.N + col] = sum;
-        continue;
-      }
-      const int64_t at = (int64_t)(cur.m0 + m) * a.ldy + col;
-      sum *= a.alpha;
-      if (a.y_bf16) static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_bf16_rne(sum);
-      else static_cast<float*>(a.y)[at] = sum;
-    }
+    // Four columns a thread keep this to half of the waves; with few rows it is the latency
+    // that counts.  One and four columns a thread: 61 tokens x 4 of 32 experts (8 rows a tile)
+    // 64.9 and 60.5 us, 1024 rows of 4096 x 4096 83.7 and 70.9, one token's 4 rows 10.7 and
+    // 11.0.  A float32 x has four rows and three terms to read: two columns (256 rows of
+    // 2880 x 2880 41.9 and 38.2 us).
+    if constexpr (X == 3) join(std::integral_constant<int, 2>());
+    else if (cur.mrows <= 4) join(std::integral_constant<int, 1>());
+    else join(std::integral_constant<int, 4>());
     if (++t == t_end) break;
     turn ^= 1;
     const int grp = cur.grp, m0 = cur.m0, ks = cur.ks;
