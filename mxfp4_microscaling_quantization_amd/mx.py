@@ -138,7 +138,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream):
     if stream is None:  # the handle alone: a Stream object costs 2.6 us more
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -525,7 +525,7 @@ def _device_error(tensors):
 
 
 def _on_current_device(*tensors) -> None:
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise _device_error(tensors)
@@ -551,7 +551,7 @@ def _torch_stream(stream):
 def _empty(shape, dtype, like, stream):
     """A tensor of the current device, allocated on the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(_torch_stream(stream)):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -582,14 +582,18 @@ def _nbytes(workspace) -> int:
 
 
 def _check_packed(codes, scales, K):
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    """Leading dimensions of packed weights and the pitch of their scale rows."""
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise ValueError("packed weights are uint8")
-    if codes.shape[:-1] != scales.shape[:-1]:
+    *rows, half = codes.shape
+    *scale_rows, scale_ld = scales.shape
+    if rows != scale_rows:
         raise ValueError("codes and scales must have the same rows")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("packed weights must be contiguous")
-    if 2 * codes.shape[-1] != K:
-        raise ValueError(f"x has {K} columns, the weight {2 * codes.shape[-1]}")
+    if 2 * half != K:
+        raise ValueError(f"x has {K} columns, the weight {2 * half}")
+    return rows, scale_ld
 
 
 def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, workspace=None,
@@ -598,10 +602,10 @@ def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, works
     w = (codes [N, K/2], scales [N, >= K/32]); returns [M, N]."""
     codes, scales = w
     M, K = x.shape
-    _check_packed(codes, scales, K)
-    if codes.dim() != 2:
+    rows, scale_ld = _check_packed(codes, scales, K)
+    if len(rows) != 1:
         raise ValueError("one packed weight has codes [N, K/2] and scales [N, >= K/32]")
-    N = codes.shape[0]
+    N = rows[0]
     _on_current_device(x, codes, scales, out, workspace)
     xt, ldx = dtype_code(x), _row_ld(x, "x")
     if out is not None:
@@ -609,7 +613,7 @@ def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, works
     y = _output(out, (M, N), out_dtype, x, stream)
     _keep(stream, x, codes, scales, out, workspace)
     workspace = _workspace(workspace, mx_gemv_workspace_size(xt, M, N, K), x, stream)
-    mx_gemv(x, xt, ldx, codes, scales, scales.shape[1], M, N, K, alpha, y, dtype_code(y),
+    mx_gemv(x, xt, ldx, codes, scales, scale_ld, M, N, K, alpha, y, dtype_code(y),
             _row_ld(y, "out"), workspace, _nbytes(workspace), stream)
     return y
 
@@ -623,10 +627,10 @@ def gemv_grouped(x: torch.Tensor, w, offs, src=None, top_k=1, alpha=1.0, out=Non
     codes, scales = w
     xr, K = x.shape
     groups = offs.numel() - 1
-    _check_packed(codes, scales, K)
-    if codes.dim() != 3 or codes.shape[0] != groups:
+    w_rows, scale_ld = _check_packed(codes, scales, K)
+    if len(w_rows) != 2 or w_rows[0] != groups:
         raise ValueError(f"codes and scales must have the same rows, {groups} groups of them")
-    N = codes.shape[1]
+    N = w_rows[1]
     if offs.dtype != torch.int64 or not offs.is_contiguous():
         raise ValueError("offs must be int64")
     if src is not None and (src.dtype != torch.int32 or not src.is_contiguous()):
@@ -637,7 +641,7 @@ def gemv_grouped(x: torch.Tensor, w, offs, src=None, top_k=1, alpha=1.0, out=Non
         out_dtype = out.dtype
     y = _output(out, (rows, N), out_dtype, x, stream)
     _keep(stream, x, codes, scales, offs, src, out)
-    mx_gemv_grouped(x, dtype_code(x), _row_ld(x, "x"), xr, src, top_k, codes, scales, scales.shape[2],
+    mx_gemv_grouped(x, dtype_code(x), _row_ld(x, "x"), xr, src, top_k, codes, scales, scale_ld,
                     offs, groups, rows, N, K, alpha, y, dtype_code(y), _row_ld(y, "out"), stream)
     return y
 
