@@ -170,11 +170,11 @@ struct GroupTiles {
   }
 };
 
-// Measured (one launch): one bf16 row of 14336 x 4096, 31 MB of weights, 8.3 us (3.8 TB/s,
-// its start and end in it); 61 tokens x 4 of 32 experts 5760 x 2880, 285 MB, 62.5 us (4.6
-// TB/s); 16 float32 tokens x 4 of 32, 2880 x 2880, 32.5 us; 47 bf16 rows of 4096 x 14336
-// 26.6 us.  Of the 61 tokens' time the loads alone take 53 us and the rest alone 44 us; the
-// 47 rows are bound by the rest (25 us), each of their three row tiles decoding the weights.
+// Measured (one launch): one bf16 row of 14336 x 4096, 31 MB of weights, 8.4 us (3.7 TB/s,
+// its start and end in it); 61 tokens x 4 of 32 experts 5760 x 2880, 285 MB, 60.6 us (4.7
+// TB/s); 16 float32 tokens x 4 of 32, 2880 x 2880, 32.6 us; 47 bf16 rows of 4096 x 14336
+// 25.6 us.  Of the 61 tokens' time the loads alone take 53 us and the rest alone some 40; the
+// 47 rows are bound by the rest, each of their three row tiles decoding the weights.
 //
 // One workgroup per compute unit: two of them, with smaller windows, took 68 us for the 61
 // tokens where one takes 63, and several row tiles per workgroup, decoded once, 36 us for the
@@ -379,8 +379,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
         for (int k = 0; k < X; ++k)
 #pragma unroll
           for (int w = 0; w < kMaxWaves; ++w)
-            __builtin_memcpy(v[k][w], __builtin_assume_aligned(p + (min(w, waves - 1) * 16 + 4 * k) * ldp, 4 * V),
-                             4 * V);
+            __builtin_memcpy(
+                v[k][w], __builtin_assume_aligned(p + (min(w, waves - 1) * 16 + 4 * k) * ldp, 4 * V), 4 * V);
 #pragma unroll
         for (int k = X - 1; k >= 0; --k)
 #pragma unroll
