@@ -425,8 +425,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_gemv(const GemvArgs a) {
           if (4 * four < cur.mrows) x_put(four, b0, b1);
       }
       if (nblk) {
-        // this round's scale bytes: the stream is at most a tile's subtiles ahead, so it has not
-        // come to the next round's yet
+        // these windows' scale bytes: the stream is at most a tile's subtiles ahead, so it has not
+        // come to the next windows' yet
         wave_sync();
         s_scale[64 * wave + lane] = scale16;
         wave_sync();
