@@ -573,6 +573,12 @@ def _output(out, shape, dtype, like, stream):
     return out
 
 
+def _check_workspace(workspace) -> None:
+    """The library takes a workspace as one run of bytes."""
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _workspace(workspace, need, like, stream):
     return _empty((need,), torch.uint8, like, stream) if workspace is None and need else workspace
 
@@ -606,6 +612,7 @@ def gemv(x: torch.Tensor, w, alpha=1.0, out=None, out_dtype=torch.float32, works
     if len(rows) != 1:
         raise ValueError("one packed weight has codes [N, K/2] and scales [N, >= K/32]")
     N = rows[0]
+    _check_workspace(workspace)
     _on_current_device(x, codes, scales, out, workspace)
     xt, ldx = dtype_code(x), _row_ld(x, "x")
     if out is not None:
@@ -655,6 +662,7 @@ def moe_plan(ids: torch.Tensor, experts: int, workspace=None, stream=None):
         raise ValueError("ids must be int32 or int64")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
+    _check_workspace(workspace)
     _on_current_device(ids, workspace)
     _keep(stream, ids, workspace)
     workspace = _workspace(workspace, mx_moe_plan_workspace_size(tokens, top_k, experts), ids, stream)
