@@ -515,8 +515,8 @@ def linear_bwd(dy: torch.Tensor, xq, wq, M, N, K, seed, workspace=None, stream=N
 
 
 # The conveniences below check what the C calls cannot see: types, shapes, that
-# every tensor is on the current device and that rows are contiguous (row strides
-# are passed on).  Outputs are allocated on the stream the call runs on.  They sit
+# every tensor and the stream are the current device's and that rows are contiguous
+# (row strides are passed on).  Outputs are allocated on the stream the call runs on.  They sit
 # in front of calls of a few microseconds, so the checks are plain conditions and
 # messages are made only for an error.
 def _device_error(tensors):
@@ -545,7 +545,11 @@ def _row_ld(t: torch.Tensor, what: str) -> int:
 
 
 def _torch_stream(stream):
-    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream)
+    if stream.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"stream of {stream.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return stream
 
 
 def _empty(shape, dtype, like, stream):
