@@ -690,13 +690,22 @@ def _routing(pos, weights, tokens):
     return pos.shape[1]
 
 
+def _check_rows(rows, out_rows) -> None:
+    if rows is not None and rows != out_rows:
+        raise ValueError(f"out has {out_rows} rows, not {rows}")
+
+
 def moe_dispatch(x: torch.Tensor, pos, weights=None, rows=None, out=None, stream=None):
     """Rows of x [tokens, cols] copied (times weights) to out[pos]: [rows, cols], rows = all
     slots if neither it nor out is given.  Rows no slot maps to are left as `out` had them."""
     tokens, cols = x.shape
     top_k = _routing(pos, weights, tokens)
+    if out is not None:
+        _check_rows(rows, out.shape[0])
+        rows = out.shape[0]
+    elif rows is None:
+        rows = pos.numel()
     _on_current_device(x, pos, weights, out)
-    rows = out.shape[0] if out is not None else pos.numel() if rows is None else rows
     o = _output(out, (rows, cols), x.dtype, x, stream)
     _keep(stream, x, pos, weights, out)
     mx_moe_dispatch(x, dtype_code(x), _row_ld(x, "x"), pos, weights, tokens, top_k, rows, cols, o,
@@ -714,6 +723,7 @@ def moe_dispatch_quantize(x: torch.Tensor, pos, rows=None, out=None, stream=None
         out = (_empty((rows, cols // 2), torch.uint8, x, stream),
                _empty((rows, cols // 32), torch.uint8, x, stream))
     codes, scales = out
+    _check_rows(rows, codes.shape[0])
     rows = codes.shape[0]
     if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous()
             or not scales.is_contiguous() or codes.dim() != 2 or codes.shape[1] != cols // 2

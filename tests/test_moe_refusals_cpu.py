@@ -1,5 +1,6 @@
 """CPU checks of what the routing and few-row conveniences refuse before the library is called:
-workspaces that are not one run of memory, streams of another device."""
+workspaces that are not one run of memory, streams of another device,
+a number of rows that is not out's."""
 from types import SimpleNamespace
 
 import pytest
@@ -45,3 +46,12 @@ def test_streams_of_another_device_are_refused(name, monkeypatch):
     other = SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0x1000)
     with pytest.raises(ValueError, match="stream of cuda:1"):
         calls(other)[name]()
+
+
+def test_rows_that_are_not_out_s_are_refused():
+    x, pos = torch.zeros(2, 64), torch.zeros((2, 2), dtype=torch.int32)
+    for rows in (2, 8):
+        with pytest.raises(ValueError, match=f"out has 4 rows, not {rows}"):
+            mx.moe_dispatch(x, pos, rows=rows, out=torch.zeros(4, 64))
+        with pytest.raises(ValueError, match=f"out has 4 rows, not {rows}"):
+            mx.moe_dispatch_quantize(x, pos, rows=rows, out=packed(4, 64))
