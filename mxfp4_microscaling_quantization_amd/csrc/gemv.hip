@@ -608,7 +608,8 @@ extern "C" int mx_gemv(const void* x, int x_dtype, int64_t ldx, const uint8_t* w
   a.x = x; a.ldx = ldx; a.x_rows = (int)M; a.M = (int)M; a.N = N; a.K = (int)K;
   a.codes = w_codes; a.scales = w_scales; a.scale_ld = w_scale_ld;
   a.scale_end = (N - 1) * w_scale_ld + K / 32;
-  a.alpha = alpha; a.y = y; a.y_bf16 = y_dtype == MX_BF16; a.ldy = ldy;
+  a.alpha = K ? alpha : 0.0f;  // an empty sum is 0 under any alpha
+  a.y = y; a.y_bf16 = y_dtype == MX_BF16; a.ldy = ldy;
   a.partial = static_cast<float*>(workspace);
   return gemv_any<false>(a, p, x_dtype, 0, as_stream(stream));
 }
@@ -632,6 +633,7 @@ extern "C" int mx_gemv_grouped(const void* x, int x_dtype, int64_t ldx, int64_t 
   a.M = (int)rows; a.N = N; a.K = (int)K; a.offs = offs; a.groups = (int)groups;
   a.codes = w_codes; a.scales = w_scales; a.scale_ld = w_scale_ld;
   a.scale_end = (groups * N - 1) * w_scale_ld + K / 32;
-  a.alpha = alpha; a.y = y; a.y_bf16 = y_dtype == MX_BF16; a.ldy = ldy;
+  a.alpha = K ? alpha : 0.0f;  // an empty sum is 0 under any alpha
+  a.y = y; a.y_bf16 = y_dtype == MX_BF16; a.ldy = ldy;
   return gemv_any<true>(a, p, x_dtype, held, as_stream(stream));
 }
