@@ -4,13 +4,15 @@
 // and the same per expert of a mixture-of-experts layer, with the routed rows'
 // ranges and sources read on the device.
 //
-// What bounds it: the weights are read once, 17/32 byte each, and every value
-// meets only M rows of x, so for few rows HBM (or the latency of one pass over
-// it) is the bound.  The products run on V_MFMA_F32_16X16X32_BF16: E2M1 values
-// times a power of two are exact in bf16 (one conversion instruction per two
-// codes), the products are exact in float32 and the sums are float32.  A bf16 x
-// goes in as it is; a float32 x is split exactly into three bf16 terms (8
-// significant bits each, by truncation), one MFMA each.
+// What bounds it: a tile of rows of x (16 of a bf16 x, 4 of a float32 x) reads and
+// decodes all the weights, 17/32 byte each.  For one row tile that read is the bound,
+// HBM's rate or, where the weights stay in it, the Infinity Cache's, or the latency of
+// one pass where there is little to read; from two row tiles on it is the decoding and
+// the products, which are done again for each.  The products run on
+// V_MFMA_F32_16X16X32_BF16: E2M1 values times a power of two are exact in bf16 (one
+// conversion instruction per two codes), the products are exact in float32 and the sums
+// are float32.  A bf16 x goes in as it is; a float32 x is split exactly into three bf16
+// terms (8 significant bits each, by truncation), which take three of an MFMA's columns.
 //
 // Lane layout: lane l holds MFMA row l & 15 (a weight row) or column l & 15 (a row of
 // x) and the 8 contraction values of group l >> 4.  The contraction may run in any
@@ -171,14 +173,19 @@ struct GroupTiles {
 };
 
 // Measured (one launch): one bf16 row of 14336 x 4096, 31 MB of weights, 8.4 us (3.7 TB/s,
-// its start and end in it); 61 tokens x 4 of 32 experts 5760 x 2880, 285 MB, 60.6 us (4.7
-// TB/s); 16 float32 tokens x 4 of 32, 2880 x 2880, 32.6 us; 47 bf16 rows of 4096 x 14336
-// 25.6 us.  Of the 61 tokens' time the loads alone take 53 us and the rest alone some 40; the
-// 47 rows are bound by the rest, each of their three row tiles decoding the weights.
+// its start and end in it) with three such weights in turn, which the Infinity Cache holds,
+// and 8.9 with 21, which it does not; 61 tokens x 4 of 32 experts 5760 x 2880, 285 MB, 60.6
+// us (4.7 TB/s); 16 float32 tokens x 4 of 32, 2880 x 2880, 32.6 us; 47 bf16 rows of 4096 x
+// 14336 25.6 us and 64 float32 rows 67.5 us.  Of the 61 tokens' time the loads alone take 53
+// us and the rest alone some 40; the 47 rows are bound by the rest, each of their three row
+// tiles decoding the weights, and the 64 rows' 16 row tiles the more so.
 //
 // One workgroup per compute unit: two of them, with smaller windows, took 68 us for the 61
 // tokens where one takes 63, and several row tiles per workgroup, decoded once, 36 us for the
 // 47 rows where one each takes 30 (more x to stage, registers for it, fewer loads ahead).
+// That is for the eight waves of 1024 values and more.  Shorter contractions have a wave per
+// 128 values and leave the card idle with it: four bf16 rows of 262144 x 768, x 384 and x 128
+// take 35, 35 and 41 us, 3.1, 1.5 and 0.4 TB/s.
 // The alternative of x in LDS and whole rows of weights per wave, without sums across
 // waves, computes faster but reads 64-byte pieces of 128 rows at once: 73 us for the 61
 // tokens.
@@ -187,7 +194,7 @@ struct GroupTiles {
 // run of consecutive tiles, column tiles first, so that it keeps its rows of x while the
 // group and row tile stay.  Its waves split the contraction into windows of up to 4 S
 // blocks (wave w takes windows w, w + W, ...): a wave holds a window's x operands in
-// registers and walks the tile's weight rows, 16 at a time, two loads of them ahead of
+// registers and walks the tile's weight rows, 16 at a time, Q loads of them ahead of
 // their use -- also across tiles, so that the weight stream does not stop at a tile's
 // end.  Its sums go to LDS, where the waves' are added in wave order.
 //
