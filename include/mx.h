@@ -79,6 +79,7 @@ enum { MX_F32 = 0, MX_BF16 = 1 };   /* element types of unquantized tensors */
 enum { MX_ROW = 0, MX_COL = 1 };    /* 1x32 blocks along cols / 32x1 blocks along rows */
 enum { MX_RNE = 0, MX_SR = 1 };     /* Q_D: nearest, ties to even / Q_S: stochastic */
 enum { MX_I32 = 0, MX_I64 = 1 };    /* types of expert ids */
+enum { MX_SILU = 0, MX_GELU = 1 };  /* activations of mx_glu: g / (1 + e^-g), g Phi(g) */
 
 /* Largest number of groups mx_gemm_grouped accepts. */
 #define MX_MAX_GROUPS 128
@@ -415,6 +416,155 @@ int mx_gemv_grouped(const void* x, int x_dtype, int64_t ldx, int64_t x_rows, con
                     int64_t w_scale_ld, const int64_t* offs, int64_t groups, int64_t rows,
                     int64_t N, int64_t K, float alpha, void* y, int y_dtype, int64_t ldy,
                     void* stream);
+
+/* ------------------------------------------------------------------ 8-bit matrices
+ * For layers that four bits are too coarse for, and for what is kept for a backward pass.
+ * An 8-bit matrix of logical shape [rows, cols] is codes [rows][ld] (OCP E4M3: sign, four
+ * exponent bits of bias 7, three mantissa bits, largest value 448) and scales
+ * [rows][scale_ld] (E8M0), one byte per 128 columns; the last block of a row may be
+ * shorter.  ld >= cols rounded up to a multiple of 16, ld % 16 == 0, ld <= 2^23; the bytes
+ * from cols up to that multiple are 0.  scale_ld >= 4 ceil(cols / 512), scale_ld % 4 == 0;
+ * the quantizers fill the last dword of a row with 0.  Any rows and cols.
+ * A block's scale is the smallest 2^e, e >= -127, with max|v| <= 448 2^e (e = -127 for a
+ * block of zeros); an element's code is the E4M3 value nearest to v 2^-e, ties to even, with
+ * v's sign.  A block holding NaN or Inf gets scale byte 0xFF and zero codes.  Blocks are
+ *   1x128 along the columns (MX_ROW: activations, gradients),
+ *   128x1 along the rows, stored transposed as a [cols, rows] matrix (MX_COL), or
+ *   128x128 (tile: weights; each row of a tile holds the tile's byte), so that a product and
+ *   its transpose see the same values.
+ * The rules for NULL, empty sizes, alignment and errors are those of the calls above.
+ *
+ * mx_quantize8: x [rows][cols] (`dtype`, rows ldx >= cols elements apart) along `axis`. */
+int mx_quantize8(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t cols, int axis,
+                 uint8_t* codes, int64_t ld, uint8_t* scales, int64_t scale_ld, void* stream);
+
+/* mx_quantize8_dual: both layouts from one read of x: codes / scales [rows, cols] and
+ * codes_t / scales_t [cols, rows].  tile == 0: 1x128 and 128x1 blocks, equal bit for bit to
+ * two mx_quantize8 calls (a gradient that both backward products take).  tile == 1: 128x128
+ * blocks, the same values in both layouts (a weight); codes_t and scales_t may then both be
+ * NULL (a weight that is not trained). */
+int mx_quantize8_dual(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t cols, int tile,
+                      uint8_t* codes, int64_t ld, uint8_t* scales, int64_t scale_ld,
+                      uint8_t* codes_t, int64_t ld_t, uint8_t* scales_t, int64_t scale_ld_t,
+                      void* stream);
+
+/* mx_requantize8: double quantization: the values of an 8-bit matrix [rows, cols] quantized
+ * with 128x1 blocks, transposed -- equal to mx_quantize8(MX_COL) of its float32 values
+ * (values past the float32 range, which a block of float32 values near it can round to,
+ * count as infinite). */
+int mx_requantize8(const uint8_t* codes, int64_t ld, const uint8_t* scales, int64_t scale_ld,
+                   int64_t rows, int64_t cols, uint8_t* codes_t, int64_t ld_t, uint8_t* scales_t,
+                   int64_t scale_ld_t, void* stream);
+
+/* mx_dequantize8: float32 values (exact; rounded to nearest even for a bf16 out) of an 8-bit
+ * matrix, out rows ldo >= cols elements apart; a block with scale byte 0xFF is NaN. */
+int mx_dequantize8(const uint8_t* codes, int64_t ld, const uint8_t* scales, int64_t scale_ld,
+                   int64_t rows, int64_t cols, void* out, int out_dtype, int64_t ldo, void* stream);
+
+/* mx_gemm8: C[m][n] = alpha * sum_k deq(A)[m][k] * deq(B)[n][k] of two 8-bit matrices
+ * A [M, K] and B [N, K]; C (c_dtype) has rows ldc >= N elements apart.  Any M, N < 2^31,
+ * K <= 2^23 (M or N == 0: no-op; K == 0: C = 0, the operands may be NULL).  Sums are float32
+ * in a fixed order, one rounding to nearest even gives a bf16 C.  For a float32 C, and for up
+ * to 64 rows of A, the products are exact too (of values used down to bits of 2^-133).  A
+ * bf16 C of more rows takes the 8-bit matrix instructions at twice the rate: they add the
+ * products of eight neighbouring k with 13 bits below the largest of them (2e-5 of C's norm
+ * for normal operands).  Scale byte 0xFF makes its row's or column's sums NaN.  Up to 64 rows
+ * of A the weights B are read once.  workspace: at least mx_gemm8_workspace_size bytes (the partial sums of a sliced
+ * contraction; 0: may be NULL), 16-byte aligned. */
+size_t mx_gemm8_workspace_size(int64_t M, int64_t N, int64_t K);
+int mx_gemm8(const uint8_t* a_codes, int64_t lda, const uint8_t* a_scales, int64_t a_scale_ld,
+             const uint8_t* b_codes, int64_t ldb, const uint8_t* b_scales, int64_t b_scale_ld,
+             int64_t M, int64_t N, int64_t K, float alpha, void* c, int c_dtype, int64_t ldc,
+             void* workspace, size_t workspace_bytes, void* stream);
+
+/* mx_linear8_fwd / mx_linear8_bwd: the linear layer on 8-bit matrices,
+ *   Y = Q(X) Q(W)^T;  dX = Q(dY) Q(W);  dW = Q^T(dY) Q^T(Q(X))^T (straight-through)
+ * with Q(X), Q(dY) in 1x128 blocks along the contraction, Q(W) in 128x128 tiles, and Q^T the
+ * 128x1 blocks along the rows.  X [M, K], W [N, K], Y, dY [M, N]; each with a type and rows
+ * ld* elements apart of its own; dw is float32.  The forward writes y and what the backward
+ * takes: the 8-bit checkpoint of X (xq_codes [M][K16], xq_scales [M][4 ceil(K/512)]; K16: K
+ * rounded up to a multiple of 16), and the weight in both layouts (wq_codes [N][K16],
+ * wq_scales [N][4 ceil(K/512)], wt_codes [K][N16], wt_scales [K][4 ceil(N/512)]).  wt_codes
+ * and wt_scales NULL: no backward is to come.  w NULL: wq holds the quantized weight already
+ * (several forwards with the same weight; wt is not touched).  Any M, N, K <= 2^23.  Forward:
+ * M or N == 0 writes no y; K == 0: y = 0.  Backward: K == 0 is a no-op; M or N == 0 gives dx = 0
+ * and dw = 0 and reads nothing.  workspace as mx_linear_bwd's, of at least the bytes that the
+ * _workspace_size call gives (0: may be NULL). */
+size_t mx_linear8_fwd_workspace_size(int64_t M, int64_t N, int64_t K);
+int mx_linear8_fwd(const void* x, int x_dtype, int64_t ldx, const void* w, int w_dtype, int64_t ldw,
+                   int64_t M, int64_t N, int64_t K, void* y, int y_dtype, int64_t ldy,
+                   uint8_t* xq_codes, uint8_t* xq_scales, uint8_t* wq_codes, uint8_t* wq_scales,
+                   uint8_t* wt_codes, uint8_t* wt_scales, void* workspace, size_t workspace_bytes,
+                   void* stream);
+size_t mx_linear8_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
+int mx_linear8_bwd(const void* dy, int dy_dtype, int64_t lddy, int64_t M, int64_t N, int64_t K,
+                   const uint8_t* xq_codes, const uint8_t* xq_scales, const uint8_t* wt_codes,
+                   const uint8_t* wt_scales, void* dx, int dx_dtype, int64_t lddx, float* dw,
+                   int64_t lddw, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ gated activation
+ * h = act(g) u of rows z = (g, u): z [rows][2 cols], rows ldz >= 2 cols elements apart, g the
+ * first half of a row, u the second; act MX_SILU or MX_GELU (Phi the normal distribution);
+ * float32 arithmetic, one rounding to h's type.  It stands between an MLP's up and down
+ * products.  live: DEVICE counter of the rows in use (mx_moe_plan's offs + experts, 8-byte
+ * aligned), or NULL for all; outputs of rows from *live on are left as they were.
+ * kept_codes / kept_scales (both NULL: nothing is kept): the checkpoint for the backward
+ * pass, the 8-bit matrix of [2 rows, cols] whose rows 2r and 2r+1 are g and u of row r --
+ * what mx_quantize8 (MX_ROW) writes for z seen as [2 rows][cols].  Any rows < 2^30, cols <=
+ * 2^23; rows or cols == 0: no-op.
+ *
+ * mx_glu: h [rows][cols] (h_dtype, rows ldh elements apart).
+ * mx_glu_quantize: h as the packed MXFP4 operand of the next product instead, the codes and
+ *   scales of mx_quantize_ld (MX_ROW, MX_RNE, no rotation) of float32 h; cols % 32 == 0.
+ * mx_glu_quantize8: h as an 8-bit matrix, mx_quantize8 (MX_ROW) of float32 h.
+ * mx_glu_bwd: dz = (dh u act'(g), dh act(g)), g and u the values that the checkpoint holds,
+ *   one rounding to dz's type. */
+int mx_glu(const void* z, int z_dtype, int64_t ldz, const int64_t* live, int64_t rows, int64_t cols,
+           int act, void* h, int h_dtype, int64_t ldh, uint8_t* kept_codes, int64_t kept_ld,
+           uint8_t* kept_scales, int64_t kept_scale_ld, void* stream);
+int mx_glu_quantize(const void* z, int z_dtype, int64_t ldz, const int64_t* live, int64_t rows,
+                    int64_t cols, int act, uint8_t* codes, uint8_t* scales, int64_t scale_ld,
+                    uint8_t* kept_codes, int64_t kept_ld, uint8_t* kept_scales,
+                    int64_t kept_scale_ld, void* stream);
+int mx_glu_quantize8(const void* z, int z_dtype, int64_t ldz, const int64_t* live, int64_t rows,
+                     int64_t cols, int act, uint8_t* codes, int64_t ld, uint8_t* scales,
+                     int64_t scale_ld, uint8_t* kept_codes, int64_t kept_ld, uint8_t* kept_scales,
+                     int64_t kept_scale_ld, void* stream);
+int mx_glu_bwd(const void* dh, int dh_dtype, int64_t lddh, const uint8_t* kept_codes, int64_t kept_ld,
+               const uint8_t* kept_scales, int64_t kept_scale_ld, const int64_t* live, int64_t rows,
+               int64_t cols, int act, void* dz, int dz_dtype, int64_t lddz, void* stream);
+
+/* ------------------------------------------------------------------ router
+ * mx_moe_route: the choices of a mixture-of-experts layer's router.  logits [tokens][experts]
+ * (`dtype`, rows ld >= experts elements apart), s their softmax over the experts.  A token takes
+ * part if mask [tokens] is NULL or not 0 there and some logit of it is not -Inf; n such tokens.
+ *   ids [tokens][top_k]     the experts of the largest logits, in falling order, of equal ones
+ *                           the lowest first; -1 (a slot left out, as mx_moe_plan takes it)
+ *                           where only -Inf or NaN is left, and for a token that takes no part
+ *   weights [tokens][top_k] float32: s of the choice, divided by the choices' sum where
+ *                           renormalize is 1; 0 for a slot left out
+ *   counts [experts + 1]    slots of each expert; n
+ *   sums [experts]          float32: sum of s over the tokens that take part
+ *   loss [1]                float32: the balance loss E sum_e f_e P_e, f_e = counts_e / (n
+ *                           top_k), P_e = sums_e / n; 0 if n is 0
+ * NaN or +Inf among a token's logits makes its weights, the sums and the loss NaN.  The order of
+ * the sums is fixed.  1 <= experts <= MX_MAX_GROUPS, 1 <= top_k <= min(experts, 16), tokens *
+ * top_k < 2^31.  workspace: at least mx_moe_route_workspace_size bytes (0: may be NULL).
+ *
+ * mx_moe_route_bwd: dlogits (`dtype`, rows ldd elements apart) from dweights [tokens][top_k]
+ * (mx_moe_combine_bwd's) and dloss [1] (each float32 or NULL for 0), with the forward's ids
+ * and counts; the choices and counts are constants of the gradient.  counts may be summed over
+ * several devices' batches first (the loss is then that of all of them).  0 for a token that
+ * takes no part; dweights of a slot left out are not used. */
+size_t mx_moe_route_workspace_size(int64_t tokens, int64_t experts, int64_t top_k);
+int mx_moe_route(const void* logits, int dtype, int64_t ld, const uint8_t* mask, int64_t tokens,
+                 int64_t experts, int64_t top_k, int renormalize, int32_t* ids, float* weights,
+                 int32_t* counts, float* sums, float* loss, void* workspace,
+                 size_t workspace_bytes, void* stream);
+int mx_moe_route_bwd(const void* logits, int dtype, int64_t ld, const uint8_t* mask, int64_t tokens,
+                     int64_t experts, int64_t top_k, int renormalize, const int32_t* ids,
+                     const int32_t* counts, const float* dweights, const float* dloss,
+                     void* dlogits, int64_t ldd, void* stream);
 
 /* ------------------------------------------------------------------ expert routing
  * Rows of a mixture-of-experts layer ([ALTO] news paragraph: the MoE model trained

@@ -19,7 +19,8 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = ROOT / "_build"
 LIB = PKG / "libmx355.so"
-SOURCES = ["quant.hip", "gemm.hip", "linear.hip", "deosc.hip", "moe.hip", "gemv.hip"]
+SOURCES = ["quant.hip", "gemm.hip", "linear.hip", "deosc.hip", "moe.hip", "gemv.hip",
+           "quant8.hip", "gemm8.hip", "linear8.hip", "glu.hip", "route.hip"]
 # The synthetic optimizer step that drives the de-oscillation workload (a
 # workload generator, not part of the method) lives in a library of its own.
 SYNTH_LIB = PKG / "libmx355_synth.so"

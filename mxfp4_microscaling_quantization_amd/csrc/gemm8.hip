@@ -1,0 +1,626 @@
+// Products of 8-bit block-scaled matrices:
+//   C[m][n] = alpha sum_k deq(A)[m][k] deq(B)[n][k]
+// A [M, K] and B [N, K] hold E4M3 codes and one E8M0 byte per 128 values of k.
+//
+// Two kinds of products.  A bf16 C takes the scaled 8-bit matrix instructions, which take the codes
+// and scale bytes as they are (one byte per 32 values of k and row; a block of 128 gives the same
+// byte four times).  They add the products of eight neighbouring values with about 14 bits below the
+// largest of the eight before these sums meet in float32 (measured: a product 2^-13 of its neighbour
+// survives, 2^-14 is lost, between groups 2^-23 survives): 2e-5 of C's norm for normal operands,
+// against the 2e-3 of C's own rounding.  A float32 C and few rows take V_MFMA_F32_*_BF16 instead
+// (wide), half the rate: a code times a power of two is exact in bf16 (down to bits of 2^-133),
+// and every product joins a float32 sum.
+//
+// Per lane an operand is 32 bytes of one row: row (lane % 32), k [32 (lane / 32), + 32) of the 64 of
+// V_MFMA_SCALE_F32_32X32X64_F8F6F4.  The bf16 instructions take a quarter of those each, 8 values a
+// lane: k may run in any order as long as both operands agree.  B goes in first, so that a lane
+// holds consecutive columns of a row of C.
+//
+// Code rows are padded with zeros to a multiple of 16 bytes (K is that multiple here), scale
+// rows to whole dwords, which hold the bytes of 512 values of k.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "mx_device8.h"
+#include "mx_host8.h"
+
+namespace mx {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr int kFmtE4m3 = 0;  // cbsz / blgp operand format
+
+struct Gemm8Args {
+  const uint8_t* a;
+  const uint8_t* sa;
+  const uint8_t* b;
+  const uint8_t* sb;
+  int64_t lda, lsa, ldb, lsb, M, N, K;
+  void* c;        // output, or the partial sums of a sliced contraction [slices][M][N] float32
+  int64_t ldc;
+  int tiles_m, tiles_n, slices;
+  int64_t slice;  // contraction values a slice, a multiple of 512
+  float alpha;
+};
+
+// Eight codes times a scale (0xFF: +Inf, which gives NaN), as bf16.
+__device__ __forceinline__ v8bf widen8(uint32_t lo, uint32_t hi, float scale) {
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  v8bf v;
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
+  return v;
+}
+
+// The first n of V consecutive outputs at T's alignment.  Outputs go past the caches' replacement
+// (nontemporal) where the next launch does not read them.
+template <typename T, int V, bool KEEP>
+__device__ __forceinline__ void store_run8(T* p, const float* v, int64_t n) {
+  typedef T vec __attribute__((ext_vector_type(V)));
+  typedef vec avec __attribute__((aligned(sizeof(T))));
+  vec raw;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if constexpr (sizeof(T) == 2) raw[i] = (T)f32_to_bf16_rne(v[i]);
+    else raw[i] = v[i];
+  }
+  if (n >= V) {
+    if constexpr (KEEP) *reinterpret_cast<avec*>(p) = raw;
+    else __builtin_nontemporal_store(raw, reinterpret_cast<avec*>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = raw[i];
+  }
+}
+
+// s_waitcnt with only the vector-memory counter constrained (gfx9 encoding).
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+typedef __attribute__((address_space(3))) void* lds8_ptr_t;
+// Direct global -> LDS loads from a scalar base and a 32-bit offset a lane: lane i's 16 (4) bytes
+// land at LDS address M0 + 16 i (4 i).  Written as asm so that the compiler does not wait for
+// them by itself; the kernel counts them and waits before its barriers.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_load16(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load4(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+// A load from any address: the last step of a contraction takes its missing codes from here.
+__device__ const uint4 kZero16 = {0, 0, 0, 0};
+__device__ __forceinline__ void lds_load16_at(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory", "m0");
+}
+// The same loads if `yes`, without a branch (a branch between the products of a step would let the
+// compiler move them past it): by no lane otherwise.  Every lane is active around them.
+__device__ __forceinline__ void lds_load16_if(bool yes, const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
+               :
+               : "s"(lds), "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(yes ? -1 : 0))
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load4_if(bool yes, const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\tglobal_load_lds_dword %1, %2\n\ts_mov_b64 exec, -1"
+               :
+               : "s"(lds), "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(yes ? -1 : 0))
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+__device__ __forceinline__ int64_t lmin8(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// ============================================================== tiles
+// A workgroup of 2 x 2 waves owns a T x T tile of C and walks K in steps of 64 through a ring of
+// four stages in LDS (codes [rows][64 bytes]; the 16-byte chunks of row r stand in the order
+// c ^ ((r >> 2) & 3), which spreads a fragment read over all banks).  A wave holds (T/64)^2
+// accumulators of 32x32 and the fragments of two steps: while the products of one step run, it
+// reads the next step's fragments and issues the loads of the step four ahead, between the
+// products.  One barrier a step: before it, each wave has its fragments of the step in registers
+// (so the step's stage is free) and its share of the next step's loads has landed.
+template <int T, typename TY, bool SLICED, bool TAIL, bool WIDE>
+__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm8Args g) {
+  constexpr int W = T / 64;                  // 32-row accumulators of a wave along m and n
+  constexpr int LC = T / 32;                 // code loads a wave and step (16 rows each)
+  constexpr int LS = T / 128;                // scale loads a wave and 8 steps (64 rows each)
+  constexpr int STAGE = 2 * T * 64;          // bytes
+  __shared__ __align__(16) uint8_t ring[4 * STAGE];
+  __shared__ __align__(16) uint32_t s_scale[2][2 * T];
+
+  const int tiles = g.tiles_m * g.tiles_n;
+  int id = blockIdx.x;
+  {  // consecutive tiles to one die, whose workgroups are dealt round-robin over 8
+    const int total = gridDim.x, q = total / 8, r = total % 8, x = id % 8;
+    id = x * q + min(x, r) + id / 8;
+  }
+  const int slice = SLICED ? id / tiles : 0;
+  id -= slice * tiles;
+  constexpr int kRows = 4;  // tile rows walked together: B tiles are read again from L2
+  const int span = kRows * g.tiles_n, first_m = id / span * kRows;
+  const int gm = min(g.tiles_m - first_m, kRows);
+  const int64_t m0 = (int64_t)(first_m + id % span % gm) * T, n0 = (int64_t)(id % span / gm) * T;
+  const int64_t k0 = SLICED ? slice * g.slice : 0;
+  const int64_t klen = SLICED ? lmin8(g.slice, g.K - k0) : g.K;
+  const int KT = (int)((klen + 63) / 64);
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave >> 1) * (T / 2), wn = (wave & 1) * (T / 2);
+  const int lr = lane & 31, lh = lane >> 5;
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(lds8_ptr_t)ring;
+  const uint32_t scale0 = (uint32_t)(uintptr_t)(lds8_ptr_t)s_scale;
+
+  // sources: wave w loads rows [w T/2, + T/2) of the tile's 2 T operand rows (A's, then B's), 16
+  // rows a load, rows past the matrix clamped to its last (they feed outputs that are not stored)
+  const bool isA = wave < 2;
+  const uint8_t* base = (isA ? g.a + m0 * g.lda : g.b + n0 * g.ldb) + k0;
+  const int64_t ld = isA ? g.lda : g.ldb, last = (isA ? g.M - m0 : g.N - n0) - 1;
+  const int dr = lane >> 2, dc = ((lane & 3) ^ ((dr >> 2) & 3)) * 16;
+  const int half = (wave & 1) * (T / 2);
+  uint32_t off[LC];
+#pragma unroll
+  for (int j = 0; j < LC; ++j) off[j] = (uint32_t)(lmin8(half + j * 16 + dr, last) * ld) + dc;
+  const uint8_t* sbase = (isA ? g.sa + m0 * g.lsa : g.sb + n0 * g.lsb) + k0 / 128;
+  const int64_t lds_ = isA ? g.lsa : g.lsb;
+  uint32_t soff[LS];
+#pragma unroll
+  for (int j = 0; j < LS; ++j) soff[j] = (uint32_t)(lmin8(half + j * 64 + lane, last) * lds_);
+
+  // Load j of step kt.  TAIL (K no multiple of 64): chunks past the contraction are zeros, steps
+  // past it too.  Else such steps are not loaded; SURE: it is no such step.
+  auto issue_one = [&](int kt, int j, auto SURE) {
+    const uint32_t to = ring0 + (uint32_t)(kt & 3) * STAGE + (uint32_t)(wave * (T / 2) + j * 16) * 64;
+    const int64_t k = (int64_t)kt * 64;
+    if constexpr (TAIL) lds_load16_at(k + dc < klen ? base + k + off[j] : reinterpret_cast<const uint8_t*>(&kZero16), to);
+    else if constexpr (decltype(SURE)::value) lds_load16(base + k, off[j], to);
+    else lds_load16_if(kt < KT, base + k, off[j], to);
+  };
+  // the scale bytes of steps 8 grp .. 8 grp + 7, if `yes`
+  auto issue_scales = [&](int grp, bool yes) {
+#pragma unroll
+    for (int j = 0; j < LS; ++j)
+      lds_load4_if(yes, sbase + grp * 4, soff[j],
+                   scale0 + (uint32_t)((grp & 1) * 2 * T + wave * (T / 2) + j * 64) * 4);
+  };
+
+  v16f acc[W][W];
+#pragma unroll
+  for (int a = 0; a < W; ++a)
+#pragma unroll
+    for (int b = 0; b < W; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+
+  // fragments of two steps: chunks 2 lh and 2 lh + 1 of row lr of accumulator row (column) t
+  v8i fa[2][W], fb[2][W];
+  uint32_t sa[W], sb[W], na[W], nb[W];
+  const uint32_t key = (lr >> 2) & 3;
+  const uint8_t* pa[2] = {ring + (wm + lr) * 64 + ((2 * lh) ^ key) * 16,
+                          ring + (wm + lr) * 64 + ((2 * lh + 1) ^ key) * 16};
+  const uint8_t* pb[2] = {ring + (T + wn + lr) * 64 + ((2 * lh) ^ key) * 16,
+                          ring + (T + wn + lr) * 64 + ((2 * lh + 1) ^ key) * 16};
+  auto read_one = [&](auto P, int kt, int i) {  // i: 4 W reads
+    constexpr int p = decltype(P)::value;
+    const int t = i >> 2, h = i & 1;
+    const uint32_t at = (uint32_t)(kt & 3) * STAGE + t * 32 * 64;
+    const v4i c = *reinterpret_cast<const v4i*>((i & 2 ? pb[h] : pa[h]) + at);
+    v8i& f = i & 2 ? fb[p][t] : fa[p][t];
+    f = h ? __builtin_shufflevector(f, __builtin_shufflevector(c, c, 0, 1, 2, 3, 0, 1, 2, 3), 0, 1, 2, 3, 8, 9, 10, 11)
+          : __builtin_shufflevector(c, c, 0, 1, 2, 3, -1, -1, -1, -1);
+  };
+  // the scale bytes of steps kt and kt + 1 (kt even)
+  auto read_scales = [&](int kt, uint32_t (&x)[W], uint32_t (&y)[W]) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(s_scale[(kt >> 3) & 1]) + ((kt >> 1) & 3);
+#pragma unroll
+    for (int t = 0; t < W; ++t) {
+      x[t] = p[(wm + t * 32 + lr) * 4];
+      y[t] = p[(T + wn + t * 32 + lr) * 4];
+    }
+  };
+  auto barrier = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // prologue: the first scales and up to four steps on their way, the first step's fragments read
+  issue_scales(0, true);
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    if (s < KT) {
+#pragma unroll
+      for (int j = 0; j < LC; ++j) issue_one(s, j, std::true_type{});
+    }
+  if (KT > 3) wait_vm<3 * LC>();
+  else if (KT > 2) wait_vm<2 * LC>();
+  else if (KT > 1) wait_vm<LC>();
+  else wait_vm<0>();
+  barrier();
+  read_scales(0, sa, sb);
+#pragma unroll
+  for (int i = 0; i < 4 * W; ++i) read_one(std::integral_constant<int, 0>{}, 0, i);
+
+  // Step kt, kt % 2 == P.  SURE: step kt + 4 exists; without it the loads and reads of steps past
+  // the contraction move nothing that is used.
+  auto step = [&](int kt, auto P, auto SURE) {
+    constexpr int p = decltype(P)::value;
+    constexpr int Q = 1 - p;
+    // the loads of steps kt + 2 and kt + 3 may stay in flight
+    if (decltype(SURE)::value || kt + 3 < KT) wait_vm<2 * LC>();
+    else if (kt + 2 < KT) wait_vm<LC>();
+    else wait_vm<0>();
+    barrier();
+    if constexpr (p == 0) issue_scales((kt >> 3) + 1, (kt & 7) == 0 && kt + 8 < KT);
+    else read_scales(kt + 1, na, nb);
+    constexpr int kParts = WIDE ? 4 : 1, kProducts = kParts * W * W;
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) {
+      v8bf xa[W], xb[W];
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int t = 0; t < W; ++t) {
+          xa[t] = widen8(fa[p][t][2 * j], fa[p][t][2 * j + 1], scale_of(sa[t]));
+          xb[t] = widen8(fb[p][t][2 * j], fb[p][t][2 * j + 1], scale_of(sb[t]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < W * W; ++i) {
+        const int a = i / W, b = i % W, at = j * W * W + i;
+        if constexpr (WIDE)
+          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb[a], xa[b], acc[a][b], 0, 0, 0);
+        else
+          acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[p][a], fa[p][b], acc[a][b], kFmtE4m3,
+                                                                      kFmtE4m3, 0, (int)sb[a], 0, (int)sa[b]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int r = 4 * W * at / kProducts; r < 4 * W * (at + 1) / kProducts; ++r)
+          read_one(std::integral_constant<int, Q>{}, kt + 1, r);
+#pragma unroll
+        for (int l = LC * at / kProducts; l < LC * (at + 1) / kProducts; ++l) issue_one(kt + 4, l, SURE);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if constexpr (p == 1) {
+#pragma unroll
+      for (int t = 0; t < W; ++t) sa[t] = na[t], sb[t] = nb[t];
+    }
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  int kt = 0;
+  for (; kt + 5 < KT; kt += 2) {
+    step(kt, I0{}, std::true_type{});
+    step(kt + 1, I1{}, std::true_type{});
+  }
+  for (; kt < KT; kt += 2) {
+    step(kt, I0{}, std::false_type{});
+    if (kt + 1 < KT) step(kt + 1, I1{}, std::false_type{});
+  }
+
+  // Epilogue: a lane holds C[m = lr][n = 8 q + 4 lh + i] of each accumulator.  A wave stages 64
+  // rows at a time in its quarter of the idle ring (16-byte chunks XORed with row & 15) and stores
+  // whole row segments.
+  constexpr int CH = W * 8;                  // 16-byte chunks of float32 a row
+  constexpr int RB = CH * 16;
+  constexpr int V = sizeof(TY) == 2 ? 8 : 4; // outputs a lane and store
+  constexpr int LPR = W * 32 / V;            // lanes a row
+  wait_vm<0>();  // loads past the contraction (TAIL) have landed
+  __syncthreads();
+  uint8_t* stg = ring + wave * 64 * RB;
+  static_assert(4 * 64 * RB <= (int)sizeof(ring), "staging space");
+  TY* c = static_cast<TY*>(g.c) + (SLICED ? (int64_t)slice * g.M * g.N : 0);
+#pragma unroll
+  for (int p = 0; p < W / 2; ++p) {
+#pragma unroll
+    for (int bb = 0; bb < 2; ++bb) {
+      const int r = bb * 32 + lr;
+#pragma unroll
+      for (int a = 0; a < W; ++a)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v16f& t = acc[a][2 * p + bb];
+          *reinterpret_cast<float4*>(stg + r * RB + (((a * 8 + q * 2 + lh) ^ (r & 15)) * 16)) =
+              make_float4(t[4 * q] * g.alpha, t[4 * q + 1] * g.alpha, t[4 * q + 2] * g.alpha,
+                          t[4 * q + 3] * g.alpha);
+        }
+    }
+#pragma unroll 4
+    for (int it = 0; it < LPR; ++it) {
+      const int r = it * (64 / LPR) + lane / LPR, col = (lane % LPR) * V;
+      float v[V];
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q)
+        *reinterpret_cast<float4*>(v + 4 * q) =
+            *reinterpret_cast<const float4*>(stg + r * RB + (((col / 4 + q) ^ (r & 15)) * 16));
+      const int64_t m = m0 + wm + p * 64 + r, n = n0 + wn + col;
+      if (m < g.M && n < g.N) store_run8<TY, V, SLICED>(c + m * g.ldc + n, v, g.N - n);
+    }
+  }
+}
+
+// C = alpha times the slices' sums, in their order.
+template <typename TY>
+__global__ __launch_bounds__(256) void k_gemm8_sum(const float* __restrict__ part, int slices, int64_t M,
+                                                   int64_t N, int64_t runs, float alpha, TY* __restrict__ c,
+                                                   int64_t ldc) {
+  const int64_t total = M * runs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / runs, n = i % runs * 4;
+    const int left = (int)lmin8(4, N - n);
+    float s[4] = {};
+    for (int k = 0; k < slices; ++k) {
+      const float* p = part + ((int64_t)k * M + m) * N + n;
+      if (left == 4) {
+        float v[4];
+        __builtin_memcpy(v, p, 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = k ? s[e] + v[e] : v[e];
+      } else {
+        for (int e = 0; e < left; ++e) s[e] = k ? s[e] + p[e] : p[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] *= alpha;
+    store_run8<TY, 4, false>(c + m * ldc + n, s, N - n);
+  }
+}
+
+// ============================================================== few rows
+// Up to 64 rows of A: the weights are read once, and that read is the bound.  A wave takes 16 NT
+// columns and up to 16 MT rows over units of 512 values of k, straight from memory into the
+// operand registers; the waves of a workgroup take turns over the units of the same columns, and
+// their sums meet in LDS in a fixed order.
+struct Rows8Args {
+  Gemm8Args g;
+  int units, waves;
+};
+
+// Most waves of a workgroup: the operands of 512 values take registers.
+constexpr int rows8_waves(int mt, int nt) { return mt * nt > 1 ? 8 : 16; }
+
+template <int MT, int NT, typename TY>
+__global__ __launch_bounds__(rows8_waves(MT, NT) * 64) void k_gemm8_rows(const Rows8Args r) {
+  extern __shared__ __align__(16) float s_sum[];  // [waves - 1][MT * NT][64][4]
+  const Gemm8Args& g = r.g;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, kg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
+  const uint8_t* wp[NT];
+  const uint8_t* wsp[NT];
+  const uint8_t* xp[MT];
+  const uint8_t* xsp[MT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t n = lmin8(n0 + t * 16 + l16, g.N - 1);
+    wp[t] = g.b + n * g.ldb;
+    wsp[t] = g.sb + n * g.lsb;
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t m = lmin8(t * 16 + l16, g.M - 1);
+    xp[t] = g.a + m * g.lda;
+    xsp[t] = g.sa + m * g.lsa;
+  }
+  v4f acc[NT][MT];
+#pragma unroll
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int b = 0; b < MT; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[a][b][e] = 0.f;
+  for (int u = wave; u < r.units; u += r.waves) {
+    const int64_t k0 = (int64_t)u * 512;
+    uint32_t ws[NT], xs[MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) ws[t] = *reinterpret_cast<const uint32_t*>(wsp[t] + u * 4);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xs[t] = *reinterpret_cast<const uint32_t*>(xsp[t] + u * 4);
+    v8i w[4][NT], x[4][MT];
+    const bool whole = k0 + 512 <= g.K;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t k = k0 + s * 128 + kg * 32 + h * 16;
+        const int64_t at = whole ? k : lmin8(k, g.K - 16);
+        auto take = [&](const uint8_t* p, v8i& f) {
+          const v4i c = *reinterpret_cast<const v4i*>(p + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[4 * h + e] = whole || k < g.K ? c[e] : 0;
+        };
+#pragma unroll
+        for (int t = 0; t < NT; ++t) take(wp[t], w[s][t]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) take(xp[t], x[s][t]);
+      }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (k0 + s * 128 >= g.K) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v8bf wj[NT], xj[MT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          wj[t] = widen8(w[s][t][2 * j], w[s][t][2 * j + 1], scale_of(ws[t] >> (8 * s) & 255u));
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          xj[t] = widen8(x[s][t][2 * j], x[s][t][2 * j + 1], scale_of(xs[t] >> (8 * s) & 255u));
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+          for (int b = 0; b < MT; ++b)
+            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wj[a], xj[b], acc[a][b], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int b = 0; b < MT; ++b)
+      *reinterpret_cast<v4f*>(s_sum + (((wave * NT + a) * MT + b) * 64 + lane) * 4) = acc[a][b];
+  __syncthreads();
+  for (int t = wave; t < NT * MT; t += r.waves) {
+    v4f sum = *reinterpret_cast<const v4f*>(s_sum + (t * 64 + lane) * 4);
+    for (int w = 1; w < r.waves; ++w)
+      sum += *reinterpret_cast<const v4f*>(s_sum + ((w * NT * MT + t) * 64 + lane) * 4);
+    const int64_t m = t % MT * 16 + l16, n = n0 + t / MT * 16 + kg * 4;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = sum[e] * g.alpha;
+    if (m < g.M && n < g.N) store_run8<TY, 4, true>(static_cast<TY*>(g.c) + m * g.ldc + n, v, g.N - n);
+  }
+}
+
+// C = 0: an empty contraction, without touching the operands.
+template <typename TY>
+__global__ __launch_bounds__(256) void k_gemm8_zero(int64_t M, int64_t N, TY* __restrict__ c, int64_t ldc) {
+  const int64_t runs = (N + 3) / 4, total = M * runs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const float zero[4] = {};
+    store_run8<TY, 4, false>(c + i / runs * ldc + i % runs * 4, zero, N - i % runs * 4);
+  }
+}
+
+// ============================================================== launches
+struct Plan8 {
+  bool rows, big;
+  int slices;
+  int64_t slice;
+};
+
+// Few rows take the wave-per-column kernel.  Tiles of 256 where they fill the compute units,
+// else tiles of 128, the contraction sliced where even they leave units idle.
+static Plan8 gemm8_plan(int64_t M, int64_t N, int64_t K) {
+  Plan8 p{M <= 64, false, 1, K};
+  if (p.rows) return p;
+  p.big = cdiv(M, 256) * cdiv(N, 256) >= 200;
+  const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
+  if (p.big || tiles >= 256 || K < 2048) return p;
+  const int64_t n = hmin(hmin(cdiv(512, tiles), K / 1024), 64);
+  if (n < 2) return p;
+  p.slice = cdiv(cdiv(K, n), 512) * 512;
+  p.slices = (int)cdiv(K, p.slice);
+  if (p.slices < 2) p.slices = 1, p.slice = K;
+  return p;
+}
+
+size_t gemm8_workspace(int64_t M, int64_t N, int64_t K) {
+  const Plan8 p = gemm8_plan(M, N, round16(K));
+  return p.slices > 1 ? (size_t)p.slices * M * N * sizeof(float) : 0;
+}
+
+template <int T, typename TY, bool SLICED, bool WIDE>
+static int launch_tiles(Gemm8Args g, hipStream_t st) {
+  const int64_t tm = cdiv(g.M, T), tn = cdiv(g.N, T);
+  if (tm * tn * g.slices > 0x7FFFFFFFll / 256) return MX_ERR_SHAPE;
+  g.tiles_m = (int)tm;
+  g.tiles_n = (int)tn;
+  const dim3 grid((unsigned)(tm * tn * g.slices));
+  if (g.K % 64) k_gemm8_tile<T, TY, SLICED, true, WIDE><<<grid, 256, 0, st>>>(g);
+  else k_gemm8_tile<T, TY, SLICED, false, WIDE><<<grid, 256, 0, st>>>(g);
+  return launch_status();
+}
+
+template <int MT, int NT, typename TY>
+static int launch_rows(const Gemm8Args& g, hipStream_t st) {
+  Rows8Args r{g, (int)cdiv(g.K, 512), 1};
+  const int64_t rounds = cdiv(r.units, rows8_waves(MT, NT));
+  r.waves = (int)cdiv(r.units, rounds);
+  k_gemm8_rows<MT, NT, TY><<<dim3((unsigned)cdiv(g.N, 16 * NT)), r.waves * 64, (size_t)r.waves * MT * NT * 1024, st>>>(r);
+  return launch_status();
+}
+
+template <typename TY>
+static int gemm8_launch(Gemm8Args g, void* workspace, hipStream_t st) {
+  const int64_t threads = g.M * cdiv(g.N, 4);
+  const dim3 flat((unsigned)hmin(cdiv(threads, 256), 4096));
+  if (g.K == 0) {
+    k_gemm8_zero<TY><<<flat, 256, 0, st>>>(g.M, g.N, static_cast<TY*>(g.c), g.ldc);
+    return launch_status();
+  }
+  const Plan8 p = gemm8_plan(g.M, g.N, g.K);
+  g.slices = p.slices;
+  g.slice = p.slice;
+  if (p.rows) {
+    if (g.M <= 16) return launch_rows<1, 1, TY>(g, st);
+    if (g.M <= 32) return launch_rows<2, 2, TY>(g, st);
+    if (g.M <= 48) return launch_rows<3, 2, TY>(g, st);
+    return launch_rows<4, 2, TY>(g, st);
+  }
+  constexpr bool kWide = sizeof(TY) == 4;
+  if (p.big) return launch_tiles<256, TY, false, kWide>(g, st);
+  if (p.slices == 1) return launch_tiles<128, TY, false, kWide>(g, st);
+  Gemm8Args part = g;
+  part.c = workspace;
+  part.ldc = g.N;
+  part.alpha = 1.0f;
+  const int s = launch_tiles<128, float, true, kWide>(part, st);
+  if (s != MX_OK) return s;
+  k_gemm8_sum<TY><<<flat, 256, 0, st>>>(static_cast<const float*>(workspace), p.slices, g.M, g.N, cdiv(g.N, 4),
+                                        g.alpha, static_cast<TY*>(g.c), g.ldc);
+  return launch_status();
+}
+
+int gemm8_impl(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t lsa, const uint8_t* b, int64_t ldb,
+               const uint8_t* sb, int64_t lsb, int64_t M, int64_t N, int64_t K, float alpha, void* c,
+               int c_dtype, int64_t ldc, void* workspace, hipStream_t st) {
+  if (M == 0 || N == 0) return MX_OK;
+  const Gemm8Args g{a, sa, b, sb, lda, lsa, ldb, lsb, M, N, round16(K), c, ldc, 0, 0, 1, 0, alpha};
+  return c_dtype == MX_F32 ? gemm8_launch<float>(g, workspace, st) : gemm8_launch<uint16_t>(g, workspace, st);
+}
+
+}  // namespace mx
+
+using namespace mx;
+
+static bool gemm8_shape(int64_t M, int64_t N, int64_t K) {
+  return M >= 0 && N >= 0 && K >= 0 && M < kMax8 && N < kMax8 && K <= kMaxAxis8;
+}
+
+extern "C" size_t mx_gemm8_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return gemm8_shape(M, N, K) && M && N && K ? gemm8_workspace(M, N, K) : 0;
+}
+
+extern "C" int mx_gemm8(const uint8_t* a_codes, int64_t lda, const uint8_t* a_scales, int64_t a_scale_ld,
+                        const uint8_t* b_codes, int64_t ldb, const uint8_t* b_scales, int64_t b_scale_ld,
+                        int64_t M, int64_t N, int64_t K, float alpha, void* c, int c_dtype, int64_t ldc,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  MX_REQUIRE(float_type(c_dtype), MX_ERR_ENUM);
+  MX_REQUIRE(gemm8_shape(M, N, K) && ldc >= N, MX_ERR_SHAPE);
+  MX_REQUIRE(matrix8(K, lda, a_scale_ld) && matrix8(K, ldb, b_scale_ld), MX_ERR_SHAPE);
+  if (M == 0 || N == 0) return MX_OK;
+  MX_REQUIRE(c && (K == 0 || (a_codes && a_scales && b_codes && b_scales)), MX_ERR_NULL);
+  MX_REQUIRE(aligned16(c) && aligned16(a_codes) && aligned16(a_scales) && aligned16(b_codes) &&
+                 aligned16(b_scales), MX_ERR_ALIGN);
+  const size_t need = mx_gemm8_workspace_size(M, N, K);
+  if (need) {
+    MX_REQUIRE(workspace && workspace_bytes >= need, MX_ERR_WORKSPACE);
+    MX_REQUIRE(aligned16(workspace), MX_ERR_ALIGN);
+  }
+  return gemm8_impl(a_codes, lda, a_scales, a_scale_ld, b_codes, ldb, b_scales, b_scale_ld, M, N, K, alpha, c,
+                    c_dtype, ldc, workspace, as_stream(stream));
+}

@@ -1,0 +1,118 @@
+// Device-side building blocks of the 8-bit matrices (gfx950, wave64).
+//
+// An 8-bit matrix holds E4M3 codes (OCP: bit 7 sign, 4 exponent bits of bias 7, 3 mantissa bits,
+// largest value 448, 0x7F and 0xFF NaN) and one E8M0 byte per 128 values, the smallest power of
+// two 2^e with amax <= 448 2^e: 448 = 1.75 2^8, so e is the exponent of amax less 8, and one more
+// where its mantissa is past 1.75.  No value is past the largest code, so nothing saturates.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_device.h"
+
+namespace mx {
+
+constexpr int kBlock8 = 128;
+
+// Scale byte from the bit pattern of the block's largest magnitude: 0xFF for NaN or Inf, 0 (e =
+// -127) at the lower end and for a block of zeros, at most 247.
+__device__ __forceinline__ uint32_t scale8_byte_of(uint32_t amax) {
+  if (amax >= 0x7F800000u) return 255u;
+  const uint32_t f = (amax + 0x1FFFFFu) >> 23;  // the carry of a mantissa past 1.75
+  return f > 8u ? f - 8u : 0u;
+}
+
+// 2^e of a scale byte as a float32 factor of decoded codes (0xFF: NaN, whatever the code).
+__device__ __forceinline__ float scale8_of(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FC00000u) : scale_of(byte);
+}
+
+// Largest pattern over the 16 lanes of a row.
+__device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
+  v = quad_max_u32(v);
+  v = max(v, dpp_u32<0x124>(v));  // rotations by 4 and by 8 within the row
+  v = max(v, dpp_u32<0x128>(v));
+  return v;
+}
+
+// E4M3 codes of four values times inv = 2^-e: a value times a power of two is exact in float32
+// but for results below 2^-126, which round to code 0 either way; the conversion rounds to
+// nearest, ties to even, and keeps the sign of zeros.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
+}
+
+// The 8 codes of v under scale byte `byte` (0xFF: code 0).
+__device__ __forceinline__ uint2 encode8(const float v[8], uint32_t byte) {
+  if (byte == 255u) return make_uint2(0u, 0u);
+  const float inv = inv_scale_of(byte);
+  return make_uint2(encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv));
+}
+
+// Exact values of 8 codes times a scale (values past the float32 range come out infinite).
+__device__ __forceinline__ void decode8_e4m3(uint2 w, float scale, float v[8]) {
+  const mx_v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false);
+  const mx_v2f b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, true);
+  const mx_v2f c = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, false);
+  const mx_v2f d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, true);
+  v[0] = a.x * scale; v[1] = a.y * scale; v[2] = b.x * scale; v[3] = b.y * scale;
+  v[4] = c.x * scale; v[5] = c.y * scale; v[6] = d.x * scale; v[7] = d.y * scale;
+}
+
+// The first n (any number, 8 or more: all) of 8 consecutive values at T's alignment, 0 for the
+// others.  T: float or uint16_t (bf16).
+template <typename T>
+__device__ __forceinline__ void load8(const T* __restrict__ p, int64_t n, float v[8]) {
+  if (n >= 8) {
+    T raw[8];
+    __builtin_memcpy(raw, p, sizeof(raw));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2) v[i] = bf16_lo(raw[i]);
+      else v[i] = raw[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.0f;
+      if (i < n) {
+        if constexpr (sizeof(T) == 2) v[i] = bf16_lo(p[i]);
+        else v[i] = p[i];
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* __restrict__ p, int64_t n, const float v[8]) {
+  T raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 2) raw[i] = (T)f32_to_bf16_rne(v[i]);
+    else raw[i] = v[i];
+  }
+  if (n >= 8) {
+    __builtin_memcpy(p, raw, sizeof(raw));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = raw[i];
+  }
+}
+
+// Position of a thread in the flat order (row, lane of the row), `per` lanes a row: the
+// workgroup's first index is divided in 64 bits once, the threads' in 32.
+struct RowLane {
+  int64_t row;
+  int lane;
+};
+__device__ __forceinline__ RowLane row_lane(int64_t first, int at, int per) {
+  const int64_t r0 = first / per;
+  const uint32_t r = (uint32_t)(first - r0 * per) + (uint32_t)at;
+  const uint32_t q = r / (uint32_t)per;
+  return {r0 + q, (int)(r - q * (uint32_t)per)};
+}
+
+}  // namespace mx

@@ -1,0 +1,35 @@
+// Host-side layout of the 8-bit matrices, shared by the quantizers, products and layers.
+#pragma once
+
+#include "mx_host.h"
+
+namespace mx {
+
+inline int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+inline int64_t blocks8(int64_t n) { return cdiv(n, 128); }
+inline int64_t scale8_pitch(int64_t n) { return cdiv(n, 512) * 4; }  // whole dwords of bytes
+inline bool float_type(int t) { return t == MX_F32 || t == MX_BF16; }
+constexpr int64_t kMax8 = (int64_t)1 << 31;       // rows and columns are below this
+constexpr int64_t kMaxAxis8 = (int64_t)1 << 23;   // contraction axes: 256 rows span less than 2^31 bytes
+
+// A [rows, cols] 8-bit matrix at these pitches.
+inline bool matrix8(int64_t cols, int64_t ld, int64_t scale_ld) {
+  return ld >= round16(cols) && ld % 16 == 0 && ld <= kMaxAxis8 && scale_ld >= scale8_pitch(cols) &&
+         scale_ld % 4 == 0 && scale_ld < kMax8;
+}
+
+int quant8_row_impl(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t cols, uint8_t* codes,
+                    int64_t ld, uint8_t* scales, int64_t scale_ld, hipStream_t st);
+// Blocks of 128x128 (tile) or 1x128 and 128x1 from one read; either output may be NULL.
+int quant8_tile_impl(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t cols, bool tile,
+                     uint8_t* codes, int64_t ld, uint8_t* scales, int64_t scale_ld, uint8_t* codes_t,
+                     int64_t ld_t, uint8_t* scales_t, int64_t scale_ld_t, hipStream_t st);
+int requant8_impl(const uint8_t* codes, int64_t ld, const uint8_t* scales, int64_t scale_ld,
+                  int64_t rows, int64_t cols, uint8_t* codes_t, int64_t ld_t, uint8_t* scales_t,
+                  int64_t scale_ld_t, hipStream_t st);
+size_t gemm8_workspace(int64_t M, int64_t N, int64_t K);
+int gemm8_impl(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t lsa, const uint8_t* b,
+               int64_t ldb, const uint8_t* sb, int64_t lsb, int64_t M, int64_t N, int64_t K,
+               float alpha, void* c, int c_dtype, int64_t ldc, void* workspace, hipStream_t st);
+
+}  // namespace mx

@@ -20,6 +20,7 @@ MX_F32, MX_BF16 = 0, 1
 MX_ROW, MX_COL = 0, 1
 MX_RNE, MX_SR = 0, 1
 MX_I32, MX_I64 = 0, 1
+MX_SILU, MX_GELU = 0, 1
 MX_MAX_GROUPS = 128
 
 LIB_PATH = Path(__file__).resolve().parent / "libmx355.so"
@@ -72,6 +73,26 @@ SIGNATURES = {
     "mx_moe_combine": ([_P, _i32, _i64, _i64, _P, _P, _i64, _i64, _i64, _P, _i32, _i64, _P], _i32),
     "mx_moe_combine_bwd": ([_P, _i32, _i64, _P, _i32, _i64, _i64, _P, _P, _i64, _i64, _i64, _P, _i64,
                             _P, _P], _i32),
+    "mx_quantize8": ([_P, _i32, _i64, _i64, _i64, _i32, _P, _i64, _P, _i64, _P], _i32),
+    "mx_quantize8_dual": ([_P, _i32, _i64, _i64, _i64, _i32, _P, _i64, _P, _i64, _P, _i64, _P, _i64, _P], _i32),
+    "mx_requantize8": ([_P, _i64, _P, _i64, _i64, _i64, _P, _i64, _P, _i64, _P], _i32),
+    "mx_dequantize8": ([_P, _i64, _P, _i64, _i64, _i64, _P, _i32, _i64, _P], _i32),
+    "mx_gemm8_workspace_size": ([_i64, _i64, _i64], _sz),
+    "mx_gemm8": ([_P, _i64, _P, _i64, _P, _i64, _P, _i64, _i64, _i64, _i64, _f32, _P, _i32, _i64, _P, _sz, _P],
+                 _i32),
+    "mx_linear8_fwd_workspace_size": ([_i64, _i64, _i64], _sz),
+    "mx_linear8_fwd": ([_P, _i32, _i64, _P, _i32, _i64, _i64, _i64, _i64, _P, _i32, _i64, _P, _P, _P, _P, _P, _P,
+                        _P, _sz, _P], _i32),
+    "mx_linear8_bwd_workspace_size": ([_i64, _i64, _i64], _sz),
+    "mx_linear8_bwd": ([_P, _i32, _i64, _i64, _i64, _i64, _P, _P, _P, _P, _P, _i32, _i64, _P, _i64, _P, _sz, _P],
+                       _i32),
+    "mx_glu": ([_P, _i32, _i64, _P, _i64, _i64, _i32, _P, _i32, _i64, _P, _i64, _P, _i64, _P], _i32),
+    "mx_glu_quantize": ([_P, _i32, _i64, _P, _i64, _i64, _i32, _P, _P, _i64, _P, _i64, _P, _i64, _P], _i32),
+    "mx_glu_quantize8": ([_P, _i32, _i64, _P, _i64, _i64, _i32, _P, _i64, _P, _i64, _P, _i64, _P, _i64, _P], _i32),
+    "mx_glu_bwd": ([_P, _i32, _i64, _P, _i64, _P, _i64, _P, _i64, _i64, _i32, _P, _i32, _i64, _P], _i32),
+    "mx_moe_route_workspace_size": ([_i64, _i64, _i64], _sz),
+    "mx_moe_route": ([_P, _i32, _i64, _P, _i64, _i64, _i64, _i32, _P, _P, _P, _P, _P, _P, _sz, _P], _i32),
+    "mx_moe_route_bwd": ([_P, _i32, _i64, _P, _i64, _i64, _i64, _i32, _P, _P, _P, _P, _P, _i64, _P], _i32),
     "mx_deosc_init": ([_P, _i64, _i64, _P, _P, _P, _P], _i32),
     "mx_deosc_step": ([_P, _i64, _i64, _P, _P, _P, _i32, _f32, _P, _P], _i32),
     "mx_deosc_step_quantize": ([_P, _i64, _i64, _P, _P, _P, _i32, _f32, _P, _P, _P, _P], _i32),
@@ -388,6 +409,108 @@ def mx_moe_combine_bwd(dy, dy_dtype, lddy, z, z_dtype, ldz, rows, pos, weights, 
     _check("mx_moe_combine_bwd", lib().mx_moe_combine_bwd(
         _ptr(dy), dy_dtype, lddy, _ptr(z), z_dtype, ldz, rows, _ptr(pos), _ptr(weights), tokens,
         top_k, cols, _ptr(dz), lddz, _ptr(dweights), _stream(stream)))
+
+
+def mx_quantize8(x, dtype, ldx, rows, cols, axis, codes, ld, scales, scale_ld, stream=None):
+    _check("mx_quantize8", lib().mx_quantize8(_ptr(x), dtype, ldx, rows, cols, axis, _ptr(codes), ld,
+                                              _ptr(scales), scale_ld, _stream(stream)))
+
+
+def mx_quantize8_dual(x, dtype, ldx, rows, cols, tile, codes, ld, scales, scale_ld, codes_t, ld_t, scales_t,
+                      scale_ld_t, stream=None):
+    _check("mx_quantize8_dual", lib().mx_quantize8_dual(
+        _ptr(x), dtype, ldx, rows, cols, tile, _ptr(codes), ld, _ptr(scales), scale_ld, _ptr(codes_t), ld_t,
+        _ptr(scales_t), scale_ld_t, _stream(stream)))
+
+
+def mx_requantize8(codes, ld, scales, scale_ld, rows, cols, codes_t, ld_t, scales_t, scale_ld_t, stream=None):
+    _check("mx_requantize8", lib().mx_requantize8(
+        _ptr(codes), ld, _ptr(scales), scale_ld, rows, cols, _ptr(codes_t), ld_t, _ptr(scales_t), scale_ld_t,
+        _stream(stream)))
+
+
+def mx_dequantize8(codes, ld, scales, scale_ld, rows, cols, out, out_dtype, ldo, stream=None):
+    _check("mx_dequantize8", lib().mx_dequantize8(_ptr(codes), ld, _ptr(scales), scale_ld, rows, cols, _ptr(out),
+                                                  out_dtype, ldo, _stream(stream)))
+
+
+def mx_gemm8_workspace_size(M, N, K) -> int:
+    return int(lib().mx_gemm8_workspace_size(M, N, K))
+
+
+def mx_gemm8(a_codes, lda, a_scales, a_scale_ld, b_codes, ldb, b_scales, b_scale_ld, M, N, K, alpha, c, c_dtype,
+             ldc, workspace=None, workspace_bytes=0, stream=None):
+    _check("mx_gemm8", lib().mx_gemm8(
+        _ptr(a_codes), lda, _ptr(a_scales), a_scale_ld, _ptr(b_codes), ldb, _ptr(b_scales), b_scale_ld, M, N, K,
+        alpha, _ptr(c), c_dtype, ldc, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def mx_linear8_fwd_workspace_size(M, N, K) -> int:
+    return int(lib().mx_linear8_fwd_workspace_size(M, N, K))
+
+
+def mx_linear8_fwd(x, x_dtype, ldx, w, w_dtype, ldw, M, N, K, y, y_dtype, ldy, xq_codes, xq_scales, wq_codes,
+                   wq_scales, wt_codes, wt_scales, workspace=None, workspace_bytes=0, stream=None):
+    _check("mx_linear8_fwd", lib().mx_linear8_fwd(
+        _ptr(x), x_dtype, ldx, _ptr(w), w_dtype, ldw, M, N, K, _ptr(y), y_dtype, ldy, _ptr(xq_codes),
+        _ptr(xq_scales), _ptr(wq_codes), _ptr(wq_scales), _ptr(wt_codes), _ptr(wt_scales), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def mx_linear8_bwd_workspace_size(M, N, K) -> int:
+    return int(lib().mx_linear8_bwd_workspace_size(M, N, K))
+
+
+def mx_linear8_bwd(dy, dy_dtype, lddy, M, N, K, xq_codes, xq_scales, wt_codes, wt_scales, dx, dx_dtype, lddx, dw,
+                   lddw, workspace, workspace_bytes, stream=None):
+    _check("mx_linear8_bwd", lib().mx_linear8_bwd(
+        _ptr(dy), dy_dtype, lddy, M, N, K, _ptr(xq_codes), _ptr(xq_scales), _ptr(wt_codes), _ptr(wt_scales),
+        _ptr(dx), dx_dtype, lddx, _ptr(dw), lddw, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def mx_glu(z, z_dtype, ldz, live, rows, cols, act, h, h_dtype, ldh, kept_codes=None, kept_ld=0, kept_scales=None,
+           kept_scale_ld=0, stream=None):
+    _check("mx_glu", lib().mx_glu(_ptr(z), z_dtype, ldz, _ptr(live), rows, cols, act, _ptr(h), h_dtype, ldh,
+                                  _ptr(kept_codes), kept_ld, _ptr(kept_scales), kept_scale_ld, _stream(stream)))
+
+
+def mx_glu_quantize(z, z_dtype, ldz, live, rows, cols, act, codes, scales, scale_ld, kept_codes=None, kept_ld=0,
+                    kept_scales=None, kept_scale_ld=0, stream=None):
+    _check("mx_glu_quantize", lib().mx_glu_quantize(
+        _ptr(z), z_dtype, ldz, _ptr(live), rows, cols, act, _ptr(codes), _ptr(scales), scale_ld,
+        _ptr(kept_codes), kept_ld, _ptr(kept_scales), kept_scale_ld, _stream(stream)))
+
+
+def mx_glu_quantize8(z, z_dtype, ldz, live, rows, cols, act, codes, ld, scales, scale_ld, kept_codes=None,
+                     kept_ld=0, kept_scales=None, kept_scale_ld=0, stream=None):
+    _check("mx_glu_quantize8", lib().mx_glu_quantize8(
+        _ptr(z), z_dtype, ldz, _ptr(live), rows, cols, act, _ptr(codes), ld, _ptr(scales), scale_ld,
+        _ptr(kept_codes), kept_ld, _ptr(kept_scales), kept_scale_ld, _stream(stream)))
+
+
+def mx_glu_bwd(dh, dh_dtype, lddh, kept_codes, kept_ld, kept_scales, kept_scale_ld, live, rows, cols, act, dz,
+               dz_dtype, lddz, stream=None):
+    _check("mx_glu_bwd", lib().mx_glu_bwd(
+        _ptr(dh), dh_dtype, lddh, _ptr(kept_codes), kept_ld, _ptr(kept_scales), kept_scale_ld, _ptr(live), rows,
+        cols, act, _ptr(dz), dz_dtype, lddz, _stream(stream)))
+
+
+def mx_moe_route_workspace_size(tokens, experts, top_k) -> int:
+    return int(lib().mx_moe_route_workspace_size(tokens, experts, top_k))
+
+
+def mx_moe_route(logits, dtype, ld, mask, tokens, experts, top_k, renormalize, ids, weights, counts, sums, loss,
+                 workspace=None, workspace_bytes=0, stream=None):
+    _check("mx_moe_route", lib().mx_moe_route(
+        _ptr(logits), dtype, ld, _ptr(mask), tokens, experts, top_k, renormalize, _ptr(ids), _ptr(weights),
+        _ptr(counts), _ptr(sums), _ptr(loss), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def mx_moe_route_bwd(logits, dtype, ld, mask, tokens, experts, top_k, renormalize, ids, counts, dweights, dloss,
+                     dlogits, ldd, stream=None):
+    _check("mx_moe_route_bwd", lib().mx_moe_route_bwd(
+        _ptr(logits), dtype, ld, _ptr(mask), tokens, experts, top_k, renormalize, _ptr(ids), _ptr(counts),
+        _ptr(dweights), _ptr(dloss), _ptr(dlogits), ldd, _stream(stream)))
 
 
 def mx_deosc_init(w, rows, cols, w_prev, d_w, d_q, stream=None):
@@ -767,3 +890,298 @@ def moe_combine_bwd(dy: torch.Tensor, z: torch.Tensor, pos, weights=None, out=No
     mx_moe_combine_bwd(dy, dtype_code(dy), _row_ld(dy, "dy"), z, dtype_code(z), _row_ld(z, "z"), rows,
                        pos, weights, tokens, top_k, cols, dz, _row_ld(dz, "out"), dw, stream)
     return dz, dw
+
+
+# ------------------------------------------------------------------ 8-bit matrices
+def _matrix8(rows, cols, like, stream):
+    """An 8-bit matrix [rows, cols] to write: codes [rows, cols rounded up to 16], scales
+    [rows, 4 bytes per 512 columns]."""
+    return (_empty((rows, -(-cols // 16) * 16), torch.uint8, like, stream),
+            _empty((rows, -(-cols // 512) * 4), torch.uint8, like, stream))
+
+
+def _check_matrix8(m, what: str, cols=None):
+    """(rows, code pitch, scale pitch) of an 8-bit matrix of `cols` columns (None: its codes')."""
+    codes, scales = m
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise ValueError(f"{what}: codes and scales are uint8")
+    if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0]:
+        raise ValueError(f"{what}: codes [rows, cols] and scales [rows, blocks] must have the same rows")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{what}: codes and scales must be contiguous")
+    ld, scale_ld = codes.shape[1], scales.shape[1]
+    cols = ld if cols is None else cols
+    if ld % 16 or ld < cols or scale_ld % 4 or scale_ld * 128 < cols:
+        raise ValueError(f"{what}: rows of {ld} codes and {scale_ld} scales do not hold {cols} columns")
+    return codes.shape[0], ld, scale_ld
+
+
+def quantize8(x: torch.Tensor, axis=MX_ROW, stream=None):
+    """The 8-bit matrix (codes, scales) of x [rows, cols] (float32 or bf16) in 1x128 blocks, or of
+    its transpose in 128x1 blocks (MX_COL)."""
+    rows, cols = x.shape
+    ldx = _row_ld(x, "x")
+    _on_current_device(x)
+    q = _matrix8(rows, cols, x, stream) if axis == MX_ROW else _matrix8(cols, rows, x, stream)
+    _keep(stream, x)
+    mx_quantize8(x, dtype_code(x), ldx, rows, cols, axis, q[0], q[0].shape[1], q[1], q[1].shape[1], stream)
+    return q
+
+
+def quantize8_dual(x: torch.Tensor, tile=False, stream=None):
+    """(codes, scales, codes_t, scales_t) of x [rows, cols] from one read: x in 1x128 and its transpose
+    in 128x1 blocks, or both in the same 128x128 tiles (a weight)."""
+    rows, cols = x.shape
+    ldx = _row_ld(x, "x")
+    _on_current_device(x)
+    q, t = _matrix8(rows, cols, x, stream), _matrix8(cols, rows, x, stream)
+    _keep(stream, x)
+    mx_quantize8_dual(x, dtype_code(x), ldx, rows, cols, int(bool(tile)), q[0], q[0].shape[1], q[1], q[1].shape[1],
+                      t[0], t[0].shape[1], t[1], t[1].shape[1], stream)
+    return (*q, *t)
+
+
+def requantize8(q, cols=None, stream=None):
+    """The transpose of an 8-bit matrix [rows, cols] (cols: its code row's length by default), its
+    values quantized again in 128x1 blocks."""
+    rows, ld, scale_ld = _check_matrix8(q, "q", cols)
+    cols = ld if cols is None else cols
+    _on_current_device(*q)
+    t = _matrix8(cols, rows, q[0], stream)
+    _keep(stream, *q)
+    mx_requantize8(q[0], ld, q[1], scale_ld, rows, cols, t[0], t[0].shape[1], t[1], t[1].shape[1], stream)
+    return t
+
+
+def dequantize8(q, cols=None, out_dtype=torch.float32, stream=None):
+    """The values [rows, cols] of an 8-bit matrix (cols: its code row's length by default)."""
+    rows, ld, scale_ld = _check_matrix8(q, "q", cols)
+    cols = ld if cols is None else cols
+    _on_current_device(*q)
+    out = _empty((rows, cols), out_dtype, q[0], stream)
+    _keep(stream, *q)
+    mx_dequantize8(q[0], ld, q[1], scale_ld, rows, cols, out, dtype_code(out), cols, stream)
+    return out
+
+
+def gemm8(a, b, alpha=1.0, out=None, out_dtype=torch.float32, workspace=None, stream=None):
+    """alpha A B^T [M, N] of two 8-bit matrices (codes, scales), A [M, K] and B [N, K]."""
+    M, lda, lsa = _check_matrix8(a, "a")
+    N, ldb, lsb = _check_matrix8(b, "b")
+    if lda != ldb:
+        raise ValueError(f"a has rows of {lda} codes, b of {ldb}")
+    _check_workspace(workspace)
+    _on_current_device(*a, *b, out, workspace)
+    if out is not None:
+        out_dtype = out.dtype
+    c = _output(out, (M, N), out_dtype, a[0], stream)
+    _keep(stream, *a, *b, out, workspace)
+    workspace = _workspace(workspace, mx_gemm8_workspace_size(M, N, lda), a[0], stream)
+    mx_gemm8(a[0], lda, a[1], lsa, b[0], ldb, b[1], lsb, M, N, lda, alpha, c, dtype_code(c), _row_ld(c, "out"),
+             workspace, _nbytes(workspace), stream)
+    return c
+
+
+def _check_exact8(m, what: str, rows: int, cols: int) -> None:
+    """An 8-bit matrix of just this size, as _matrix8 lays it out."""
+    r, ld, scale_ld = _check_matrix8(m, what, cols)
+    if r != rows or ld != -(-cols // 16) * 16 or scale_ld != -(-cols // 512) * 4:
+        raise ValueError(f"{what} is not the 8-bit matrix of [{rows}, {cols}]")
+
+
+def linear8_fwd(x: torch.Tensor, w, out=None, out_dtype=torch.float32, backward=True, workspace=None, stream=None):
+    """(y, xq, wq) of the 8-bit linear layer: y = Q(x) Q(w)^T [M, N] of x [M, K] and w [N, K] (float32 or
+    bf16), xq the 8-bit checkpoint of x, wq = (codes, scales, codes_t, scales_t) the weight's tiles in both
+    layouts (the first alone without `backward`).  w may be such a wq of an earlier call."""
+    M, K = x.shape
+    quantized = not isinstance(w, torch.Tensor)
+    if quantized:
+        if len(w) not in (2, 4):
+            raise ValueError("a quantized weight is (codes, scales) or (codes, scales, codes_t, scales_t)")
+        N = w[0].shape[0]
+        _check_exact8(w[:2], "w", N, K)
+        wq, ldw, wt = tuple(w), K, MX_F32
+    else:
+        N = w.shape[0]
+        if w.dim() != 2 or w.shape[1] != K:
+            raise ValueError(f"x has {K} columns, the weight {tuple(w.shape)}")
+        ldw, wt = _row_ld(w, "w"), dtype_code(w)
+    _check_workspace(workspace)
+    _on_current_device(x, *(w if quantized else (w,)), out, workspace)
+    xt, ldx = dtype_code(x), _row_ld(x, "x")
+    if out is not None:
+        out_dtype = out.dtype
+    y = _output(out, (M, N), out_dtype, x, stream)
+    yt, ldy = dtype_code(y), _row_ld(y, "out")
+    xq = _matrix8(M, K, x, stream)
+    if not quantized:
+        wq = _matrix8(N, K, x, stream) + (_matrix8(K, N, x, stream) if backward else ())
+    _keep(stream, x, *(w if quantized else (w,)), out, workspace)
+    workspace = _workspace(workspace, mx_linear8_fwd_workspace_size(M, N, K), x, stream)
+    t = wq[2:] if len(wq) == 4 else (None, None)
+    mx_linear8_fwd(x, xt, ldx, None if quantized else w, wt, ldw, M, N, K, y, yt, ldy, *xq, *wq[:2], *t, workspace,
+                   _nbytes(workspace), stream)
+    return y, xq, wq
+
+
+def linear8_bwd(dy: torch.Tensor, xq, wq, M, N, K, dx_dtype=torch.float32, workspace=None, stream=None):
+    """(dx [M, K] of dx_dtype, dw [N, K] float32) of linear8_fwd, given dy [M, N] and what it kept."""
+    if tuple(dy.shape) != (M, N):
+        raise ValueError(f"dy must be [{M}, {N}], not {tuple(dy.shape)}")
+    if len(wq) != 4:
+        raise ValueError("the backward takes the weight in both layouts (linear8_fwd with backward=True)")
+    _check_exact8(xq, "xq", M, K)
+    _check_exact8(wq[2:], "wq", K, N)
+    _check_workspace(workspace)
+    _on_current_device(dy, *xq, *wq, workspace)
+    dyt, lddy = dtype_code(dy), _row_ld(dy, "dy")
+    dx = _empty((M, K), dx_dtype, dy, stream)
+    dw = _empty((N, K), torch.float32, dy, stream)
+    _keep(stream, dy, *xq, *wq, workspace)
+    workspace = _workspace(workspace, mx_linear8_bwd_workspace_size(M, N, K), dy, stream)
+    mx_linear8_bwd(dy, dyt, lddy, M, N, K, *xq, *wq[2:], dx, dtype_code(dx), K, dw, K, workspace, _nbytes(workspace),
+                   stream)
+    return dx, dw
+
+
+# ------------------------------------------------------------------ gated activation
+def _glu_rows(rows) -> None:
+    if rows is not None and (rows.dtype != torch.int64 or rows.numel() != 1):
+        raise ValueError("rows must be one int64 on the device (moe_plan's offs[-1:])")
+
+
+def _glu_kept(rows, cols, like, stream):
+    return _matrix8(2 * rows, cols, like, stream)
+
+
+def _glu_size(z):
+    if z.dim() != 2 or z.shape[1] % 2:
+        raise ValueError("z must be [rows, 2 cols]")
+    return z.shape[0], z.shape[1] // 2
+
+
+def glu(z: torch.Tensor, act=MX_SILU, rows=None, checkpoint=False, out=None, out_dtype=torch.float32, stream=None):
+    """h = act(g) u [rows, cols] of z = (g, u) [rows, 2 cols]; with checkpoint (h, kept), kept the 8-bit matrix
+    of z's halves [2 rows, cols] that glu_bwd takes.  rows: device counter of the rows in use (moe_plan's
+    offs[-1:]); those behind are left as `out` had them."""
+    n, cols = _glu_size(z)
+    _glu_rows(rows)
+    _on_current_device(z, rows, out)
+    zt, ldz = dtype_code(z), _row_ld(z, "z")
+    if out is not None:
+        out_dtype = out.dtype
+    h = _output(out, (n, cols), out_dtype, z, stream)
+    ht, ldh = dtype_code(h), _row_ld(h, "out")
+    kept = _glu_kept(n, cols, z, stream) if checkpoint else None
+    _keep(stream, z, rows, out)
+    k = (kept[0], kept[0].shape[1], kept[1], kept[1].shape[1]) if checkpoint else (None, 0, None, 0)
+    mx_glu(z, zt, ldz, rows, n, cols, act, h, ht, ldh, *k, stream)
+    return (h, kept) if checkpoint else h
+
+
+def glu_quantize(z: torch.Tensor, act=MX_SILU, rows=None, checkpoint=False, out=None, stream=None):
+    """glu with h as packed MXFP4 (codes [rows, cols/2], scales [rows, >= cols/32]), the operand of the
+    next product."""
+    n, cols = _glu_size(z)
+    _glu_rows(rows)
+    if out is None:
+        out = _empty((n, cols // 2), torch.uint8, z, stream), _empty((n, cols // 32), torch.uint8, z, stream)
+    codes, scales = out
+    if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous()
+            or not scales.is_contiguous() or codes.shape != (n, cols // 2) or scales.dim() != 2
+            or scales.shape[0] != n):
+        raise ValueError("out must be packed uint8 codes and scales")
+    _on_current_device(z, rows, codes, scales)
+    zt, ldz = dtype_code(z), _row_ld(z, "z")
+    kept = _glu_kept(n, cols, z, stream) if checkpoint else None
+    _keep(stream, z, rows, codes, scales)
+    k = (kept[0], kept[0].shape[1], kept[1], kept[1].shape[1]) if checkpoint else (None, 0, None, 0)
+    mx_glu_quantize(z, zt, ldz, rows, n, cols, act, codes, scales, scales.shape[1], *k, stream)
+    return ((codes, scales), kept) if checkpoint else (codes, scales)
+
+
+def glu_quantize8(z: torch.Tensor, act=MX_SILU, rows=None, checkpoint=False, out=None, stream=None):
+    """glu with h as an 8-bit matrix (codes, scales), gemm8's operand."""
+    n, cols = _glu_size(z)
+    _glu_rows(rows)
+    q = _matrix8(n, cols, z, stream) if out is None else out
+    r, ld, scale_ld = _check_matrix8(q, "out", cols)
+    if r != n:
+        raise ValueError(f"out has {r} rows, not {n}")
+    _on_current_device(z, rows, *q)
+    zt, ldz = dtype_code(z), _row_ld(z, "z")
+    kept = _glu_kept(n, cols, z, stream) if checkpoint else None
+    _keep(stream, z, rows, *q)
+    k = (kept[0], kept[0].shape[1], kept[1], kept[1].shape[1]) if checkpoint else (None, 0, None, 0)
+    mx_glu_quantize8(z, zt, ldz, rows, n, cols, act, q[0], ld, q[1], scale_ld, *k, stream)
+    return (tuple(q), kept) if checkpoint else tuple(q)
+
+
+def glu_bwd(dh: torch.Tensor, kept, act=MX_SILU, rows=None, out=None, out_dtype=None, stream=None):
+    """dz [rows, 2 cols] (of dh's type by default) of glu, given dh [rows, cols] and the checkpoint; rows behind
+    the counter `rows` are left as `out` had them."""
+    n, cols = dh.shape
+    r, ld, scale_ld = _check_matrix8(kept, "kept", cols)
+    if r != 2 * n:
+        raise ValueError(f"kept has {r} rows, not {2 * n}")
+    _glu_rows(rows)
+    _on_current_device(dh, *kept, rows, out)
+    dt, lddh = dtype_code(dh), _row_ld(dh, "dh")
+    dz = _output(out, (n, 2 * cols), out.dtype if out is not None else out_dtype or dh.dtype, dh, stream)
+    _keep(stream, dh, *kept, rows, out)
+    mx_glu_bwd(dh, dt, lddh, kept[0], ld, kept[1], scale_ld, rows, n, cols, act, dz, dtype_code(dz),
+               _row_ld(dz, "out"), stream)
+    return dz
+
+
+# ------------------------------------------------------------------ router
+def _route_mask(mask, tokens) -> None:
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (tokens,)
+                             or not mask.is_contiguous()):
+        raise ValueError("mask must be bool [tokens]")
+
+
+def moe_route(logits: torch.Tensor, top_k: int, renormalize=True, mask=None, workspace=None, stream=None):
+    """(ids [tokens, top_k] int32, weights [tokens, top_k] float32, counts [experts + 1] int32, sums [experts]
+    float32, loss [1] float32) of router logits [tokens, experts]: each token's top_k experts (-1: slot left
+    out, moe_plan's convention) and their softmax weights, slots per expert and behind them the tokens that take
+    part, the softmax's sums over those, and the balance loss.  mask [tokens]: False for padding tokens."""
+    tokens, experts = logits.shape
+    _route_mask(mask, tokens)
+    _check_workspace(workspace)
+    _on_current_device(logits, mask, workspace)
+    lt, ld = dtype_code(logits), _row_ld(logits, "logits")
+    _keep(stream, logits, mask, workspace)
+    workspace = _workspace(workspace, mx_moe_route_workspace_size(tokens, experts, top_k), logits, stream)
+    ids = _empty((tokens, top_k), torch.int32, logits, stream)
+    weights = _empty((tokens, top_k), torch.float32, logits, stream)
+    counts = _empty((experts + 1,), torch.int32, logits, stream)
+    sums = _empty((experts,), torch.float32, logits, stream)
+    loss = _empty((1,), torch.float32, logits, stream)
+    mx_moe_route(logits, lt, ld, mask, tokens, experts, top_k, int(bool(renormalize)), ids, weights, counts, sums,
+                 loss, workspace, _nbytes(workspace), stream)
+    return ids, weights, counts, sums, loss
+
+
+def moe_route_bwd(logits: torch.Tensor, ids, counts, dweights=None, dloss=None, renormalize=True, mask=None,
+                  out=None, stream=None):
+    """dlogits [tokens, experts] (logits' type) of moe_route, given its ids and counts and the gradients of its
+    weights (moe_combine_bwd's dweights) and of its loss ([1] float32), each None for 0."""
+    tokens, experts = logits.shape
+    _route_mask(mask, tokens)
+    if ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != tokens or not ids.is_contiguous():
+        raise ValueError("ids must be int32 [tokens, top_k]")
+    if counts.dtype != torch.int32 or counts.shape != (experts + 1,) or not counts.is_contiguous():
+        raise ValueError("counts must be int32 [experts + 1]")
+    if dweights is not None and (dweights.dtype != torch.float32 or dweights.shape != ids.shape
+                                 or not dweights.is_contiguous()):
+        raise ValueError("dweights must be float32 like ids")
+    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
+        raise ValueError("dloss must be one float32")
+    _on_current_device(logits, ids, counts, dweights, dloss, mask, out)
+    lt, ld = dtype_code(logits), _row_ld(logits, "logits")
+    d = _output(out, (tokens, experts), logits.dtype, logits, stream)
+    _keep(stream, logits, ids, counts, dweights, dloss, mask, out)
+    mx_moe_route_bwd(logits, lt, ld, mask, tokens, experts, ids.shape[1], int(bool(renormalize)), ids, counts,
+                     dweights, dloss, d, _row_ld(d, "out"), stream)
+    return d

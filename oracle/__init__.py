@@ -6,3 +6,4 @@ import this package. It shares no code, tables or constants with the HIP path.
 """
 from .mxfp4 import *  # noqa: F401,F403
 from .moe import *  # noqa: F401,F403
+from .eight import *  # noqa: F401,F403

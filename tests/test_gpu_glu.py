@@ -1,0 +1,170 @@
+"""GPU checks of the gated activation and its gradient against the oracle; the checkpoint and the packed
+outputs are exact.
+
+Tolerances, with u = 2^-24 the largest error of one float32 rounding.  Gate g / (1 + e^-g): the
+exponential within 2 steps (4 u), the sum, the division and the product with u one rounding each: 8 u of
+the value.  Its derivative s + s (g (1 - s)): s carries 6 u, 1 - s an error of 7 u against 1, so the
+sum is off by at most 24 u s (1 + |g|).  g Phi(g): erfc within 8 steps (16 u); its argument, off by 2 u
+of itself, moves erfc(y) by 2 y^2 2u = 2 g^2 u at most; so (20 + 4 g^2) u of the value, and the same of
+both terms of the derivative.  The rounding to the output type adds 2^-24 or 2^-8 of the value.  2^-115
+covers factors below the normal range."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from mxfp4_microscaling_quantization_amd import mx
+from tests.gpu_util import DEV, assert_bytes_equal, host, oracle_input, to_dev_f32
+from tests.test_gpu_moe_routing import STEP, stored, strided, torch_type, values
+from tests.test_gpu_quant8 import padded, same
+
+pytestmark = pytest.mark.gpu
+
+U, TINY = 2.0 ** -24, 2.0 ** -115
+SIZES = [(1, 1), (1, 2880), (3, 8), (5, 33), (4, 127), (17, 128), (2, 130), (70, 264), (33, 96), (300, 40), (9, 1504)]
+
+
+def gate_error(g, act):
+    return (8 if act == O.SILU else 20 + 4 * g * g) * U
+
+
+def slope_error(g, act):
+    """Absolute error of act'(g)."""
+    if act == O.SILU:
+        return 24 * U * sigmoid(g) * (1 + np.abs(g))
+    phi = O.activation(g, act)[0] / np.where(g == 0, 1, g)
+    phi = np.where(g == 0, 0.5, phi)
+    return (20 + 4 * g * g) * U * (phi + np.abs(g) * np.exp(-g * g / 2) / np.sqrt(2 * np.pi))
+
+
+def sigmoid(g):
+    e = np.exp(-np.abs(g))
+    return np.where(g >= 0, 1 / (1 + e), e / (1 + e))
+
+
+def within(got, want, tol):
+    err = np.abs(values(got) - want)
+    bad = ~(err <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:4], values(got)[bad][:4], want[bad][:4], (err / tol)[bad].max())
+
+
+def inputs(rng, rows, cols):
+    z = rng.standard_normal((rows, 2 * cols)) * 3
+    z[rng.random(z.shape) < 0.02] *= 20
+    z[rng.random(z.shape) < 0.02] = 0.0
+    return z
+
+
+@pytest.mark.parametrize("act", [O.SILU, O.GELU])
+@pytest.mark.parametrize("z_type,h_type", [("f32", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_forward_checkpoint_and_backward(rows, cols, z_type, h_type, act):
+    rng = np.random.default_rng(rows + cols)
+    a = stored(inputs(rng, rows, cols), z_type)
+    z = oracle_input(a, z_type).astype(np.float64)
+    g, u = z[:, :cols], z[:, cols:]
+    x = strided(a, z_type, 2 * cols + 3)
+    want = O.glu(z, act)
+    h, kept = mx.glu(x, act, checkpoint=True, out_dtype=torch_type(h_type))
+    within(h, want, gate_error(g, act) * np.abs(want) + STEP[h_type] * np.abs(want) + TINY)
+    assert torch.equal(h, mx.glu(x, act, out_dtype=torch_type(h_type)))
+    same(kept, O.quantize8(z.reshape(2 * rows, cols)), "checkpoint")
+    # backward, from what the checkpoint holds
+    v = O.dequantize8(*O.quantize8(z.reshape(2 * rows, cols))).reshape(rows, 2, cols)
+    g, u = v[:, 0], v[:, 1]
+    d = stored(rng.standard_normal((rows, cols)), h_type)
+    dh = oracle_input(d, h_type).astype(np.float64)
+    for dz_type in ("f32", "bf16"):
+        dz = mx.glu_bwd(strided(d, h_type, cols + 1), kept, act, out_dtype=torch_type(dz_type))
+        want = O.glu_bwd(dh, g, u, act)
+        tol = np.concatenate((np.abs(dh * u) * slope_error(g, act) + 2 * U * np.abs(want[:, :cols]),
+                              (gate_error(g, act) + U) * np.abs(want[:, cols:])), axis=1)
+        within(dz, want, tol + STEP[dz_type] * np.abs(want) + TINY)
+
+
+@pytest.mark.parametrize("act", [O.SILU, O.GELU])
+def test_packed_outputs_are_those_of_the_quantizers(act):
+    for rows, cols in ((1, 32), (5, 96), (130, 288), (3, 2880), (64, 1536)):
+        z = to_dev_f32(inputs(np.random.default_rng(cols), rows, cols))
+        h = mx.glu(z, act)
+        for got, want in ((mx.glu_quantize8(z, act), mx.quantize8(h)), (mx.glu_quantize(z, act), mx.quantize(h))):
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (rows, cols)
+        q, kept = mx.glu_quantize8(z, act, checkpoint=True)
+        _, kept4 = mx.glu_quantize(z, act, checkpoint=True)
+        want = mx.quantize8(z.reshape(2 * rows, cols))
+        assert all(torch.equal(a, b) for k in (kept, kept4) for a, b in zip(k, want))
+    for rows, cols in ((3, 1), (7, 50), (2, 333)):      # 8-bit rows of any length
+        z = to_dev_f32(inputs(np.random.default_rng(cols), rows, cols))
+        assert all(torch.equal(a, b) for a, b in zip(mx.glu_quantize8(z, act), mx.quantize8(mx.glu(z, act))))
+
+
+@pytest.mark.parametrize("live", [-3, 0, 1, 5, 8, 100])
+def test_rows_behind_the_counter_stay(live):
+    rows, cols = 8, 160
+    z = to_dev_f32(inputs(np.random.default_rng(0), rows, cols))
+    n, offs = min(max(live, 0), rows), torch.tensor([0, 3, live], device=DEV)
+    h, kept = mx.glu(z, checkpoint=True)
+    full = (h, mx.glu_bwd(h, kept), *mx.glu_quantize(z), *mx.glu_quantize8(z))
+    out = tuple(torch.full_like(t, 7) for t in full)
+    mx.glu(z, rows=offs[-1:], out=out[0])
+    mx.glu_bwd(h, kept, rows=offs[-1:], out=out[1])
+    mx.glu_quantize(z, rows=offs[-1:], out=out[2:4])
+    mx.glu_quantize8(z, rows=offs[-1:], out=out[4:6])
+    for got, want in zip(out, full):
+        assert torch.equal(got[:n], want[:n]) and torch.all(got[n:] == 7)
+
+
+def test_special_values():
+    """Zeros, the largest magnitudes, infinities and NaN: the limits of act(g) u and no NaN from far g."""
+    g = np.array([0.0, -0.0, 100.0, -100.0, 3e38, -3e38, np.inf, np.nan, 1.0, 1.0])
+    z = np.concatenate((g, np.r_[np.full(8, 2.0), np.inf, np.nan]))[None].astype(np.float32)
+    for act in (O.SILU, O.GELU):
+        h = values(mx.glu(to_dev_f32(z), act))[0]
+        assert h[0] == 0 and h[1] == 0 and h[2] == 200 and abs(h[3]) < 1e-30 and np.isinf(h[4]) and h[5] == 0
+        assert h[6] == np.inf and np.isnan(h[7]) and h[8] == np.inf and np.isnan(h[9])
+    # a block of the checkpoint that is not finite makes its gradients NaN, the others stay
+    z = np.random.default_rng(1).standard_normal((2, 512)).astype(np.float32)
+    z[0, 3] = np.inf
+    _, kept = mx.glu(to_dev_f32(z), checkpoint=True)
+    dz = host(mx.glu_bwd(torch.ones((2, 256), device=DEV), kept))
+    assert np.isnan(dz[0, :128]).all() and np.isnan(dz[0, 256:384]).all()
+    assert np.isfinite(dz[0, 128:256]).all() and np.isfinite(dz[0, 384:]).all() and np.isfinite(dz[1]).all()
+
+
+@pytest.mark.parametrize("act", [O.SILU, O.GELU])
+def test_gradient_against_differences_of_the_forward(act):
+    """On values that the checkpoint holds exactly; a step of 2^-6 of float32 values of h around 1."""
+    rng = np.random.default_rng(2)
+    z = rng.integers(-12, 13, (4, 32)) / 8.0
+    dh = rng.integers(1, 5, (4, 16)) * 1.0
+    _, kept = mx.glu(to_dev_f32(z), act, checkpoint=True)
+    dz = values(mx.glu_bwd(to_dev_f32(dh), kept, act))
+    step = 2.0 ** -6
+    for i, j in ((0, 0), (1, 5), (2, 15), (3, 16), (0, 31), (2, 20)):
+        up, down = z.copy(), z.copy()
+        up[i, j] += step
+        down[i, j] -= step
+        diff = ((values(mx.glu(to_dev_f32(up), act)) - values(mx.glu(to_dev_f32(down), act))) * dh).sum() / (2 * step)
+        # third derivatives are below 1, |u| <= 1.5, |dh| <= 4: step^2 / 6 of 6; float32 values of h below 4
+        assert abs(diff - dz[i, j]) < 6 * step ** 2 / 6 + 4 * 4 * 16 * 2.0 ** -23 / step
+
+
+def test_rows_past_2_31_elements_and_calls_on_a_stream():
+    rows, cols = 33000, 33000
+    z = torch.zeros((rows, 2 * cols), dtype=torch.bfloat16, device=DEV)
+    last = torch.randn((2, 2 * cols), device=DEV).to(torch.bfloat16)
+    z[-2:] = last
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    h, kept = mx.glu(z, checkpoint=True, out_dtype=torch.bfloat16, stream=side)
+    dz = mx.glu_bwd(h, kept, stream=side)
+    side.synchronize()
+    want_h, want_kept = mx.glu(last, checkpoint=True, out_dtype=torch.bfloat16)
+    assert torch.equal(h[-2:], want_h) and all(torch.equal(a[-4:], b) for a, b in zip(kept, want_kept))
+    assert torch.equal(dz[-2:], mx.glu_bwd(want_h, want_kept)) and not h[:-2].any()
+
+
+def test_empty_sizes():
+    for rows, cols in ((0, 32), (3, 0)):
+        h, kept = mx.glu(torch.zeros((rows, 2 * cols), device=DEV), checkpoint=True)
+        assert h.shape == (rows, cols) and mx.glu_bwd(h, kept).shape == (rows, 2 * cols)
