@@ -111,10 +111,10 @@ __device__ __forceinline__ void lds_load4(const uint8_t* base, uint32_t off, uin
 }
 // A load from any address: the last step of a contraction takes its missing codes from here.
 __device__ const uint4 kZero16 = {0, 0, 0, 0};
-__device__ __forceinline__ void lds_load16_at(const uint8_t* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+__device__ __forceinline__ void lds_load16_at(bool yes, const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %2\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1"
                :
-               : "s"(lds), "v"(p)
+               : "s"(lds), "v"(p), "s"(__builtin_amdgcn_readfirstlane(yes ? -1 : 0))
                : "memory", "m0");
 }
 // The same loads if `yes`, without a branch (a branch between the products of a step would let the
@@ -136,15 +136,301 @@ __device__ __forceinline__ void lds_load4_if(bool yes, const uint8_t* base, uint
 __device__ __forceinline__ int64_t lmin8(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // ============================================================== tiles
-// A workgroup of 2 x 2 waves owns a T x T tile of C and walks K in steps of 64 through a ring of
+// A tile's outputs.  A lane holds C[m = lr][n = 8 q + 4 lh + i] of each 32x32 accumulator.  A wave stages
+// 64 rows at a time in its quarter of the idle LDS ring (16-byte chunks XORed with row & 15) and stores
+// whole row segments.
+template <int W, typename TY, bool SLICED>
+__device__ __forceinline__ void store_tile8(const Gemm8Args& g, const v16f (&acc)[W][W], uint8_t* ring, int64_t m0,
+                                            int64_t n0, int slice) {
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave >> 1) * W * 32, wn = (wave & 1) * W * 32;
+  constexpr int CH = W * 8;                  // 16-byte chunks of float32 a row
+  constexpr int RB = CH * 16;
+  constexpr int V = sizeof(TY) == 2 ? 8 : 4; // outputs a lane and store
+  constexpr int LPR = W * 32 / V;            // lanes a row
+  wait_vm<0>();
+  __syncthreads();
+  uint8_t* stg = ring + wave * 64 * RB;
+  TY* c = static_cast<TY*>(g.c) + (SLICED ? (int64_t)slice * g.M * g.N : 0);
+#pragma unroll
+  for (int p = 0; p < W / 2; ++p) {
+#pragma unroll
+    for (int bb = 0; bb < 2; ++bb) {
+      const int r = bb * 32 + lr;
+#pragma unroll
+      for (int a = 0; a < W; ++a)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v16f& t = acc[a][2 * p + bb];
+          *reinterpret_cast<float4*>(stg + r * RB + (((a * 8 + q * 2 + lh) ^ (r & 15)) * 16)) =
+              make_float4(t[4 * q] * g.alpha, t[4 * q + 1] * g.alpha, t[4 * q + 2] * g.alpha,
+                          t[4 * q + 3] * g.alpha);
+        }
+    }
+#pragma unroll 4
+    for (int it = 0; it < LPR; ++it) {
+      const int r = it * (64 / LPR) + lane / LPR, col = (lane % LPR) * V;
+      float v[V];
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q)
+        *reinterpret_cast<float4*>(v + 4 * q) =
+            *reinterpret_cast<const float4*>(stg + r * RB + (((col / 4 + q) ^ (r & 15)) * 16));
+      const int64_t m = m0 + wm + p * 64 + r, n = n0 + wn + col;
+      if (m < g.M && n < g.N) store_run8<TY, V, SLICED>(c + m * g.ldc + n, v, g.N - n);
+    }
+  }
+}
+
+// Which tile and slice a workgroup takes.  Workgroups are dealt round-robin over 8 dies: consecutive
+// tiles go to one die; tile rows are walked four together, so that B tiles are read again from L2.
+struct Place8 {
+  int64_t m0, n0, k0, klen;
+  int slice;
+};
+template <int T, bool SLICED>
+__device__ __forceinline__ Place8 place8(const Gemm8Args& g) {
+  Place8 p;
+  const int tiles = g.tiles_m * g.tiles_n, total = gridDim.x, q = total / 8, r = total % 8;
+  const int x = (int)blockIdx.x % 8;
+  int id = x * q + min(x, r) + (int)blockIdx.x / 8;
+  p.slice = SLICED ? id / tiles : 0;
+  id -= p.slice * tiles;
+  constexpr int kRows = 4;
+  const int span = kRows * g.tiles_n, first_m = id / span * kRows;
+  const int gm = min(g.tiles_m - first_m, kRows);
+  p.m0 = (int64_t)(first_m + id % span % gm) * T;
+  p.n0 = (int64_t)(id % span / gm) * T;
+  p.k0 = SLICED ? p.slice * g.slice : 0;
+  p.klen = SLICED ? lmin8(g.slice, g.K - p.k0) : g.K;
+  return p;
+}
+
+// How many of n things are due before turn `at` of `turns`.
+constexpr int due8(int at, int turns, int n) { return at <= 0 ? 0 : (at >= turns ? n : n * at / turns); }
+
+// The 8-bit instructions' kernel: 2 x 2 waves, T x T outputs, (T/64)^2 accumulators of 32x32 a wave.
+//
+// K goes by in steps of 128, two stages in LDS: rows of 128 bytes, so that a load instruction takes
+// eight whole cache lines (64-byte rows, sixteen half lines, cost the address unit twice the time: 455
+// us where lines take LINE_TIME, 8192 x 14336 x 4096); the 16-byte chunks of row r stand in the order
+// c ^ ((r >> 1) & 7), which spreads a fragment read over all banks.
+//
+// A wave holds the A fragments of a whole step and goes through its W column tiles of B one after the
+// other ("turns" of 2 W products).  In turn b it reads column tile b + 1, in the second half of a step
+// also the next step's A.  So A's part of a stage is free as soon as its step begins, and B's tile by
+// tile; the loads of step p + 2 follow at once, in two groups, each behind a barrier that ends the reads
+// of what it overwrites:
+//   first half of step p    B tiles W/2+1 .. W-1 of step p + 1, A of step p + 2
+//   second half of step p   B tiles 0 .. W/2 of step p + 2
+// Everything is on its way for a step at least before the barrier in front of its first read, where
+// its wave waits for it.  Between two products of a wave there is room for a read or a load: 64 cycles.
+template <int T, typename TY, bool SLICED>
+__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm8Args g) {
+  constexpr int W = T / 64;
+  constexpr int LA = T / 32;                   // A loads a wave and step (8 rows each)
+  constexpr int NB = W / 2 + 1;                // B tiles loaded in the second half of a step (2 loads each)
+  constexpr int kFirst = 2 * (W - NB) + LA, kSecond = 2 * NB;
+  constexpr int LS = T / 128;                  // scale loads a wave and four steps (64 rows each)
+  constexpr int STAGE = 2 * T * 128;
+  __shared__ __align__(16) uint8_t ring[2 * STAGE];
+  __shared__ __align__(16) uint32_t s_scale[2][2 * T];
+
+  const Place8 at = place8<T, SLICED>(g);
+  const int64_t m0 = at.m0, n0 = at.n0, klen = at.klen;
+  const int KT = (int)((klen + 127) / 128);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave >> 1) * (T / 2), wn = (wave & 1) * (T / 2);
+  const int lr = lane & 31, lh = lane >> 5;
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(lds8_ptr_t)ring;
+  const uint32_t scale0 = (uint32_t)(uintptr_t)(lds8_ptr_t)s_scale;
+
+  // Sources, rows past the matrix clamped to its last (they feed outputs that are not stored).  A
+  // wave loads T/4 rows of A, and of each B tile (32 rows of either half) 16 rows.
+  const uint8_t* abase = g.a + m0 * g.lda + at.k0;
+  const uint8_t* bbase = g.b + n0 * g.ldb + at.k0;
+  const int64_t alast = g.M - m0 - 1, blast = g.N - n0 - 1;
+  auto a_row = [&](int j) { return wave * (T / 4) + j * 8; };
+  auto b_row = [&](int j) { return (wave >> 1) * (T / 2) + (j >> 1) * 32 + (wave & 1) * 16 + (j & 1) * 8; };
+  const int dr = lane >> 3;
+  auto chunk = [&](int row0) { return ((lane & 7) ^ (((row0 + dr) >> 1) & 7)) * 16; };  // of this lane's load
+  uint32_t aoff[LA], boff[2 * W];
+#pragma unroll
+  for (int j = 0; j < LA; ++j) aoff[j] = (uint32_t)(lmin8(a_row(j) + dr, alast) * g.lda) + chunk(a_row(j));
+#pragma unroll
+  for (int j = 0; j < 2 * W; ++j) boff[j] = (uint32_t)(lmin8(b_row(j) + dr, blast) * g.ldb) + chunk(b_row(j));
+  const bool isA = wave < 2;
+  const uint8_t* sbase = (isA ? g.sa + m0 * g.lsa : g.sb + n0 * g.lsb) + at.k0 / 128;
+  uint32_t soff[LS];
+#pragma unroll
+  for (int j = 0; j < LS; ++j)
+    soff[j] = (uint32_t)(lmin8((wave & 1) * (T / 2) + j * 64 + lane, isA ? alast : blast) * (isA ? g.lsa : g.lsb));
+
+  // A load of step p (j < LA: A's j-th, else B's).  SURE: the step exists and is whole.  Else chunks
+  // past the contraction are zeros, and steps past it are not loaded.
+  auto issue_one = [&](int p, int j, auto SURE) {
+    const int row0 = j < LA ? a_row(j) : T + b_row(j - LA);
+    const uint32_t to = ring0 + (uint32_t)(p & 1) * STAGE + (uint32_t)row0 * 128;
+    const uint8_t* base = (j < LA ? abase : bbase) + (int64_t)p * 128;
+    const uint32_t off = j < LA ? aoff[j] : boff[j - LA];
+    if constexpr (decltype(SURE)::value) {
+      lds_load16(base, off, to);
+    } else {
+      const int c = chunk(j < LA ? a_row(j) : b_row(j - LA));
+      lds_load16_at(p < KT, (int64_t)p * 128 + c < klen ? base + off : reinterpret_cast<const uint8_t*>(&kZero16), to);
+    }
+  };
+  auto issue_first = [&](int p, int i, auto SURE) {   // load i of the first half of step p
+    if (i < 2 * (W - NB)) issue_one(p + 1, LA + 2 * NB + i, SURE);
+    else issue_one(p + 2, i - 2 * (W - NB), SURE);
+  };
+  auto issue_scales = [&](int grp, bool yes) {        // of steps 4 grp .. 4 grp + 3
+#pragma unroll
+    for (int j = 0; j < LS; ++j)
+      lds_load4_if(yes, sbase + grp * 4, soff[j],
+                   scale0 + (uint32_t)((grp & 1) * 2 * T + wave * (T / 2) + j * 64) * 4);
+  };
+
+  v16f acc[W][W];
+#pragma unroll
+  for (int a = 0; a < W; ++a)
+#pragma unroll
+    for (int b = 0; b < W; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+
+  // Fragments: both 64-halves of the rows of A, of this step and the next, and of two B tiles.  Half h of a
+  // row's 128 bytes: chunks 4 h + 2 lh and the next.
+  v8i fa[2][W][2], fb[2][2];
+  uint32_t sa[W], sb[W], na[W], nb[W];
+  const uint8_t *pa[4], *pb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = ((4 * (i >> 1) + 2 * lh + (i & 1)) ^ ((lr >> 1) & 7)) * 16;
+    pa[i] = ring + (wm + lr) * 128 + c;
+    pb[i] = ring + (T + wn + lr) * 128 + c;
+  }
+  auto put = [&](v8i& f, int e, const v4i& c) {
+    f = e ? __builtin_shufflevector(f, __builtin_shufflevector(c, c, 0, 1, 2, 3, 0, 1, 2, 3), 0, 1, 2, 3, 8, 9, 10, 11)
+          : __builtin_shufflevector(c, c, 0, 1, 2, 3, -1, -1, -1, -1);
+  };
+  auto read_a = [&](auto P, int p, int i) {           // read i of 4 W: tile i / 4
+    constexpr int q = decltype(P)::value;
+    put(fa[q][i >> 2][(i >> 1) & 1], i & 1,
+        *reinterpret_cast<const v4i*>(pa[i & 3] + (p & 1) * STAGE + (i >> 2) * 32 * 128));
+  };
+  auto read_b = [&](int p, int tile, int i) {         // read i of 4
+    put(fb[tile & 1][i >> 1], i & 1, *reinterpret_cast<const v4i*>(pb[i] + (p & 1) * STAGE + tile * 32 * 128));
+  };
+  auto read_scales = [&](int p, uint32_t (&x)[W], uint32_t (&y)[W]) {
+    const uint8_t* s = reinterpret_cast<const uint8_t*>(s_scale[(p >> 2) & 1]) + (p & 3);
+#pragma unroll
+    for (int t = 0; t < W; ++t) {
+      x[t] = s[(wm + t * 32 + lr) * 4];
+      y[t] = s[(T + wn + t * 32 + lr) * 4];
+    }
+  };
+  auto barrier = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // Prologue, in the order of the steps: scales, step 0 but for its last B tiles; those and A of step 1;
+  // the first B tiles of step 1.
+  issue_scales(0, true);
+  using No = std::false_type;
+#pragma unroll
+  for (int j = 0; j < LA + 2 * NB; ++j) issue_one(0, j, No{});
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) issue_first(-1, i, No{});
+#pragma unroll
+  for (int i = 0; i < kSecond; ++i) issue_one(1, LA + i, No{});
+  if (KT > 1) wait_vm<2 * (NB - 1) + kFirst + kSecond>();
+  else wait_vm<0>();
+  barrier();
+  read_scales(0, sa, sb);
+#pragma unroll
+  for (int i = 0; i < 4 * W; ++i) read_a(std::integral_constant<int, 0>{}, 0, i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) read_b(0, 0, i);
+
+  // Turn B of step p, p % 2 == P.  SURE: steps p + 1 and p + 2 exist and are whole.
+  auto turn = [&](int p, auto P, auto B, auto SURE) {
+    constexpr int q = decltype(P)::value, b = decltype(B)::value;
+    constexpr bool sure = decltype(SURE)::value;
+    constexpr bool second = b >= W / 2;
+    constexpr int kTurn = 2 * W, kHalf = kTurn * W / 2;  // products
+    if constexpr (b == 0) {  // B tiles 1 .. W/2 of this step have landed
+      if (sure || p + 1 < KT) wait_vm<kFirst + kSecond>();
+      else wait_vm<2 * (W - NB)>();
+      barrier();
+      issue_scales((p >> 2) + 1, (p & 3) == 0 && p + 4 < KT);
+    }
+    if constexpr (b == W / 2) {  // the other B tiles, A and B tile 0 of the next step have landed
+      if (sure || p + 2 < KT) wait_vm<2 * (NB - 1) + kFirst>();
+      else if (p + 1 < KT) wait_vm<2 * (NB - 1) + 2 * (W - NB)>();
+      else wait_vm<0>();
+      barrier();
+    }
+    if constexpr (b == W - 1) read_scales(p + 1, na, nb);
+    constexpr int kReads = second ? 4 + 8 : 4;  // of this turn
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) {
+      const int h = i / W, a = i % W;
+      acc[b][a] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[b & 1][h], fa[q][a][h], acc[b][a], kFmtE4m3,
+                                                                  kFmtE4m3, 0, (int)sb[b], 0, (int)sa[a]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int r = due8(i, kTurn, kReads); r < due8(i + 1, kTurn, kReads); ++r) {
+        if (r < 4) read_b(b == W - 1 ? p + 1 : p, (b + 1) % W, r);
+        else read_a(std::integral_constant<int, 1 - q>{}, p + 1, (b - W / 2) * 8 + r - 4);
+      }
+      const int done = (second ? b - W / 2 : b) * kTurn + i;
+      if constexpr (second) {
+#pragma unroll
+        for (int l = due8(done, kHalf, kSecond); l < due8(done + 1, kHalf, kSecond); ++l) issue_one(p + 2, LA + l, SURE);
+      } else {
+#pragma unroll
+        for (int l = due8(done, kHalf, kFirst); l < due8(done + 1, kHalf, kFirst); ++l) issue_first(p, l, SURE);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto step = [&](int p, auto P, auto SURE) {
+    turn(p, P, std::integral_constant<int, 0>{}, SURE);
+    turn(p, P, std::integral_constant<int, 1>{}, SURE);
+    if constexpr (W == 4) {
+      turn(p, P, std::integral_constant<int, 2>{}, SURE);
+      turn(p, P, std::integral_constant<int, 3>{}, SURE);
+    }
+#pragma unroll
+    for (int t = 0; t < W; ++t) sa[t] = na[t], sb[t] = nb[t];
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  int p = 0;
+  for (; (int64_t)(p + 4) * 128 <= klen; p += 2) {
+    step(p, I0{}, std::true_type{});
+    step(p + 1, I1{}, std::true_type{});
+  }
+  for (; p < KT; p += 2) {
+    step(p, I0{}, No{});
+    if (p + 1 < KT) step(p + 1, I1{}, No{});
+  }
+  store_tile8<W, TY, SLICED>(g, acc, ring, m0, n0, at.slice);
+}
+
+// The wide kernel.  A workgroup of 2 x 2 waves owns a T x T tile of C and walks K in steps of 64 through a ring of
 // four stages in LDS (codes [rows][64 bytes]; the 16-byte chunks of row r stand in the order
 // c ^ ((r >> 2) & 3), which spreads a fragment read over all banks).  A wave holds (T/64)^2
 // accumulators of 32x32 and the fragments of two steps: while the products of one step run, it
 // reads the next step's fragments and issues the loads of the step four ahead, between the
 // products.  One barrier a step: before it, each wave has its fragments of the step in registers
 // (so the step's stage is free) and its share of the next step's loads has landed.
-template <int T, typename TY, bool SLICED, bool TAIL, bool WIDE>
-__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm8Args g) {
+template <int T, typename TY, bool SLICED, bool TAIL>
+__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_wide(const Gemm8Args g) {
   constexpr int W = T / 64;                  // 32-row accumulators of a wave along m and n
   constexpr int LC = T / 32;                 // code loads a wave and step (16 rows each)
   constexpr int LS = T / 128;                // scale loads a wave and 8 steps (64 rows each)
@@ -152,20 +438,8 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm
   __shared__ __align__(16) uint8_t ring[4 * STAGE];
   __shared__ __align__(16) uint32_t s_scale[2][2 * T];
 
-  const int tiles = g.tiles_m * g.tiles_n;
-  int id = blockIdx.x;
-  {  // consecutive tiles to one die, whose workgroups are dealt round-robin over 8
-    const int total = gridDim.x, q = total / 8, r = total % 8, x = id % 8;
-    id = x * q + min(x, r) + id / 8;
-  }
-  const int slice = SLICED ? id / tiles : 0;
-  id -= slice * tiles;
-  constexpr int kRows = 4;  // tile rows walked together: B tiles are read again from L2
-  const int span = kRows * g.tiles_n, first_m = id / span * kRows;
-  const int gm = min(g.tiles_m - first_m, kRows);
-  const int64_t m0 = (int64_t)(first_m + id % span % gm) * T, n0 = (int64_t)(id % span / gm) * T;
-  const int64_t k0 = SLICED ? slice * g.slice : 0;
-  const int64_t klen = SLICED ? lmin8(g.slice, g.K - k0) : g.K;
+  const Place8 at = place8<T, SLICED>(g);
+  const int64_t m0 = at.m0, n0 = at.n0, k0 = at.k0, klen = at.klen;
   const int KT = (int)((klen + 63) / 64);
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -196,7 +470,7 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm
   auto issue_one = [&](int kt, int j, auto SURE) {
     const uint32_t to = ring0 + (uint32_t)(kt & 3) * STAGE + (uint32_t)(wave * (T / 2) + j * 16) * 64;
     const int64_t k = (int64_t)kt * 64;
-    if constexpr (TAIL) lds_load16_at(k + dc < klen ? base + k + off[j] : reinterpret_cast<const uint8_t*>(&kZero16), to);
+    if constexpr (TAIL) lds_load16_at(true, k + dc < klen ? base + k + off[j] : reinterpret_cast<const uint8_t*>(&kZero16), to);
     else if constexpr (decltype(SURE)::value) lds_load16(base + k, off[j], to);
     else lds_load16_if(kt < KT, base + k, off[j], to);
   };
@@ -276,25 +550,19 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm
     barrier();
     if constexpr (p == 0) issue_scales((kt >> 3) + 1, (kt & 7) == 0 && kt + 8 < KT);
     else read_scales(kt + 1, na, nb);
-    constexpr int kParts = WIDE ? 4 : 1, kProducts = kParts * W * W;
+    constexpr int kProducts = 4 * W * W;
 #pragma unroll
-    for (int j = 0; j < kParts; ++j) {
+    for (int j = 0; j < 4; ++j) {
       v8bf xa[W], xb[W];
-      if constexpr (WIDE) {
 #pragma unroll
-        for (int t = 0; t < W; ++t) {
-          xa[t] = widen8(fa[p][t][2 * j], fa[p][t][2 * j + 1], scale_of(sa[t]));
-          xb[t] = widen8(fb[p][t][2 * j], fb[p][t][2 * j + 1], scale_of(sb[t]));
-        }
+      for (int t = 0; t < W; ++t) {
+        xa[t] = widen8(fa[p][t][2 * j], fa[p][t][2 * j + 1], scale_of(sa[t]));
+        xb[t] = widen8(fb[p][t][2 * j], fb[p][t][2 * j + 1], scale_of(sb[t]));
       }
 #pragma unroll
       for (int i = 0; i < W * W; ++i) {
         const int a = i / W, b = i % W, at = j * W * W + i;
-        if constexpr (WIDE)
-          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb[a], xa[b], acc[a][b], 0, 0, 0);
-        else
-          acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[p][a], fa[p][b], acc[a][b], kFmtE4m3,
-                                                                      kFmtE4m3, 0, (int)sb[a], 0, (int)sa[b]);
+        acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb[a], xa[b], acc[a][b], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int r = 4 * W * at / kProducts; r < 4 * W * (at + 1) / kProducts; ++r)
@@ -321,45 +589,7 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm
     if (kt + 1 < KT) step(kt + 1, I1{}, std::false_type{});
   }
 
-  // Epilogue: a lane holds C[m = lr][n = 8 q + 4 lh + i] of each accumulator.  A wave stages 64
-  // rows at a time in its quarter of the idle ring (16-byte chunks XORed with row & 15) and stores
-  // whole row segments.
-  constexpr int CH = W * 8;                  // 16-byte chunks of float32 a row
-  constexpr int RB = CH * 16;
-  constexpr int V = sizeof(TY) == 2 ? 8 : 4; // outputs a lane and store
-  constexpr int LPR = W * 32 / V;            // lanes a row
-  wait_vm<0>();  // loads past the contraction (TAIL) have landed
-  __syncthreads();
-  uint8_t* stg = ring + wave * 64 * RB;
-  static_assert(4 * 64 * RB <= (int)sizeof(ring), "staging space");
-  TY* c = static_cast<TY*>(g.c) + (SLICED ? (int64_t)slice * g.M * g.N : 0);
-#pragma unroll
-  for (int p = 0; p < W / 2; ++p) {
-#pragma unroll
-    for (int bb = 0; bb < 2; ++bb) {
-      const int r = bb * 32 + lr;
-#pragma unroll
-      for (int a = 0; a < W; ++a)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const v16f& t = acc[a][2 * p + bb];
-          *reinterpret_cast<float4*>(stg + r * RB + (((a * 8 + q * 2 + lh) ^ (r & 15)) * 16)) =
-              make_float4(t[4 * q] * g.alpha, t[4 * q + 1] * g.alpha, t[4 * q + 2] * g.alpha,
-                          t[4 * q + 3] * g.alpha);
-        }
-    }
-#pragma unroll 4
-    for (int it = 0; it < LPR; ++it) {
-      const int r = it * (64 / LPR) + lane / LPR, col = (lane % LPR) * V;
-      float v[V];
-#pragma unroll
-      for (int q = 0; q < V / 4; ++q)
-        *reinterpret_cast<float4*>(v + 4 * q) =
-            *reinterpret_cast<const float4*>(stg + r * RB + (((col / 4 + q) ^ (r & 15)) * 16));
-      const int64_t m = m0 + wm + p * 64 + r, n = n0 + wn + col;
-      if (m < g.M && n < g.N) store_run8<TY, V, SLICED>(c + m * g.ldc + n, v, g.N - n);
-    }
-  }
+  store_tile8<W, TY, SLICED>(g, acc, ring, m0, n0, at.slice);
 }
 
 // C = alpha times the slices' sums, in their order.
@@ -540,8 +770,12 @@ static int launch_tiles(Gemm8Args g, hipStream_t st) {
   g.tiles_m = (int)tm;
   g.tiles_n = (int)tn;
   const dim3 grid((unsigned)(tm * tn * g.slices));
-  if (g.K % 64) k_gemm8_tile<T, TY, SLICED, true, WIDE><<<grid, 256, 0, st>>>(g);
-  else k_gemm8_tile<T, TY, SLICED, false, WIDE><<<grid, 256, 0, st>>>(g);
+  if constexpr (!WIDE) {
+    k_gemm8_tile<T, TY, SLICED><<<grid, 256, 0, st>>>(g);
+  } else {
+    if (g.K % 64) k_gemm8_wide<T, TY, SLICED, true><<<grid, 256, 0, st>>>(g);
+    else k_gemm8_wide<T, TY, SLICED, false><<<grid, 256, 0, st>>>(g);
+  }
   return launch_status();
 }
 
