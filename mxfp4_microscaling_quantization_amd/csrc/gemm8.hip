@@ -28,6 +28,7 @@
 
 namespace mx {
 
+typedef int v2i __attribute__((ext_vector_type(2)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
@@ -62,25 +63,31 @@ __device__ __forceinline__ v8bf widen8(uint32_t lo, uint32_t hi, float scale) {
   return v;
 }
 
-// The first n of V consecutive outputs at T's alignment.  Outputs go past the caches' replacement
-// (nontemporal) where the next launch does not read them.
-template <typename T, int V, bool KEEP>
-__device__ __forceinline__ void store_run8(T* p, const float* v, int64_t n) {
-  typedef T vec __attribute__((ext_vector_type(V)));
-  typedef vec avec __attribute__((aligned(sizeof(T))));
-  vec raw;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if constexpr (sizeof(T) == 2) raw[i] = (T)f32_to_bf16_rne(v[i]);
-    else raw[i] = v[i];
-  }
+// The first n of a run of consecutive outputs (RAW: their 8 or 16 bytes) at T's alignment.  Outputs go
+// past the caches' replacement (nontemporal) where the next launch does not read them.
+template <typename T, bool KEEP, typename RAW>
+__device__ __forceinline__ void store_run8(T* p, const RAW& raw, int64_t n) {
+  typedef RAW avec __attribute__((aligned(sizeof(T))));
+  constexpr int V = sizeof(RAW) / sizeof(T);
   if (n >= V) {
     if constexpr (KEEP) *reinterpret_cast<avec*>(p) = raw;
     else __builtin_nontemporal_store(raw, reinterpret_cast<avec*>(p));
   } else {
+    T v[V];
+    __builtin_memcpy(v, &raw, sizeof(raw));
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i < n) p[i] = raw[i];
+      if (i < n) p[i] = v[i];
+  }
+}
+template <typename T, bool KEEP>
+__device__ __forceinline__ void store_four8(T* p, const float* v, int64_t n) {
+  if constexpr (sizeof(T) == 2) {
+    const v2i raw = {(int)bf16_pair(v[0], v[1]), (int)bf16_pair(v[2], v[3])};
+    store_run8<T, KEEP>(p, raw, n);
+  } else {
+    const v4f raw = {v[0], v[1], v[2], v[3]};
+    store_run8<T, KEEP>(p, raw, n);
   }
 }
 
@@ -137,47 +144,55 @@ __device__ __forceinline__ int64_t lmin8(int64_t a, int64_t b) { return a < b ? 
 
 // ============================================================== tiles
 // A tile's outputs.  A lane holds C[m = lr][n = 8 q + 4 lh + i] of each 32x32 accumulator.  A wave stages
-// 64 rows at a time in its quarter of the idle LDS ring (16-byte chunks XORed with row & 15) and stores
-// whole row segments.
+// 64 rows at a time, in C's type, in its quarter of the idle LDS ring (16-byte chunks XORed with row & 15)
+// and stores whole row segments.  It is alone on its SIMD, and every instruction counts: with bf16 rounded by
+// integer operations after a float32 staging this took 6 of a tile's 57 us.
 template <int W, typename TY, bool SLICED>
-__device__ __forceinline__ void store_tile8(const Gemm8Args& g, const v16f (&acc)[W][W], uint8_t* ring, int64_t m0,
+__device__ __forceinline__ void store_tile8(const Gemm8Args& g, v16f (&acc)[W][W], uint8_t* ring, int64_t m0,
                                             int64_t n0, int slice) {
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave >> 1) * W * 32, wn = (wave & 1) * W * 32;
-  constexpr int CH = W * 8;                  // 16-byte chunks of float32 a row
-  constexpr int RB = CH * 16;
-  constexpr int V = sizeof(TY) == 2 ? 8 : 4; // outputs a lane and store
-  constexpr int LPR = W * 32 / V;            // lanes a row
+  constexpr int RB = W * 32 * sizeof(TY);    // bytes a row
+  constexpr int CH = RB / 16, MASK = CH < 16 ? CH - 1 : 15;
+  constexpr int V = 16 / sizeof(TY);         // outputs a lane and store
   wait_vm<0>();
   __syncthreads();
   uint8_t* stg = ring + wave * 64 * RB;
   TY* c = static_cast<TY*>(g.c) + (SLICED ? (int64_t)slice * g.M * g.N : 0);
+  const float alpha = g.alpha;
 #pragma unroll
   for (int p = 0; p < W / 2; ++p) {
+    auto stage = [&](auto SCALED) {
 #pragma unroll
-    for (int bb = 0; bb < 2; ++bb) {
-      const int r = bb * 32 + lr;
+      for (int bb = 0; bb < 2; ++bb) {
+        const int r = bb * 32 + lr;
 #pragma unroll
-      for (int a = 0; a < W; ++a)
+        for (int a = 0; a < W; ++a)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const v16f& t = acc[a][2 * p + bb];
-          *reinterpret_cast<float4*>(stg + r * RB + (((a * 8 + q * 2 + lh) ^ (r & 15)) * 16)) =
-              make_float4(t[4 * q] * g.alpha, t[4 * q + 1] * g.alpha, t[4 * q + 2] * g.alpha,
-                          t[4 * q + 3] * g.alpha);
-        }
-    }
+          for (int q = 0; q < 4; ++q) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = decltype(SCALED)::value ? acc[a][2 * p + bb][4 * q + e] * alpha : acc[a][2 * p + bb][4 * q + e];
+            if constexpr (sizeof(TY) == 2)
+              *reinterpret_cast<uint2*>(stg + r * RB + ((a * 4 + q) ^ (r & MASK)) * 16 + lh * 8) =
+                  make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+            else
+              *reinterpret_cast<float4*>(stg + r * RB + ((a * 8 + q * 2 + lh) ^ (r & MASK)) * 16) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+          }
+      }
+    };
+    // a float32 C has its factor always: a second copy of this would spill registers
+    if (sizeof(TY) == 2 && alpha == 1.0f) stage(std::false_type{});
+    else stage(std::true_type{});
 #pragma unroll 4
-    for (int it = 0; it < LPR; ++it) {
-      const int r = it * (64 / LPR) + lane / LPR, col = (lane % LPR) * V;
-      float v[V];
-#pragma unroll
-      for (int q = 0; q < V / 4; ++q)
-        *reinterpret_cast<float4*>(v + 4 * q) =
-            *reinterpret_cast<const float4*>(stg + r * RB + (((col / 4 + q) ^ (r & 15)) * 16));
-      const int64_t m = m0 + wm + p * 64 + r, n = n0 + wn + col;
-      if (m < g.M && n < g.N) store_run8<TY, V, SLICED>(c + m * g.ldc + n, v, g.N - n);
+    for (int it = 0; it < CH; ++it) {
+      const int r = it * (64 / CH) + lane / CH, at = lane % CH;
+      const v4i raw = *reinterpret_cast<const v4i*>(stg + r * RB + (at ^ (r & MASK)) * 16);
+      const int64_t m = m0 + wm + p * 64 + r, n = n0 + wn + at * V;
+      if (m < g.M && n < g.N) store_run8<TY, SLICED>(c + m * g.ldc + n, raw, g.N - n);
     }
   }
 }
@@ -615,7 +630,7 @@ __global__ __launch_bounds__(256) void k_gemm8_sum(const float* __restrict__ par
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] *= alpha;
-    store_run8<TY, 4, false>(c + m * ldc + n, s, N - n);
+    store_four8<TY, false>(c + m * ldc + n, s, N - n);
   }
 }
 
@@ -721,7 +736,7 @@ __global__ __launch_bounds__(rows8_waves(MT, NT) * 64) void k_gemm8_rows(const R
     float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = sum[e] * g.alpha;
-    if (m < g.M && n < g.N) store_run8<TY, 4, true>(static_cast<TY*>(g.c) + m * g.ldc + n, v, g.N - n);
+    if (m < g.M && n < g.N) store_four8<TY, true>(static_cast<TY*>(g.c) + m * g.ldc + n, v, g.N - n);
   }
 }
 
@@ -731,7 +746,7 @@ __global__ __launch_bounds__(256) void k_gemm8_zero(int64_t M, int64_t N, TY* __
   const int64_t runs = (N + 3) / 4, total = M * runs;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const float zero[4] = {};
-    store_run8<TY, 4, false>(c + i / runs * ldc + i % runs * 4, zero, N - i % runs * 4);
+    store_four8<TY, false>(c + i / runs * ldc + i % runs * 4, zero, N - i % runs * 4);
   }
 }
 
@@ -742,13 +757,25 @@ struct Plan8 {
   int64_t slice;
 };
 
-// Few rows take the wave-per-column kernel.  Tiles of 256 where they fill the compute units,
-// else tiles of 128, the contraction sliced where even they leave units idle.
-static Plan8 gemm8_plan(int64_t M, int64_t N, int64_t K) {
+// What a product takes in tiles of 256 (one workgroup a compute unit) and of 128 (two), by rounds of
+// workgroups over 256 compute units, in us: a round's own cost and that of 1024 values of K.  Measured,
+// bf16 C: 4096^3 60 us in tiles of 256, 72 in tiles of 128; 12608x1536x384 37 and 22; 6000x3000x1024 47 and
+// 36; 4093x2880x5760 68 and 85; float32 C: 4096^3 113 and 124, 5760x2880x4096 197 and 143.
+struct Cost8 {
+  float round256, k256, round128, k128;
+};
+constexpr Cost8 kCost8 = {12.0f, 11.0f, 3.0f, 8.2f}, kCost8Wide = {12.0f, 24.0f, 3.0f, 15.0f};
+
+// Few rows take the wave-per-column kernel.  Else tiles by their cost, and the contraction sliced where
+// even tiles of 128 leave compute units idle.
+static Plan8 gemm8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
   Plan8 p{M <= 64, false, 1, K};
   if (p.rows) return p;
-  p.big = cdiv(M, 256) * cdiv(N, 256) >= 200;
   const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
+  const Cost8& c = wide ? kCost8Wide : kCost8;
+  const float k = (float)K / 1024.0f;
+  p.big = tiles > 256 && (float)cdiv(cdiv(M, 256) * cdiv(N, 256), 256) * (c.round256 + c.k256 * k) <
+                             (float)cdiv(tiles, 512) * (c.round128 + c.k128 * k);
   if (p.big || tiles >= 256 || K < 2048) return p;
   const int64_t n = hmin(hmin(cdiv(512, tiles), K / 1024), 64);
   if (n < 2) return p;
@@ -758,9 +785,10 @@ static Plan8 gemm8_plan(int64_t M, int64_t N, int64_t K) {
   return p;
 }
 
-size_t gemm8_workspace(int64_t M, int64_t N, int64_t K) {
-  const Plan8 p = gemm8_plan(M, N, round16(K));
-  return p.slices > 1 ? (size_t)p.slices * M * N * sizeof(float) : 0;
+size_t gemm8_workspace(int64_t M, int64_t N, int64_t K) {  // for C of either type
+  const Plan8 p = gemm8_plan(M, N, round16(K), false), q = gemm8_plan(M, N, round16(K), true);
+  const int slices = p.slices > q.slices ? p.slices : q.slices;
+  return slices > 1 ? (size_t)slices * M * N * sizeof(float) : 0;
 }
 
 template <int T, typename TY, bool SLICED, bool WIDE>
@@ -796,7 +824,8 @@ static int gemm8_launch(Gemm8Args g, void* workspace, hipStream_t st) {
     k_gemm8_zero<TY><<<flat, 256, 0, st>>>(g.M, g.N, static_cast<TY*>(g.c), g.ldc);
     return launch_status();
   }
-  const Plan8 p = gemm8_plan(g.M, g.N, g.K);
+  constexpr bool kWide = sizeof(TY) == 4;
+  const Plan8 p = gemm8_plan(g.M, g.N, g.K, kWide);
   g.slices = p.slices;
   g.slice = p.slice;
   if (p.rows) {
@@ -805,7 +834,6 @@ static int gemm8_launch(Gemm8Args g, void* workspace, hipStream_t st) {
     if (g.M <= 48) return launch_rows<3, 2, TY>(g, st);
     return launch_rows<4, 2, TY>(g, st);
   }
-  constexpr bool kWide = sizeof(TY) == 4;
   if (p.big) return launch_tiles<256, TY, false, kWide>(g, st);
   if (p.slices == 1) return launch_tiles<128, TY, false, kWide>(g, st);
   Gemm8Args part = g;

@@ -51,6 +51,14 @@ __device__ __forceinline__ uint2 encode8(const float v[8], uint32_t byte) {
   return make_uint2(encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv));
 }
 
+// Two float32 values as bf16, nearest even, a in the low half: one instruction (rounding by integer
+// operations, as f32_to_bf16_rne, takes 15).
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+  const v2 r = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
 // Exact values of 8 codes times a scale (values past the float32 range come out infinite).
 __device__ __forceinline__ void decode8_e4m3(uint2 w, float scale, float v[8]) {
   const mx_v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false);
@@ -88,10 +96,15 @@ __device__ __forceinline__ void load8(const T* __restrict__ p, int64_t n, float 
 template <typename T>
 __device__ __forceinline__ void store8(T* __restrict__ p, int64_t n, const float v[8]) {
   T raw[8];
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (sizeof(T) == 2) raw[i] = (T)f32_to_bf16_rne(v[i]);
-    else raw[i] = v[i];
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = bf16_pair(v[2 * i], v[2 * i + 1]);
+      __builtin_memcpy(raw + 2 * i, &w, 4);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = v[i];
   }
   if (n >= 8) {
     __builtin_memcpy(p, raw, sizeof(raw));
