@@ -7,8 +7,7 @@
 // byte four times).  They add the products of eight neighbouring values with about 14 bits below the
 // largest of the eight before these sums meet in float32 (measured: a product 2^-13 of its neighbour
 // survives, 2^-14 is lost, between groups 2^-23 survives): 2e-5 of C's norm for normal operands,
-// against the 2e-3 of C's own rounding.  A float32 C and few rows take V_MFMA_F32_*_BF16 instead
-// (wide), half the rate: a code times a power of two is exact in bf16 (down to bits of 2^-133),
+// against the 2e-3 of C's own rounding.  A float32 C takes V_MFMA_F32_*_BF16 instead (wide), half the rate: a code times a power of two is exact in bf16 (down to bits of 2^-133),
 // and every product joins a float32 sum.
 //
 // Per lane an operand is 32 bytes of one row: row (lane % 32), k [32 (lane / 32), + 32) of the 64 of
@@ -138,6 +137,9 @@ __device__ __forceinline__ void lds_load4_if(bool yes, const uint8_t* base, uint
                : "s"(lds), "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(yes ? -1 : 0))
                : "memory", "m0");
 }
+__device__ __forceinline__ void lds_load4_at(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(p) : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
 __device__ __forceinline__ int64_t lmin8(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -228,7 +230,7 @@ constexpr int due8(int at, int turns, int n) { return at <= 0 ? 0 : (at >= turns
 //
 // K goes by in steps of 128, two stages in LDS: rows of 128 bytes, so that a load instruction takes
 // eight whole cache lines (64-byte rows, sixteen half lines, cost the address unit twice the time: 455
-// us where lines take LINE_TIME, 8192 x 14336 x 4096); the 16-byte chunks of row r stand in the order
+// us where lines take 405, 8192 x 14336 x 4096); the 16-byte chunks of row r stand in the order
 // c ^ ((r >> 1) & 7), which spreads a fragment read over all banks.
 //
 // A wave holds the A fragments of a whole step and goes through its W column tiles of B one after the
@@ -635,41 +637,76 @@ __global__ __launch_bounds__(256) void k_gemm8_sum(const float* __restrict__ par
 }
 
 // ============================================================== few rows
-// Up to 64 rows of A: the weights are read once, and that read is the bound.  A wave takes 16 NT
-// columns and up to 16 MT rows over units of 512 values of k, straight from memory into the
-// operand registers; the waves of a workgroup take turns over the units of the same columns, and
-// their sums meet in LDS in a fixed order.
+// Up to 64 rows of A: the weights are read once, and that read is the bound.  A wave takes 16 NT columns,
+// all rows (8 XD of them) and a part of K, and streams both operands through a ring of its own in LDS, four
+// steps of 128 deep: no barrier until the waves' sums meet.  The detour keeps loads whole: eight lanes take a
+// line of 128 bytes (into the operand registers directly, neighbouring lanes take different rows, 16 bytes a
+// clock: one row of 14336x4096 14.8 us, 12.1 so, 47 of 4096x14336 35 us, 22 so), and holds what is
+// in flight, 4 KB a step and up.  Layout of a step as in the tiles: row r's chunks in the order c ^ ((r >> 1) & 7).
+constexpr int kRowsDepth = 4;
+constexpr int rows8_step(int xd, int nt) { return (2 * nt + xd) * 1024; }         // bytes in LDS
+constexpr int rows8_scales(int xd, int nt) { return (16 * nt + 8 * xd + 63) / 64; } // loads per four steps
+constexpr int rows8_lds(int xd, int nt) { return kRowsDepth * rows8_step(xd, nt) + 2 * rows8_scales(xd, nt) * 256; }
+
 struct Rows8Args {
   Gemm8Args g;
-  int units, waves;
+  int steps, per;  // steps of the contraction and of a wave (a multiple of 4)
 };
 
-// Most waves of a workgroup: the operands of 512 values take registers.
-constexpr int rows8_waves(int mt, int nt) { return mt * nt > 1 ? 8 : 16; }
-
-template <int MT, int NT, typename TY>
-__global__ __launch_bounds__(rows8_waves(MT, NT) * 64) void k_gemm8_rows(const Rows8Args r) {
-  extern __shared__ __align__(16) float s_sum[];  // [waves - 1][MT * NT][64][4]
+template <int XD, int NT, typename TY>
+__global__ __launch_bounds__(512) void k_gemm8_rows(const Rows8Args r) {
+  constexpr int MT = (XD + 1) / 2;                       // row tiles of 16
+  constexpr int LC = 2 * NT + XD, LS = rows8_scales(XD, NT);
+  constexpr int STEP = rows8_step(XD, NT);
+  static_assert((kRowsDepth - 1) * LC + LS < 64 && MT * NT * 1024 <= kRowsDepth * STEP, "loads in flight, room for the sums");
+  extern __shared__ __align__(16) uint8_t lds[];
   const Gemm8Args& g = r.g;
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, kg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
-  const uint8_t* wp[NT];
-  const uint8_t* wsp[NT];
-  const uint8_t* xp[MT];
-  const uint8_t* xsp[MT];
+  uint8_t* ring = lds + wave * rows8_lds(XD, NT);
+  uint8_t* scales = ring + kRowsDepth * STEP;
+  const uint32_t ring0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds8_ptr_t)ring);
+  const int first = wave * r.per, end = min(first + r.per, r.steps);
+
+  const int dr = lane >> 3;
+  const uint8_t* wbase = g.b + n0 * g.ldb;
+  uint32_t off[LC];  // this lane's chunk of step 0: B's loads (from wbase), then A's
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t n = lmin8(n0 + t * 16 + l16, g.N - 1);
-    wp[t] = g.b + n * g.ldb;
-    wsp[t] = g.sb + n * g.lsb;
+  for (int j = 0; j < LC; ++j) {
+    const int row = (j < 2 * NT ? j : j - 2 * NT) * 8 + dr;
+    off[j] = (uint32_t)(j < 2 * NT ? lmin8(row, g.N - 1 - n0) * g.ldb : lmin8(row, g.M - 1) * g.lda) +
+             ((lane & 7) ^ ((row >> 1) & 7)) * 16;
   }
+  const uint8_t* ssrc[LS];  // scale rows: B's 16 NT, then A's
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int64_t m = lmin8(t * 16 + l16, g.M - 1);
-    xp[t] = g.a + m * g.lda;
-    xsp[t] = g.sa + m * g.lsa;
+  for (int j = 0; j < LS; ++j) {
+    const int row = j * 64 + lane;
+    ssrc[j] = row < 16 * NT ? g.sb + lmin8(n0 + row, g.N - 1) * g.lsb
+                            : g.sa + lmin8(row - 16 * NT, g.M - 1) * g.lsa;
   }
+  auto issue = [&](int s) {
+    if ((s & 3) == 0) {
+#pragma unroll
+      for (int j = 0; j < LS; ++j)
+        lds_load4_at(ssrc[j] + s, ring0 + kRowsDepth * STEP + (((s >> 2) & 1) * LS + j) * 256);
+    }
+    const int64_t k = (int64_t)s * 128;
+    const uint32_t to = ring0 + (s % kRowsDepth) * STEP;
+    if (k + 128 <= g.K) {
+#pragma unroll
+      for (int j = 0; j < LC; ++j) lds_load16((j < 2 * NT ? wbase : g.a) + k, off[j], to + j * 1024);
+    } else {  // the last step: chunks past the contraction are zeros
+      const int c0 = ((lane & 7) ^ ((dr >> 1) & 7)) * 16;
+#pragma unroll
+      for (int j = 0; j < LC; ++j) {  // odd loads: rows 8 further, the chunk's bit 2 flipped
+        const bool in = k + (j & 1 ? c0 ^ 64 : c0) < g.K;
+        lds_load16_at(true, in ? (j < 2 * NT ? wbase : g.a) + k + off[j] : reinterpret_cast<const uint8_t*>(&kZero16),
+                      to + j * 1024);
+      }
+    }
+  };
+
   v4f acc[NT][MT];
 #pragma unroll
   for (int a = 0; a < NT; ++a)
@@ -677,61 +714,68 @@ __global__ __launch_bounds__(rows8_waves(MT, NT) * 64) void k_gemm8_rows(const R
     for (int b = 0; b < MT; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[a][b][e] = 0.f;
-  for (int u = wave; u < r.units; u += r.waves) {
-    const int64_t k0 = (int64_t)u * 512;
-    uint32_t ws[NT], xs[MT];
+
 #pragma unroll
-    for (int t = 0; t < NT; ++t) ws[t] = *reinterpret_cast<const uint32_t*>(wsp[t] + u * 4);
+  for (int i = 0; i < kRowsDepth; ++i)
+    if (first + i < end) issue(first + i);
+  const uint8_t *at[2], *last[2];  // this lane's chunks of a tile; of the last one, which has 8 rows where XD is odd
 #pragma unroll
-    for (int t = 0; t < MT; ++t) xs[t] = *reinterpret_cast<const uint32_t*>(xsp[t] + u * 4);
-    v8i w[4][NT], x[4][MT];
-    const bool whole = k0 + 512 <= g.K;
+  for (int h = 0; h < 2; ++h) {
+    const int row = XD & 1 ? l16 & 7 : l16;
+    at[h] = ring + l16 * 128 + ((2 * kg + h) ^ ((l16 >> 1) & 7)) * 16;
+    last[h] = ring + (NT + MT - 1) * 2048 + row * 128 + ((2 * kg + h) ^ ((row >> 1) & 7)) * 16;
+  }
+  for (int s = first; s < end; ++s) {
+    // steps s + 1 .. s + 3 may stay in flight
+    if (s + 3 < end) wait_vm<3 * LC>();
+    else if (s + 2 < end) wait_vm<2 * LC>();
+    else if (s + 1 < end) wait_vm<LC>();
+    else wait_vm<0>();
+    asm volatile("" ::: "memory");
+    const int step = (s % kRowsDepth) * STEP;
+    v8i f[NT + MT];
+    uint32_t sc[NT + MT];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int t = 0; t < NT + MT; ++t) {
+      const v4i lo = *reinterpret_cast<const v4i*>((t < NT + MT - 1 ? at[0] + t * 2048 : last[0]) + step);
+      const v4i hi = *reinterpret_cast<const v4i*>((t < NT + MT - 1 ? at[1] + t * 2048 : last[1]) + step);
+      f[t] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      sc[t] = scales[((s >> 2) & 1) * LS * 256 + (t * 16 + l16) * 4 + (s & 3)];
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the step's room can be filled again
+    if (s + kRowsDepth < end) issue(s + kRowsDepth);
+    if constexpr (sizeof(TY) == 2) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t k = k0 + s * 128 + kg * 32 + h * 16;
-        const int64_t at = whole ? k : lmin8(k, g.K - 16);
-        auto take = [&](const uint8_t* p, v8i& f) {
-          const v4i c = *reinterpret_cast<const v4i*>(p + at);
+      for (int a = 0; a < NT; ++a)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[4 * h + e] = whole || k < g.K ? c[e] : 0;
-        };
-#pragma unroll
-        for (int t = 0; t < NT; ++t) take(wp[t], w[s][t]);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) take(xp[t], x[s][t]);
-      }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (k0 + s * 128 >= g.K) break;
+        for (int b = 0; b < MT; ++b)
+          acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f[a], f[NT + b], acc[a][b], kFmtE4m3, kFmtE4m3, 0,
+                                                                       (int)sc[a], 0, (int)sc[NT + b]);
+    } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v8bf wj[NT], xj[MT];
+        v8bf x[NT + MT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          wj[t] = widen8(w[s][t][2 * j], w[s][t][2 * j + 1], scale_of(ws[t] >> (8 * s) & 255u));
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          xj[t] = widen8(x[s][t][2 * j], x[s][t][2 * j + 1], scale_of(xs[t] >> (8 * s) & 255u));
+        for (int t = 0; t < NT + MT; ++t) x[t] = widen8(f[t][2 * j], f[t][2 * j + 1], scale_of(sc[t]));
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
           for (int b = 0; b < MT; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wj[a], xj[b], acc[a][b], 0, 0, 0);
+            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[a], x[NT + b], acc[a][b], 0, 0, 0);
       }
     }
   }
+  // The waves' sums, in their order.  The second eight rows of a half tile (XD odd) are not stored.
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
     for (int b = 0; b < MT; ++b)
-      *reinterpret_cast<v4f*>(s_sum + (((wave * NT + a) * MT + b) * 64 + lane) * 4) = acc[a][b];
+      *reinterpret_cast<v4f*>(ring + ((a * MT + b) * 64 + lane) * 16) = acc[a][b];
   __syncthreads();
-  for (int t = wave; t < NT * MT; t += r.waves) {
-    v4f sum = *reinterpret_cast<const v4f*>(s_sum + (t * 64 + lane) * 4);
-    for (int w = 1; w < r.waves; ++w)
-      sum += *reinterpret_cast<const v4f*>(s_sum + ((w * NT * MT + t) * 64 + lane) * 4);
+  for (int t = wave; t < NT * MT; t += waves) {
+    v4f sum = *reinterpret_cast<const v4f*>(lds + (t * 64 + lane) * 16);
+    for (int w = 1; w < waves; ++w)
+      sum += *reinterpret_cast<const v4f*>(lds + w * rows8_lds(XD, NT) + (t * 64 + lane) * 16);
     const int64_t m = t % MT * 16 + l16, n = n0 + t / MT * 16 + kg * 4;
     float v[4];
 #pragma unroll
@@ -807,12 +851,18 @@ static int launch_tiles(Gemm8Args g, hipStream_t st) {
   return launch_status();
 }
 
-template <int MT, int NT, typename TY>
+template <int XD, int NT, typename TY>
 static int launch_rows(const Gemm8Args& g, hipStream_t st) {
-  Rows8Args r{g, (int)cdiv(g.K, 512), 1};
-  const int64_t rounds = cdiv(r.units, rows8_waves(MT, NT));
-  r.waves = (int)cdiv(r.units, rounds);
-  k_gemm8_rows<MT, NT, TY><<<dim3((unsigned)cdiv(g.N, 16 * NT)), r.waves * 64, (size_t)r.waves * MT * NT * 1024, st>>>(r);
+  // The waves of a workgroup share K: as many as leave room for two workgroups a compute unit, or for one
+  // where there are no more workgroups than units or half the room takes one wave (47 rows of 14336x4096 by
+  // one wave 27 us, by three 24.5; 17 rows by two waves 14.0, by four 15.5).
+  const int64_t tiles = cdiv(g.N, 16 * NT), steps = cdiv(g.K, 128), units = cdiv(steps, 4);
+  constexpr int64_t kLds = 160 * 1024, kWave = rows8_lds(XD, NT);
+  const int64_t room = tiles > device_cu_count() && kLds / 2 >= 2 * kWave ? kLds / 2 : kLds;
+  const int64_t most = hmin(hmin(room / kWave, 8), units), per = cdiv(units, most);
+  const Rows8Args r{g, (int)steps, (int)per * 4};
+  const unsigned waves = (unsigned)cdiv(units, per);
+  k_gemm8_rows<XD, NT, TY><<<dim3((unsigned)tiles), waves * 64, waves * rows8_lds(XD, NT), st>>>(r);
   return launch_status();
 }
 
@@ -829,10 +879,16 @@ static int gemm8_launch(Gemm8Args g, void* workspace, hipStream_t st) {
   g.slices = p.slices;
   g.slice = p.slice;
   if (p.rows) {
-    if (g.M <= 16) return launch_rows<1, 1, TY>(g, st);
-    if (g.M <= 32) return launch_rows<2, 2, TY>(g, st);
-    if (g.M <= 48) return launch_rows<3, 2, TY>(g, st);
-    return launch_rows<4, 2, TY>(g, st);
+    // 32 columns a wave halve the reads of A, where that leaves a workgroup for each compute unit (64 rows of
+    // 8192x8192 20 us, by 16 columns 29)
+    const bool two = g.N > 32 * 255;
+#define MX_ROWS8(XD) (two ? launch_rows<XD, 2, TY>(g, st) : launch_rows<XD, 1, TY>(g, st))
+    if (g.M <= 8) return MX_ROWS8(1);
+    if (g.M <= 16) return MX_ROWS8(2);
+    if (g.M <= 32) return MX_ROWS8(4);
+    if (g.M <= 48) return MX_ROWS8(6);
+    return MX_ROWS8(8);
+#undef MX_ROWS8
   }
   if (p.big) return launch_tiles<256, TY, false, kWide>(g, st);
   if (p.slices == 1) return launch_tiles<128, TY, false, kWide>(g, st);

@@ -81,7 +81,7 @@ struct OutPacked4 {  // Q_D with 1x32 blocks, a quad of lanes a block; cols % 32
   }
 };
 
-template <typename T, typename OUT, bool KEEP>
+template <typename T, typename OUT, bool KEEP, bool ODD>
 __global__ __launch_bounds__(256) void k_glu(const T* __restrict__ z, int64_t ldz,
                                              const int64_t* __restrict__ live, int64_t rows, int64_t cols,
                                              int per, int act, const OUT out, const Packed8 kept) {
@@ -90,10 +90,13 @@ __global__ __launch_bounds__(256) void k_glu(const T* __restrict__ z, int64_t ld
     if (first + threadIdx.x >= total) continue;
     const RowLane r = row_lane(first, threadIdx.x, per);
     const int64_t col = (int64_t)r.lane * 8;
-    const T* p = z + r.row * ldz + col;
+    const T* p = z + r.row * ldz;
+    Run8<T> gate, up;
+    gate.template load<ODD>(p, col, cols);
+    up.template load<ODD>(p + cols, col, cols);
     float g[8], u[8], h[8];
-    load8(p, cols - col, g);
-    load8(p + cols, cols - col, u);
+    gate.template values<ODD>(col, cols, true, g);
+    up.template values<ODD>(col, cols, true, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = activate<false>(g[i], act, nullptr) * u[i];
     out.store(r.row, r.lane, cols, per, h);
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(256) void k_glu(const T* __restrict__ z, int64_t ld
   }
 }
 
-template <typename TH, typename TZ>
+template <typename TH, typename TZ, bool ODD>
 __global__ __launch_bounds__(256) void k_glu_bwd(const TH* __restrict__ dh, int64_t lddh, const Packed8 kept,
                                                  const int64_t* __restrict__ live, int64_t rows, int64_t cols,
                                                  int per, int act, TZ* __restrict__ dz, int64_t lddz) {
@@ -115,10 +118,14 @@ __global__ __launch_bounds__(256) void k_glu_bwd(const TH* __restrict__ dh, int6
     const int64_t col = (int64_t)r.lane * 8, n = cols - col;
     const uint8_t* c = kept.codes + 2 * r.row * kept.ld + col;
     const uint8_t* s = kept.scales + 2 * r.row * kept.scale_ld + (col >> 7);
+    const uint2 gate = *reinterpret_cast<const uint2*>(c), up = *reinterpret_cast<const uint2*>(c + kept.ld);
+    const uint32_t gate_scale = s[0], up_scale = s[kept.scale_ld];
+    Run8<TH> run;
+    run.template load<ODD>(dh + r.row * lddh, col, cols);
     float g[8], u[8], d[8];
-    decode8_e4m3(*reinterpret_cast<const uint2*>(c), scale8_of(s[0]), g);
-    decode8_e4m3(*reinterpret_cast<const uint2*>(c + kept.ld), scale8_of(s[kept.scale_ld]), u);
-    load8(dh + r.row * lddh + col, n, d);
+    decode8_e4m3(gate, scale8_of(gate_scale), g);
+    decode8_e4m3(up, scale8_of(up_scale), u);
+    run.template values<ODD>(col, cols, true, d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float da;
@@ -142,8 +149,13 @@ static int launch_glu(const void* z, int z_dtype, int64_t ldz, const int64_t* li
                       int act, const OUT& out, const Packed8& kept, hipStream_t st) {
   const int per = (int)(blocks8(cols) * 16);
   const dim3 grid(glu_grid(rows * per));
-#define MX_GLU(T, KEEP) \
-  k_glu<T, OUT, KEEP><<<grid, 256, 0, st>>>(static_cast<const T*>(z), ldz, live, rows, cols, per, act, out, kept)
+#define MX_GLU_ODD(T, KEEP, ODD) \
+  k_glu<T, OUT, KEEP, ODD><<<grid, 256, 0, st>>>(static_cast<const T*>(z), ldz, live, rows, cols, per, act, out, kept)
+#define MX_GLU(T, KEEP)                     \
+  do {                                      \
+    if (cols % 8) MX_GLU_ODD(T, KEEP, true); \
+    else MX_GLU_ODD(T, KEEP, false);         \
+  } while (0)
   if (z_dtype == MX_F32) {
     if (kept.codes) MX_GLU(float, true);
     else MX_GLU(float, false);
@@ -152,6 +164,7 @@ static int launch_glu(const void* z, int z_dtype, int64_t ldz, const int64_t* li
     else MX_GLU(uint16_t, false);
   }
 #undef MX_GLU
+#undef MX_GLU_ODD
   return launch_status();
 }
 
@@ -239,9 +252,14 @@ extern "C" int mx_glu_bwd(const void* dh, int dh_dtype, int64_t lddh, const uint
   const dim3 grid(glu_grid(rows * per));
   const hipStream_t st = as_stream(stream);
   const Packed8 kept{const_cast<uint8_t*>(kept_codes), const_cast<uint8_t*>(kept_scales), kept_ld, kept_scale_ld};
-#define MX_GLU_BWD(TH, TZ)                                                                              \
-  k_glu_bwd<TH, TZ><<<grid, 256, 0, st>>>(static_cast<const TH*>(dh), lddh, kept, live, rows, cols, per, act, \
-                                          static_cast<TZ*>(dz), lddz)
+#define MX_GLU_BWD_ODD(TH, TZ, ODD)                                                                          \
+  k_glu_bwd<TH, TZ, ODD><<<grid, 256, 0, st>>>(static_cast<const TH*>(dh), lddh, kept, live, rows, cols, per, act, \
+                                               static_cast<TZ*>(dz), lddz)
+#define MX_GLU_BWD(TH, TZ)                     \
+  do {                                         \
+    if (cols % 8) MX_GLU_BWD_ODD(TH, TZ, true); \
+    else MX_GLU_BWD_ODD(TH, TZ, false);         \
+  } while (0)
   if (dh_dtype == MX_F32) {
     if (dz_dtype == MX_F32) MX_GLU_BWD(float, float);
     else MX_GLU_BWD(float, uint16_t);
@@ -250,5 +268,6 @@ extern "C" int mx_glu_bwd(const void* dh, int dh_dtype, int64_t lddh, const uint
     else MX_GLU_BWD(uint16_t, uint16_t);
   }
 #undef MX_GLU_BWD
+#undef MX_GLU_BWD_ODD
   return launch_status();
 }

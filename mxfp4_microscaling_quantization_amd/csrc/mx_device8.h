@@ -69,29 +69,34 @@ __device__ __forceinline__ void decode8_e4m3(uint2 w, float scale, float v[8]) {
   v[4] = c.x * scale; v[5] = c.y * scale; v[6] = d.x * scale; v[7] = d.y * scale;
 }
 
-// The first n (any number, 8 or more: all) of 8 consecutive values at T's alignment, 0 for the
-// others.  T: float or uint16_t (bf16).
+// 8 consecutive values of a row of cols from column col on, 0 from cols on.  T: float or uint16_t (bf16), at
+// its own alignment.  Loads and conversion are apart, so that a thread's loads are all on their way before the
+// first is waited for.  cols a multiple of 8 (ODD false): no branch, a run past the row loads its first columns;
+// a branch around each load made the next wait for it.
 template <typename T>
-__device__ __forceinline__ void load8(const T* __restrict__ p, int64_t n, float v[8]) {
-  if (n >= 8) {
-    T raw[8];
-    __builtin_memcpy(raw, p, sizeof(raw));
+struct Run8 {
+  T raw[8];
+  template <bool ODD>
+  __device__ __forceinline__ void load(const T* __restrict__ row, int64_t col, int64_t cols) {
+    if constexpr (!ODD) {
+      __builtin_memcpy(raw, row + (col < cols ? col : 0), sizeof(raw));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (sizeof(T) == 2) v[i] = bf16_lo(raw[i]);
-      else v[i] = raw[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0.0f;
-      if (i < n) {
-        if constexpr (sizeof(T) == 2) v[i] = bf16_lo(p[i]);
-        else v[i] = p[i];
-      }
+      for (int i = 0; i < 8; ++i) raw[i] = row[col + i < cols ? col + i : 0];
     }
   }
-}
+  template <bool ODD>
+  __device__ __forceinline__ void values(int64_t col, int64_t cols, bool there, float v[8]) const {
+    const int64_t n = there ? cols - col : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f;
+      if constexpr (sizeof(T) == 2) f = bf16_lo(raw[i]);
+      else f = raw[i];
+      v[i] = (ODD ? i : 0) < n ? f : 0.0f;
+    }
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T* __restrict__ p, int64_t n, const float v[8]) {

@@ -17,7 +17,7 @@ namespace mx {
 // 16 lanes hold a block, 8 values each; the block's amax is a rotation within the 16 lanes.
 // Lanes past the columns hold zeros: they fill the codes up to a multiple of 16 columns, and the
 // scale row up to whole dwords.
-template <typename T>
+template <typename T, bool ODD>
 __global__ __launch_bounds__(256) void k_quant8_row(const T* __restrict__ x, int64_t ldx, int64_t rows,
                                                     int64_t cols, int per, uint8_t* __restrict__ codes,
                                                     int64_t ld, uint8_t* __restrict__ scales,
@@ -27,8 +27,10 @@ __global__ __launch_bounds__(256) void k_quant8_row(const T* __restrict__ x, int
     if (first + threadIdx.x >= total) continue;
     const RowLane r = row_lane(first, threadIdx.x, per);
     const int64_t col = (int64_t)r.lane * 8;
+    Run8<T> run;
+    run.template load<ODD>(x + r.row * ldx, col, cols);
     float v[8];
-    load8(x + r.row * ldx + col, cols - col, v);
+    run.template values<ODD>(col, cols, true, v);
     const uint32_t byte = scale8_byte_of(row16_max_u32(amax_bits<8>(v)));
     if (col - (col & 8) < cols)  // 16 columns with any are written whole
       *reinterpret_cast<uint2*>(codes + r.row * ld + col) = encode8(v, byte);
@@ -40,29 +42,36 @@ __global__ __launch_bounds__(256) void k_quant8_row(const T* __restrict__ x, int
 
 // ============================================================== tiles
 // Source of a tile's values: an unquantized matrix, or an 8-bit one by its exact values.
-template <typename T>
+template <typename T, bool ODD>
 struct Source8 {
+  using Run = Run8<T>;
   const T* x;
   int64_t ld;
-  __device__ __forceinline__ void load(int64_t row, int64_t col, int64_t cols, float v[8]) const {
-    load8(x + row * ld + col, cols - col, v);
+  __device__ __forceinline__ void load(Run& r, int64_t row, int64_t col, int64_t cols) const {
+    r.template load<ODD>(x + row * ld, col, cols);
+  }
+  __device__ __forceinline__ void values(const Run& r, int64_t col, int64_t cols, bool there, float v[8]) const {
+    r.template values<ODD>(col, cols, there, v);
   }
 };
-struct Codes8 {
+struct CodeRun {
+  uint2 codes;
+  uint32_t scale;
+};
+struct Codes8 {  // the codes' columns past cols, up to a multiple of 16, are 0
+  using Run = CodeRun;
   const uint8_t* codes;
   const uint8_t* scales;
   int64_t ld, scale_ld;
-  // columns past cols up to a multiple of 16 hold code 0
-  __device__ __forceinline__ void load(int64_t row, int64_t col, int64_t cols, float v[8]) const {
-    if (col < cols) {
-      decode8_e4m3(*reinterpret_cast<const uint2*>(codes + row * ld + col),
-                   scale8_of(scales[row * scale_ld + (col >> 7)]), v);
+  __device__ __forceinline__ void load(Run& r, int64_t row, int64_t col, int64_t cols) const {
+    const int64_t c = col < cols ? col : 0;
+    r.codes = *reinterpret_cast<const uint2*>(codes + row * ld + c);
+    r.scale = scales[row * scale_ld + (c >> 7)];
+  }
+  __device__ __forceinline__ void values(const Run& r, int64_t col, int64_t cols, bool there, float v[8]) const {
+    decode8_e4m3(r.codes, scale8_of(r.scale), v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? v[i] : 0.0f;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = there && col + i < cols ? v[i] : 0.0f;
   }
 };
 
@@ -86,14 +95,12 @@ __global__ __launch_bounds__(256) void k_quant8_tile(const SRC src, int64_t rows
   const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;
   const int64_t row0 = tr * 128 + rg * 8, col0 = tc * 128 + c * 8;
   float v[8][8];
+  {
+    typename SRC::Run run[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (row0 + i < rows) {
-      src.load(row0 + i, col0, cols, v[i]);
-    } else {
+    for (int i = 0; i < 8; ++i) src.load(run[i], row0 + i < rows ? row0 + i : rows - 1, col0, cols);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    }
+    for (int i = 0; i < 8; ++i) src.values(run[i], col0, cols, row0 + i < rows, v[i]);
   }
   uint32_t tile_byte = 0;
   if constexpr (TILE) {
@@ -183,8 +190,10 @@ __global__ __launch_bounds__(256) void k_dequant8(const Codes8 src, int64_t rows
     if (first + threadIdx.x >= total) continue;
     const RowLane r = row_lane(first, threadIdx.x, per);
     const int64_t col = (int64_t)r.lane * 8;
+    CodeRun run;
+    src.load(run, r.row, col, cols);
     float v[8];
-    src.load(r.row, col, cols, v);
+    src.values(run, col, cols, true, v);
     store8(out + r.row * ldo + col, cols - col, v);
   }
 }
@@ -199,12 +208,17 @@ int quant8_row_impl(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t
   if (rows == 0 || cols == 0) return MX_OK;
   const int per = (int)(blocks8(cols) * 16);
   const dim3 grid(flat_grid(rows * per));
-  if (dtype == MX_F32)
-    k_quant8_row<float><<<grid, 256, 0, st>>>(static_cast<const float*>(x), ldx, rows, cols, per, codes, ld,
-                                              scales, scale_ld);
-  else
-    k_quant8_row<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(x), ldx, rows, cols, per, codes,
-                                                 ld, scales, scale_ld);
+#define MX_ROW8(T, ODD)                                                                                        \
+  k_quant8_row<T, ODD><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, rows, cols, per, codes, ld, scales, \
+                                             scale_ld)
+  if (dtype == MX_F32) {
+    if (cols % 8) MX_ROW8(float, true);
+    else MX_ROW8(float, false);
+  } else {
+    if (cols % 8) MX_ROW8(uint16_t, true);
+    else MX_ROW8(uint16_t, false);
+  }
+#undef MX_ROW8
   return launch_status();
 }
 
@@ -223,12 +237,14 @@ static int launch_tile(const SRC& src, int64_t rows, int64_t cols, uint8_t* code
 int quant8_tile_impl(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t cols, bool tile,
                      uint8_t* codes, int64_t ld, uint8_t* scales, int64_t scale_ld, uint8_t* codes_t,
                      int64_t ld_t, uint8_t* scales_t, int64_t scale_ld_t, hipStream_t st) {
-#define MX_TILE8(T, TILE)                                                                             \
-  launch_tile<TILE>(Source8<T>{static_cast<const T*>(x), ldx}, rows, cols, codes, ld, scales, scale_ld, \
+#define MX_TILE8_ODD(T, TILE, ODD)                                                                        \
+  launch_tile<TILE>(Source8<T, ODD>{static_cast<const T*>(x), ldx}, rows, cols, codes, ld, scales, scale_ld, \
                     codes_t, ld_t, scales_t, scale_ld_t, st)
+#define MX_TILE8(T, TILE) (cols % 8 ? MX_TILE8_ODD(T, TILE, true) : MX_TILE8_ODD(T, TILE, false))
   if (dtype == MX_F32) return tile ? MX_TILE8(float, true) : MX_TILE8(float, false);
   return tile ? MX_TILE8(uint16_t, true) : MX_TILE8(uint16_t, false);
 #undef MX_TILE8
+#undef MX_TILE8_ODD
 }
 
 int requant8_impl(const uint8_t* codes, int64_t ld, const uint8_t* scales, int64_t scale_ld, int64_t rows,

@@ -21,7 +21,7 @@
 namespace mx {
 
 constexpr int kRouteMaxK = 16;       // slot j's choice is kept by lane j
-constexpr int kRouteGroups = 256;    // workgroups whose sums the second launch adds up
+constexpr int kRouteGroups = 256;    // workgroups whose sums the second launch adds up: 8 runs of 32
 constexpr int kRouteAlone = 256;     // up to so many tokens one workgroup does all
 
 // Sums and extremes over the 16 lanes of a row, the same bits in each: neighbours, pairs, halves
@@ -153,21 +153,23 @@ __device__ __forceinline__ void route_loss(int experts, int top_k, const double*
   const int e = threadIdx.x;
   if (e <= experts) counts[e] = cnt[e];
   if (e < experts) sums[e] = (float)total[e];
-  if (e == 0) {
+  if (e < 64) {
     double l = 0.0;
-    for (int i = 0; i < experts; ++i) l += (double)cnt[i] * total[i];
+    for (int i = e; i < experts; i += 64) l += (double)cnt[i] * total[i];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
     const double n = cnt[experts];
-    *loss = n > 0 ? (float)(experts * l / (n * n * top_k)) : 0.0f;
+    if (e == 0) *loss = n > 0 ? (float)(experts * l / (n * n * top_k)) : 0.0f;
   }
 }
 
 template <typename T, int EPL, bool ALONE>
-__global__ __launch_bounds__(ALONE ? 1024 : 256) void k_route(const RouteArgs a, int32_t* __restrict__ ids,
+__global__ __launch_bounds__(1024) void k_route(const RouteArgs a, int32_t* __restrict__ ids,
                                                               float* __restrict__ p, float* __restrict__ part_sum,
                                                               int32_t* __restrict__ part_cnt,
                                                               int32_t* __restrict__ counts,
                                                               float* __restrict__ sums, float* __restrict__ loss) {
-  constexpr int kThreads = ALONE ? 1024 : 256;
+  constexpr int kThreads = 1024;
   __shared__ float s_sum[kThreads / 64][128];
   __shared__ int32_t s_cnt[129];
   __shared__ double s_total[128];
@@ -187,42 +189,45 @@ __global__ __launch_bounds__(ALONE ? 1024 : 256) void k_route(const RouteArgs a,
   }
 }
 
-// The workgroups' sums in their order: eight runs of them at once, then the runs.
+// The workgroups' sums in their order: eight runs at once, then the runs.  Every load is on its way before the
+// first sum (14.7 us for 256 workgroups one after the other, ROUTE_SUM_TIME so).
 __global__ __launch_bounds__(1024) void k_route_sum(const float* __restrict__ part_sum,
                                                     const int32_t* __restrict__ part_cnt, int groups, int experts,
                                                     int top_k, int32_t* __restrict__ counts,
                                                     float* __restrict__ sums, float* __restrict__ loss) {
+  constexpr int kRun = kRouteGroups / 8;
   __shared__ double s_run[8][128];
-  __shared__ int32_t s_crun[8][129];
+  __shared__ int32_t s_crun[8][128];
   __shared__ double s_total[128];
   __shared__ int32_t s_cnt[129];
   const int e = threadIdx.x & 127, run = threadIdx.x >> 7;
-  const int per = (groups + 7) / 8, first = run * per, end = min(groups, first + per);
-  double total = 0.0;
-  int32_t n = 0, tokens = 0;
-  if (e < experts) {
-    for (int g = first; g < end; ++g) {
-      total += part_sum[(int64_t)g * experts + e];
-      n += part_cnt[(int64_t)g * (experts + 1) + e];
-    }
+  if (threadIdx.x == 0) s_cnt[experts] = 0;
+  float x[kRun];
+  int32_t n[kRun];
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    const int g = min(run * kRun + i, groups - 1), at = min(e, experts - 1);
+    x[i] = part_sum[g * experts + at];
+    n[i] = part_cnt[g * (experts + 1) + at];
   }
-  if (e == 0)
-    for (int g = first; g < end; ++g) tokens += part_cnt[(int64_t)g * (experts + 1) + experts];
+  const int32_t tokens = (int)threadIdx.x < groups ? part_cnt[threadIdx.x * (experts + 1) + experts] : 0;
+  double total = 0.0;
+  int32_t slots = 0;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    total += run * kRun + i < groups ? x[i] : 0.0f;
+    slots += run * kRun + i < groups ? n[i] : 0;
+  }
   s_run[run][e] = total;
-  s_crun[run][e] = n;
-  if (e == 0) s_crun[run][128] = tokens;
+  s_crun[run][e] = slots;
   __syncthreads();
-  if (run == 0) {
-    double t = 0.0;
-    int32_t c = 0;
-    for (int r = 0; r < 8; ++r) t += s_run[r][e], c += s_crun[r][e];
-    s_total[e] = t;
-    if (e < experts) s_cnt[e] = c;
-    if (e == 0) {
-      int32_t all = 0;
-      for (int r = 0; r < 8; ++r) all += s_crun[r][128];
-      s_cnt[experts] = all;
-    }
+  if (tokens) atomicAdd(&s_cnt[experts], tokens);
+  if (run == 0 && e < experts) {
+    total = 0.0, slots = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) total += s_run[r][e], slots += s_crun[r][e];
+    s_total[e] = total;
+    s_cnt[e] = slots;
   }
   __syncthreads();
   route_loss(experts, top_k, s_total, s_cnt, counts, sums, loss);
@@ -307,7 +312,7 @@ using namespace mx;
 
 extern "C" size_t mx_moe_route_workspace_size(int64_t tokens, int64_t experts, int64_t top_k) {
   if (!route_shape(tokens, experts, top_k) || tokens <= kRouteAlone) return 0;
-  return (size_t)hmin(cdiv(tokens, 16), kRouteGroups) * (2 * experts + 1) * 4;
+  return (size_t)hmin(cdiv(tokens, 64), kRouteGroups) * (2 * experts + 1) * 4;
 }
 
 #define MX_ROUTE_WIDTH(CALL, T)            \
@@ -335,12 +340,12 @@ extern "C" int mx_moe_route(const void* logits, int dtype, int64_t ld, const uin
   }
   const RouteArgs a{logits, ld, tokens, mask, (int)experts, (int)top_k, renormalize};
   const hipStream_t st = as_stream(stream);
-  const int groups = (int)hmin(cdiv(tokens, 16), kRouteGroups);
+  const int groups = (int)hmin(cdiv(tokens, 64), kRouteGroups);
   float* part = static_cast<float*>(workspace);
   int32_t* cnt = reinterpret_cast<int32_t*>(part + (need ? groups * experts : 0));
 #define MX_ROUTE(T, EPL)                                                                                     \
   do {                                                                                                       \
-    if (need) k_route<T, EPL, false><<<groups, 256, 0, st>>>(a, ids, weights, part, cnt, counts, sums, loss); \
+    if (need) k_route<T, EPL, false><<<groups, 1024, 0, st>>>(a, ids, weights, part, cnt, counts, sums, loss); \
     else k_route<T, EPL, true><<<1, 1024, 0, st>>>(a, ids, weights, part, cnt, counts, sums, loss);           \
   } while (0)
   if (dtype == MX_F32) MX_ROUTE_WIDTH(MX_ROUTE, float);
