@@ -125,12 +125,6 @@ __device__ __forceinline__ void lds_load16_at(bool yes, const uint8_t* p, uint32
 }
 // The same loads if `yes`, without a branch (a branch between the products of a step would let the
 // compiler move them past it): by no lane otherwise.  Every lane is active around them.
-__device__ __forceinline__ void lds_load16_if(bool yes, const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
-               :
-               : "s"(lds), "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(yes ? -1 : 0))
-               : "memory", "m0");
-}
 __device__ __forceinline__ void lds_load4_if(bool yes, const uint8_t* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\tglobal_load_lds_dword %1, %2\n\ts_mov_b64 exec, -1"
                :
@@ -223,21 +217,31 @@ __device__ __forceinline__ Place8 place8(const Gemm8Args& g) {
   return p;
 }
 
+// This wave's LDS reads have landed, then the workgroup's barrier.
+__device__ __forceinline__ void barrier8() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int W>
+__device__ __forceinline__ void clear8(v16f (&acc)[W][W]) {
+#pragma unroll
+  for (int a = 0; a < W; ++a)
+#pragma unroll
+    for (int b = 0; b < W; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+}
+
 // How many of n things are due before turn `at` of `turns`.
 constexpr int due8(int at, int turns, int n) { return at <= 0 ? 0 : (at >= turns ? n : n * at / turns); }
 
-// The 8-bit instructions' kernel: 2 x 2 waves, T x T outputs, (T/64)^2 accumulators of 32x32 a wave.
-//
-// K goes by in steps of 128, two stages in LDS: rows of 128 bytes, so that a load instruction takes
-// eight whole cache lines (64-byte rows, sixteen half lines, cost the address unit twice the time: 455
-// us where lines take 405, 8192 x 14336 x 4096); the 16-byte chunks of row r stand in the order
-// c ^ ((r >> 1) & 7), which spreads a fragment read over all banks.
-//
-// A wave holds the A fragments of a whole step and goes through its W column tiles of B one after the
-// other ("turns" of 2 W products).  In turn b it reads column tile b + 1, in the second half of a step
-// also the next step's A.  So A's part of a stage is free as soon as its step begins, and B's tile by
-// tile; the loads of step p + 2 follow at once, in two groups, each behind a barrier that ends the reads
-// of what it overwrites:
+// The 8-bit instructions' kernel.  A wave holds the A fragments of a whole step and goes through its W column
+// tiles of B one after the other ("turns" of 2 W products).  In turn b it reads column tile b + 1, in the second
+// half of a step also the next step's A.  So A's part of a stage is free as soon as its step begins, and B's
+// tile by tile; the loads of step p + 2 follow at once, in two groups, each behind a barrier that ends the
+// reads of what it overwrites:
 //   first half of step p    B tiles W/2+1 .. W-1 of step p + 1, A of step p + 2
 //   second half of step p   B tiles 0 .. W/2 of step p + 2
 // Everything is on its way for a step at least before the barrier in front of its first read, where
@@ -439,174 +443,193 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm
   store_tile8<W, TY, SLICED>(g, acc, ring, m0, n0, at.slice);
 }
 
-// The wide kernel.  A workgroup of 2 x 2 waves owns a T x T tile of C and walks K in steps of 64 through a ring of
-// four stages in LDS (codes [rows][64 bytes]; the 16-byte chunks of row r stand in the order
-// c ^ ((r >> 2) & 3), which spreads a fragment read over all banks).  A wave holds (T/64)^2
-// accumulators of 32x32 and the fragments of two steps: while the products of one step run, it
-// reads the next step's fragments and issues the loads of the step four ahead, between the
-// products.  One barrier a step: before it, each wave has its fragments of the step in registers
-// (so the step's stage is free) and its share of the next step's loads has landed.
-template <int T, typename TY, bool SLICED, bool TAIL>
-__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_wide(const Gemm8Args g) {
-  constexpr int W = T / 64;                  // 32-row accumulators of a wave along m and n
-  constexpr int LC = T / 32;                 // code loads a wave and step (16 rows each)
-  constexpr int LS = T / 128;                // scale loads a wave and 8 steps (64 rows each)
-  constexpr int STAGE = 2 * T * 64;          // bytes
-  __shared__ __align__(16) uint8_t ring[4 * STAGE];
-  __shared__ __align__(16) uint32_t s_scale[2][2 * T];
+// The wide kernel's loads and LDS reads: two stages as above.  (The 8-bit kernel has them in its own body:
+// through this struct it took some more registers, which spilled, and 374 us became 397.)
+template <int T>
+struct Feed8 {
+  static constexpr int W = T / 64;           // accumulators of 32x32 of a wave along m and n
+  static constexpr int LA = T / 32;          // A loads a wave and step (8 rows each)
+  static constexpr int LB = T / 32;          // B loads: of each tile of 32 columns (of either half) two
+  static constexpr int LS = T / 128;         // scale loads a wave and four steps (64 rows each)
+  static constexpr int STAGE = 2 * T * 128;
+  uint8_t* ring;
+  uint32_t* scales;                          // [2][2 T]: the bytes of four steps
+  const uint8_t *abase, *bbase, *sbase;
+  uint32_t aoff[LA], boff[LB], soff[LS];
+  uint32_t ring0, scale0;
+  int64_t klen;
+  int KT, wave, dr, lane;
+  uint32_t pa[4], pb[4];                     // fragment chunks in a stage: half i / 2 of the step, 16 bytes i % 2
 
-  const Place8 at = place8<T, SLICED>(g);
-  const int64_t m0 = at.m0, n0 = at.n0, k0 = at.k0, klen = at.klen;
-  const int KT = (int)((klen + 63) / 64);
+  __device__ __forceinline__ int a_row(int j) const { return wave * (T / 4) + j * 8; }
+  __device__ __forceinline__ int b_row(int j) const {
+    return (wave >> 1) * (T / 2) + (j >> 1) * 32 + (wave & 1) * 16 + (j & 1) * 8;
+  }
+  __device__ __forceinline__ int chunk(int row0) const { return ((lane & 7) ^ (((row0 + dr) >> 1) & 7)) * 16; }
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = (wave >> 1) * (T / 2), wn = (wave & 1) * (T / 2);
-  const int lr = lane & 31, lh = lane >> 5;
-  const uint32_t ring0 = (uint32_t)(uintptr_t)(lds8_ptr_t)ring;
-  const uint32_t scale0 = (uint32_t)(uintptr_t)(lds8_ptr_t)s_scale;
-
-  // sources: wave w loads rows [w T/2, + T/2) of the tile's 2 T operand rows (A's, then B's), 16
-  // rows a load, rows past the matrix clamped to its last (they feed outputs that are not stored)
-  const bool isA = wave < 2;
-  const uint8_t* base = (isA ? g.a + m0 * g.lda : g.b + n0 * g.ldb) + k0;
-  const int64_t ld = isA ? g.lda : g.ldb, last = (isA ? g.M - m0 : g.N - n0) - 1;
-  const int dr = lane >> 2, dc = ((lane & 3) ^ ((dr >> 2) & 3)) * 16;
-  const int half = (wave & 1) * (T / 2);
-  uint32_t off[LC];
+  __device__ __forceinline__ Feed8(const Gemm8Args& g, const Place8& at, uint8_t* r, uint32_t* s) : ring(r), scales(s) {
+    const int tid = threadIdx.x;
+    lane = tid & 63;
+    dr = lane >> 3;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    ring0 = (uint32_t)(uintptr_t)(lds8_ptr_t)ring;
+    scale0 = (uint32_t)(uintptr_t)(lds8_ptr_t)scales;
+    klen = at.klen;
+    KT = (int)((klen + 127) / 128);
+    abase = g.a + at.m0 * g.lda + at.k0;
+    bbase = g.b + at.n0 * g.ldb + at.k0;
+    const int64_t alast = g.M - at.m0 - 1, blast = g.N - at.n0 - 1;
 #pragma unroll
-  for (int j = 0; j < LC; ++j) off[j] = (uint32_t)(lmin8(half + j * 16 + dr, last) * ld) + dc;
-  const uint8_t* sbase = (isA ? g.sa + m0 * g.lsa : g.sb + n0 * g.lsb) + k0 / 128;
-  const int64_t lds_ = isA ? g.lsa : g.lsb;
-  uint32_t soff[LS];
+    for (int j = 0; j < LA; ++j) aoff[j] = (uint32_t)(lmin8(a_row(j) + dr, alast) * g.lda) + chunk(a_row(j));
 #pragma unroll
-  for (int j = 0; j < LS; ++j) soff[j] = (uint32_t)(lmin8(half + j * 64 + lane, last) * lds_);
+    for (int j = 0; j < LB; ++j) boff[j] = (uint32_t)(lmin8(b_row(j) + dr, blast) * g.ldb) + chunk(b_row(j));
+    const bool isA = wave < 2;
+    sbase = (isA ? g.sa + at.m0 * g.lsa : g.sb + at.n0 * g.lsb) + at.k0 / 128;
+#pragma unroll
+    for (int j = 0; j < LS; ++j)
+      soff[j] = (uint32_t)(lmin8((wave & 1) * (T / 2) + j * 64 + lane, isA ? alast : blast) * (isA ? g.lsa : g.lsb));
+    const int lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = ((4 * (i >> 1) + 2 * lh + (i & 1)) ^ ((lr >> 1) & 7)) * 16;
+      pa[i] = ((wave >> 1) * (T / 2) + lr) * 128 + c;
+      pb[i] = (T + (wave & 1) * (T / 2) + lr) * 128 + c;
+    }
+  }
 
-  // Load j of step kt.  TAIL (K no multiple of 64): chunks past the contraction are zeros, steps
-  // past it too.  Else such steps are not loaded; SURE: it is no such step.
-  auto issue_one = [&](int kt, int j, auto SURE) {
-    const uint32_t to = ring0 + (uint32_t)(kt & 3) * STAGE + (uint32_t)(wave * (T / 2) + j * 16) * 64;
-    const int64_t k = (int64_t)kt * 64;
-    if constexpr (TAIL) lds_load16_at(true, k + dc < klen ? base + k + off[j] : reinterpret_cast<const uint8_t*>(&kZero16), to);
-    else if constexpr (decltype(SURE)::value) lds_load16(base + k, off[j], to);
-    else lds_load16_if(kt < KT, base + k, off[j], to);
-  };
-  // the scale bytes of steps 8 grp .. 8 grp + 7, if `yes`
-  auto issue_scales = [&](int grp, bool yes) {
+  // A load of step p (j < LA: A's j-th, else B's).  SURE: the step exists and is whole.  Else chunks
+  // past the contraction are zeros, and steps past it are not loaded.
+  template <bool SURE>
+  __device__ __forceinline__ void issue(int p, int j) const {
+    const int row0 = j < LA ? a_row(j) : T + b_row(j - LA);
+    const uint32_t to = ring0 + (uint32_t)(p & 1) * STAGE + (uint32_t)row0 * 128;
+    const uint8_t* base = (j < LA ? abase : bbase) + (int64_t)p * 128;
+    uint32_t off = j < LA ? aoff[j] : boff[j - LA];
+    if constexpr (SURE) {
+      lds_load16(base, off, to);
+    } else {
+      int c = ((lane & 7) ^ ((dr >> 1) & 7)) * 16;  // chunk() of this row
+      c = j & 1 ? c ^ 64 : c;
+      asm volatile("" : "+v"(off), "+v"(c));  // kept from being held, added up, over the last steps' loop
+      lds_load16_at(p < KT, (int64_t)p * 128 + c < klen ? base + off : reinterpret_cast<const uint8_t*>(&kZero16), to);
+    }
+  }
+  __device__ __forceinline__ void issue_scales(int grp, bool yes) const {  // of steps 4 grp .. 4 grp + 3
 #pragma unroll
     for (int j = 0; j < LS; ++j)
       lds_load4_if(yes, sbase + grp * 4, soff[j],
                    scale0 + (uint32_t)((grp & 1) * 2 * T + wave * (T / 2) + j * 64) * 4);
-  };
-
-  v16f acc[W][W];
-#pragma unroll
-  for (int a = 0; a < W; ++a)
-#pragma unroll
-    for (int b = 0; b < W; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
-
-  // fragments of two steps: chunks 2 lh and 2 lh + 1 of row lr of accumulator row (column) t
-  v8i fa[2][W], fb[2][W];
-  uint32_t sa[W], sb[W], na[W], nb[W];
-  const uint32_t key = (lr >> 2) & 3;
-  const uint8_t* pa[2] = {ring + (wm + lr) * 64 + ((2 * lh) ^ key) * 16,
-                          ring + (wm + lr) * 64 + ((2 * lh + 1) ^ key) * 16};
-  const uint8_t* pb[2] = {ring + (T + wn + lr) * 64 + ((2 * lh) ^ key) * 16,
-                          ring + (T + wn + lr) * 64 + ((2 * lh + 1) ^ key) * 16};
-  auto read_one = [&](auto P, int kt, int i) {  // i: 4 W reads
-    constexpr int p = decltype(P)::value;
-    const int t = i >> 2, h = i & 1;
-    const uint32_t at = (uint32_t)(kt & 3) * STAGE + t * 32 * 64;
-    const v4i c = *reinterpret_cast<const v4i*>((i & 2 ? pb[h] : pa[h]) + at);
-    v8i& f = i & 2 ? fb[p][t] : fa[p][t];
-    f = h ? __builtin_shufflevector(f, __builtin_shufflevector(c, c, 0, 1, 2, 3, 0, 1, 2, 3), 0, 1, 2, 3, 8, 9, 10, 11)
+  }
+  // 16 bytes e of half h of this lane's row of A's (B's) tile t of step p, into operand f
+  static __device__ __forceinline__ void put(v8i& f, int e, const v4i& c) {
+    f = e ? __builtin_shufflevector(f, __builtin_shufflevector(c, c, 0, 1, 2, 3, 0, 1, 2, 3), 0, 1, 2, 3, 8, 9, 10, 11)
           : __builtin_shufflevector(c, c, 0, 1, 2, 3, -1, -1, -1, -1);
-  };
-  // the scale bytes of steps kt and kt + 1 (kt even)
-  auto read_scales = [&](int kt, uint32_t (&x)[W], uint32_t (&y)[W]) {
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(s_scale[(kt >> 3) & 1]) + ((kt >> 1) & 3);
+  }
+  __device__ __forceinline__ void read_a(v8i& f, int p, int t, int h, int e) const {
+    put(f, e, *reinterpret_cast<const v4i*>(ring + pa[2 * h + e] + (p & 1) * STAGE + t * 32 * 128));
+  }
+  __device__ __forceinline__ void read_b(v8i& f, int p, int t, int h, int e) const {
+    put(f, e, *reinterpret_cast<const v4i*>(ring + pb[2 * h + e] + (p & 1) * STAGE + t * 32 * 128));
+  }
+  __device__ __forceinline__ void read_scales(int p, uint32_t (&x)[W], uint32_t (&y)[W]) const {
+    const uint8_t* s = reinterpret_cast<const uint8_t*>(scales + ((p >> 2) & 1) * 2 * T) + (p & 3);
+    const int lr = lane & 31;
 #pragma unroll
     for (int t = 0; t < W; ++t) {
-      x[t] = p[(wm + t * 32 + lr) * 4];
-      y[t] = p[(T + wn + t * 32 + lr) * 4];
+      x[t] = s[((wave >> 1) * (T / 2) + t * 32 + lr) * 4];
+      y[t] = s[(T + (wave & 1) * (T / 2) + t * 32 + lr) * 4];
     }
-  };
-  auto barrier = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  // prologue: the first scales and up to four steps on their way, the first step's fragments read
-  issue_scales(0, true);
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-    if (s < KT) {
-#pragma unroll
-      for (int j = 0; j < LC; ++j) issue_one(s, j, std::true_type{});
-    }
-  if (KT > 3) wait_vm<3 * LC>();
-  else if (KT > 2) wait_vm<2 * LC>();
-  else if (KT > 1) wait_vm<LC>();
-  else wait_vm<0>();
-  barrier();
-  read_scales(0, sa, sb);
-#pragma unroll
-  for (int i = 0; i < 4 * W; ++i) read_one(std::integral_constant<int, 0>{}, 0, i);
+  }
+};
 
-  // Step kt, kt % 2 == P.  SURE: step kt + 4 exists; without it the loads and reads of steps past
-  // the contraction move nothing that is used.
-  auto step = [&](int kt, auto P, auto SURE) {
-    constexpr int p = decltype(P)::value;
-    constexpr int Q = 1 - p;
-    // the loads of steps kt + 2 and kt + 3 may stay in flight
-    if (decltype(SURE)::value || kt + 3 < KT) wait_vm<2 * LC>();
-    else if (kt + 2 < KT) wait_vm<LC>();
-    else wait_vm<0>();
-    barrier();
-    if constexpr (p == 0) issue_scales((kt >> 3) + 1, (kt & 7) == 0 && kt + 8 < KT);
-    else read_scales(kt + 1, na, nb);
+// The wide kernel: a wave holds the fragments of two halves of a step (64 values of k each), reads the next
+// half's while one half's products run, 4 W^2 of 32 cycles, and widens them 8 values a lane at a time.  One
+// barrier a step, in front of its second half: by then every wave has that half in registers, so the step's
+// stage is free for the loads of step p + 2, and the loads of step p + 1, issued a step ago, have landed.
+template <int T, typename TY, bool SLICED>
+__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_wide(const Gemm8Args g) {
+  using Feed = Feed8<T>;
+  constexpr int W = Feed::W, L = Feed::LA + Feed::LB;
+  __shared__ __align__(16) uint8_t ring[2 * Feed::STAGE];
+  __shared__ __align__(16) uint32_t s_scale[2 * 2 * T];
+  const Place8 at = place8<T, SLICED>(g);
+  const Feed feed(g, at, ring, s_scale);
+  const int KT = feed.KT;
+
+  v16f acc[W][W];
+  clear8(acc);
+  v8i fa[2][W], fb[2][W];
+  uint32_t sa[W], sb[W], na[W], nb[W];
+  auto read_one = [&](auto H, int p, int i) {  // read i of 4 W of half H of step p
+    constexpr int h = decltype(H)::value;
+    if (i & 2) feed.read_b(fb[h][i >> 2], p, i >> 2, h, i & 1);
+    else feed.read_a(fa[h][i >> 2], p, i >> 2, h, i & 1);
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using No = std::false_type;
+
+  feed.issue_scales(0, true);
+#pragma unroll
+  for (int j = 0; j < L; ++j) feed.template issue<false>(0, j);
+#pragma unroll
+  for (int j = 0; j < L; ++j) feed.template issue<false>(1, j);
+  if (KT > 1) wait_vm<L>();
+  else wait_vm<0>();
+  barrier8();
+  feed.read_scales(0, sa, sb);
+#pragma unroll
+  for (int i = 0; i < 4 * W; ++i) read_one(I0{}, 0, i);
+
+  // Half H of step p.  SURE: step p + 2 exists and is whole.
+  auto half = [&](int p, auto H, auto SURE) {
+    constexpr int h = decltype(H)::value;
+    constexpr bool sure = decltype(SURE)::value;
+    if constexpr (h == 1) {
+      wait_vm<0>();
+      barrier8();
+      feed.issue_scales((p >> 2) + 1, (p & 3) == 0 && p + 4 < KT);
+      feed.read_scales(p + 1, na, nb);
+    }
     constexpr int kProducts = 4 * W * W;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v8bf xa[W], xb[W];
 #pragma unroll
       for (int t = 0; t < W; ++t) {
-        xa[t] = widen8(fa[p][t][2 * j], fa[p][t][2 * j + 1], scale_of(sa[t]));
-        xb[t] = widen8(fb[p][t][2 * j], fb[p][t][2 * j + 1], scale_of(sb[t]));
+        xa[t] = widen8(fa[h][t][2 * j], fa[h][t][2 * j + 1], scale_of(sa[t]));
+        xb[t] = widen8(fb[h][t][2 * j], fb[h][t][2 * j + 1], scale_of(sb[t]));
       }
 #pragma unroll
       for (int i = 0; i < W * W; ++i) {
-        const int a = i / W, b = i % W, at = j * W * W + i;
+        const int a = i / W, b = i % W, done = j * W * W + i;
         acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb[a], xa[b], acc[a][b], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 4 * W * at / kProducts; r < 4 * W * (at + 1) / kProducts; ++r)
-          read_one(std::integral_constant<int, Q>{}, kt + 1, r);
+        for (int r = due8(done, kProducts, 4 * W); r < due8(done + 1, kProducts, 4 * W); ++r)
+          read_one(std::integral_constant<int, 1 - h>{}, p + h, r);
+        if constexpr (h == 1) {
 #pragma unroll
-        for (int l = LC * at / kProducts; l < LC * (at + 1) / kProducts; ++l) issue_one(kt + 4, l, SURE);
+          for (int l = due8(done, kProducts, L); l < due8(done + 1, kProducts, L); ++l) feed.template issue<sure>(p + 2, l);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if constexpr (p == 1) {
+    if constexpr (h == 1) {
 #pragma unroll
       for (int t = 0; t < W; ++t) sa[t] = na[t], sb[t] = nb[t];
     }
   };
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  int kt = 0;
-  for (; kt + 5 < KT; kt += 2) {
-    step(kt, I0{}, std::true_type{});
-    step(kt + 1, I1{}, std::true_type{});
+  int p = 0;
+  for (; (int64_t)(p + 3) * 128 <= feed.klen; ++p) {
+    half(p, I0{}, std::true_type{});
+    half(p, I1{}, std::true_type{});
   }
-  for (; kt < KT; kt += 2) {
-    step(kt, I0{}, std::false_type{});
-    if (kt + 1 < KT) step(kt + 1, I1{}, std::false_type{});
+  for (; p < KT; ++p) {
+    half(p, I0{}, No{});
+    if ((int64_t)p * 128 + 64 < feed.klen) half(p, I1{}, No{});
   }
-
-  store_tile8<W, TY, SLICED>(g, acc, ring, m0, n0, at.slice);
+  store_tile8<W, TY, SLICED>(g, acc, ring, at.m0, at.n0, at.slice);
 }
 
 // C = alpha times the slices' sums, in their order.
@@ -845,8 +868,7 @@ static int launch_tiles(Gemm8Args g, hipStream_t st) {
   if constexpr (!WIDE) {
     k_gemm8_tile<T, TY, SLICED><<<grid, 256, 0, st>>>(g);
   } else {
-    if (g.K % 64) k_gemm8_wide<T, TY, SLICED, true><<<grid, 256, 0, st>>>(g);
-    else k_gemm8_wide<T, TY, SLICED, false><<<grid, 256, 0, st>>>(g);
+    k_gemm8_wide<T, TY, SLICED><<<grid, 256, 0, st>>>(g);
   }
   return launch_status();
 }
