@@ -29,9 +29,9 @@ __device__ __forceinline__ int64_t live_rows(const int64_t* __restrict__ live, i
 template <bool D>
 __device__ __forceinline__ float activate(float g, int act, float* d) {
   if (act == MX_SILU) {
-    const float e = 1.0f + expf(-g), s = 1.0f / e;
+    const float s = 1.0f / (1.0f + expf(-g));
     if (D) *d = s + s * (g * (1.0f - s));
-    return g / e;
+    return g * s;
   }
   const float phi = 0.5f * erfcf(g * -0.70710678118654752f);
   if (D) *d = phi + g * (0.39894228040143268f * expf(-0.5f * (g * g)));

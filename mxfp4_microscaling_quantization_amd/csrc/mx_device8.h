@@ -72,7 +72,7 @@ __device__ __forceinline__ void decode8_e4m3(uint2 w, float scale, float v[8]) {
 // 8 consecutive values of a row of cols from column col on, 0 from cols on.  T: float or uint16_t (bf16), at
 // its own alignment.  Loads and conversion are apart, so that a thread's loads are all on their way before the
 // first is waited for.  cols a multiple of 8 (ODD false): no branch, a run past the row loads its first columns;
-// a branch around each load made the next wait for it.
+// a branch around each load and its conversion made the next load wait.
 template <typename T>
 struct Run8 {
   T raw[8];
@@ -80,6 +80,8 @@ struct Run8 {
   __device__ __forceinline__ void load(const T* __restrict__ row, int64_t col, int64_t cols) {
     if constexpr (!ODD) {
       __builtin_memcpy(raw, row + (col < cols ? col : 0), sizeof(raw));
+    } else if (cols >= 8) {  // the last run starts early, and its values are moved down
+      __builtin_memcpy(raw, row + (col < cols - 8 ? col : cols - 8), sizeof(raw));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) raw[i] = row[col + i < cols ? col + i : 0];
@@ -90,11 +92,18 @@ struct Run8 {
     const int64_t n = there ? cols - col : 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float f;
-      if constexpr (sizeof(T) == 2) f = bf16_lo(raw[i]);
-      else f = raw[i];
-      v[i] = (ODD ? i : 0) < n ? f : 0.0f;
+      if constexpr (sizeof(T) == 2) v[i] = bf16_lo(raw[i]);
+      else v[i] = raw[i];
     }
+    if constexpr (ODD) {
+      const int early = cols >= 8 && n < 8 ? (int)(8 - (n > 0 ? n : 0)) : 0;
+#pragma unroll
+      for (int d = 4; d; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = early & d ? (i + d < 8 ? v[i + d] : 0.0f) : v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (ODD ? i : 0) < n ? v[i] : 0.0f;
   }
 };
 

@@ -1,0 +1,265 @@
+"""CPU checks of the 8-bit, gate and router entry points: arguments are refused before anything is launched
+(no compute calls here), by the library and by the tensor conveniences."""
+import os
+import subprocess
+import sys
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from mxfp4_microscaling_quantization_amd import build, mx
+from tests.test_abi_sanitized import ROOT, sanitized_library
+
+BAD = 0x1001       # non-null, misaligned
+GOOD = 0x10000     # non-null, aligned: only reached by calls that fail validation
+BIG = 1 << 31
+
+
+@pytest.fixture(scope="module")
+def L():
+    return mx.lib()
+
+
+def refused(call, shapes=(), enums=(), ptrs=(), aligned=()):
+    for bad in shapes:
+        assert call(**bad) == mx.MX_ERR_SHAPE, bad
+    for bad in enums:
+        assert call(**bad) == mx.MX_ERR_ENUM, bad
+    for name in ptrs:
+        assert call(**{name: None}) == mx.MX_ERR_NULL, name
+    for name in (*ptrs, *aligned):
+        assert call(**{name: BAD}) == mx.MX_ERR_ALIGN, name
+
+
+def test_quantizer_validation(L):
+    def one(x=GOOD, t=0, ldx=40, r=5, c=40, axis=0, q=GOOD, ld=48, s=GOOD, sld=4):
+        return L.mx_quantize8(x, t, ldx, r, c, axis, q, ld, s, sld, None)
+
+    refused(one, [{"ldx": 39}, {"r": -1}, {"c": -1}, {"ld": 32}, {"ld": 56}, {"sld": 0}, {"sld": 6}, {"r": BIG},
+                  {"ld": (1 << 23) + 16}, {"axis": 1, "ld": 0}, {"c": 513, "ldx": 513, "ld": 528}],
+            [{"t": 2}, {"axis": 2}, {"axis": -1}], ["x", "q", "s"])
+    assert one(r=0, x=None, q=None, s=None) == one(c=0, x=None, q=None, s=None) == mx.MX_OK
+
+    def dual(x=GOOD, t=1, ldx=40, r=5, c=40, tile=0, q=GOOD, ld=48, s=GOOD, sld=4, qt=GOOD, ldt=16, st=GOOD, sldt=4):
+        return L.mx_quantize8_dual(x, t, ldx, r, c, tile, q, ld, s, sld, qt, ldt, st, sldt, None)
+
+    refused(dual, [{"ldx": 39}, {"ld": 32}, {"sld": 0}, {"ldt": 0}, {"sldt": 2}], [{"t": -1}, {"tile": 2}],
+            ["x", "q", "s", "qt", "st"])
+    assert dual(qt=None, st=None) == mx.MX_ERR_NULL            # both layouts of a gradient
+    assert dual(qt=None, tile=1) == dual(st=None, tile=1) == mx.MX_ERR_NULL
+    assert dual(r=0, qt=None, st=None, tile=1, x=None) == mx.MX_OK
+
+    def requant(q=GOOD, ld=48, s=GOOD, sld=4, r=5, c=40, qt=GOOD, ldt=16, st=GOOD, sldt=4):
+        return L.mx_requantize8(q, ld, s, sld, r, c, qt, ldt, st, sldt, None)
+
+    refused(requant, [{"r": -1}, {"ld": 32}, {"sld": 3}, {"ldt": 24}, {"sldt": 0}], (), ["q", "s", "qt", "st"])
+
+    def values(q=GOOD, ld=48, s=GOOD, sld=4, r=5, c=40, o=GOOD, t=0, ldo=40):
+        return L.mx_dequantize8(q, ld, s, sld, r, c, o, t, ldo, None)
+
+    refused(values, [{"c": -1}, {"ldo": 39}, {"ld": 40}], [{"t": 3}], ["q", "s", "o"])
+
+
+def test_product_validation(L):
+    def call(a=GOOD, lda=64, sa=GOOD, lsa=4, b=GOOD, ldb=64, sb=GOOD, lsb=4, M=4, N=5, K=64, c=GOOD, t=0, ldc=5,
+             ws=None, n=0):
+        return L.mx_gemm8(a, lda, sa, lsa, b, ldb, sb, lsb, M, N, K, 1.0, c, t, ldc, ws, n, None)
+
+    refused(call, [{"M": -1}, {"N": -1}, {"K": -1}, {"ldc": 4}, {"lda": 48}, {"ldb": 72}, {"lsa": 0}, {"lsb": 5}, {"M": BIG},
+                   {"N": BIG, "ldc": BIG}, {"K": (1 << 23) + 1, "lda": 1 << 24, "ldb": 1 << 24}], [{"t": 2}],
+            ["a", "sa", "b", "sb", "c"])
+    assert call(M=0, a=None, c=None) == call(N=0, ldc=0, b=None, c=None) == mx.MX_OK
+    assert call(K=0, lda=0, ldb=0, lsa=0, lsb=0, a=None, b=None, c=None) == mx.MX_ERR_NULL
+    size = L.mx_gemm8_workspace_size
+    assert size(-1, 4, 4) == size(4, 4, -1) == size(64, 4096, 14336) == size(0, 4, 4096) == size(8192, 14336, 4096) == 0
+    need = size(128, 128, 8192)
+    assert need >= 2 * 128 * 128 * 4
+    long = {"M": 128, "N": 128, "K": 8192, "lda": 8192, "ldb": 8192, "lsa": 64, "lsb": 64, "ldc": 128}
+    assert call(**long) == mx.MX_ERR_WORKSPACE
+    assert call(**long, ws=GOOD, n=need - 1) == mx.MX_ERR_WORKSPACE
+    assert call(**long, ws=BAD, n=need) == mx.MX_ERR_ALIGN
+
+
+def test_layer_validation(L):
+    def fwd(x=GOOD, xt=1, ldx=40, w=GOOD, wt=0, ldw=40, M=5, N=9, K=40, y=GOOD, yt=1, ldy=9, xc=GOOD, xs=GOOD, wc=GOOD,
+            ws=GOOD, tc=GOOD, ts=GOOD, work=None, n=0):
+        return L.mx_linear8_fwd(x, xt, ldx, w, wt, ldw, M, N, K, y, yt, ldy, xc, xs, wc, ws, tc, ts, work, n, None)
+
+    refused(fwd, [{"M": -1}, {"N": -1}, {"K": -1}, {"ldx": 39}, {"ldw": 39}, {"ldy": 8}, {"M": (1 << 23) + 1}],
+            [{"xt": 2}, {"wt": 2}, {"yt": 2}], ["x", "y", "xc", "xs", "wc", "ws"], ["w", "tc", "ts"])
+    assert fwd(tc=None) == fwd(ts=None) == mx.MX_ERR_NULL
+    assert fwd(M=0, N=0, x=None, y=None) == mx.MX_OK
+    big = {"M": 128, "N": 128, "K": 8192, "ldx": 8192, "ldw": 8192, "ldy": 128}
+    assert fwd(**big) == mx.MX_ERR_WORKSPACE
+    assert fwd(**big, work=BAD, n=L.mx_linear8_fwd_workspace_size(128, 128, 8192)) == mx.MX_ERR_ALIGN
+
+    need = L.mx_linear8_bwd_workspace_size(5, 9, 40)
+
+    def bwd(dy=GOOD, dt=1, lddy=9, M=5, N=9, K=40, xc=GOOD, xs=GOOD, tc=GOOD, ts=GOOD, dx=GOOD, xt=0, lddx=40, dw=GOOD, lddw=40,
+            work=GOOD, n=need):
+        return L.mx_linear8_bwd(dy, dt, lddy, M, N, K, xc, xs, tc, ts, dx, xt, lddx, dw, lddw, work, n, None)
+
+    refused(bwd, [{"M": -1}, {"lddy": 8}, {"lddx": 39}, {"lddw": 39}, {"N": (1 << 23) + 1, "lddy": 1 << 24}], [{"dt": 7}, {"xt": 7}],
+            ["dy", "xc", "xs", "tc", "ts", "dx", "dw"], ["work"])
+    assert bwd(work=None) == bwd(n=need - 1) == mx.MX_ERR_WORKSPACE
+    assert bwd(K=0, dx=None) == bwd(M=0, N=0, dx=None, dw=None) == mx.MX_OK
+    assert bwd(M=0, dw=None) == bwd(N=0, dx=None) == mx.MX_ERR_NULL
+    assert L.mx_linear8_bwd_workspace_size(-1, 1, 1) == L.mx_linear8_bwd_workspace_size(0, 1, 1) == 0
+
+
+def test_gate_validation(L):
+    def value(z=GOOD, zt=0, ldz=64, live=None, r=3, c=32, act=0, h=GOOD, ht=1, ldh=32, k=GOOD, kld=32, ks=GOOD, ksld=4):
+        return L.mx_glu(z, zt, ldz, live, r, c, act, h, ht, ldh, k, kld, ks, ksld, None)
+
+    def four(z=GOOD, zt=0, ldz=64, live=None, r=3, c=32, act=0, h=GOOD, hs=GOOD, pitch=1, k=GOOD, kld=32, ks=GOOD, ksld=4):
+        return L.mx_glu_quantize(z, zt, ldz, live, r, c, act, h, hs, pitch, k, kld, ks, ksld, None)
+
+    def eight(z=GOOD, zt=0, ldz=64, live=None, r=3, c=32, act=0, h=GOOD, ld=32, hs=GOOD, sld=4, k=GOOD, kld=32, ks=GOOD, ksld=4):
+        return L.mx_glu_quantize8(z, zt, ldz, live, r, c, act, h, ld, hs, sld, k, kld, ks, ksld, None)
+
+    for call, ptrs in ((value, ["z", "h"]), (four, ["z", "h", "hs"]), (eight, ["z", "h", "hs"])):
+        refused(call, [{"r": -1}, {"c": -32}, {"ldz": 63}, {"kld": 16}, {"ksld": 2}, {"r": 1 << 30}, {"c": (1 << 23) + 32, "ldz": 1 << 25}],
+                [{"zt": 2}, {"act": 2}, {"act": -1}], ptrs, ["k", "ks"])
+        assert call(live=0x10004) == mx.MX_ERR_ALIGN
+        assert call(k=None) == call(ks=None) == mx.MX_ERR_NULL
+        assert call(r=0, z=None, h=None, k=None, ks=None) == mx.MX_OK
+    assert value(ldh=31) == four(pitch=0) == four(c=40, ldz=80, kld=48) == eight(ld=16) == eight(sld=0) == mx.MX_ERR_SHAPE
+    assert value(ht=2) == mx.MX_ERR_ENUM
+
+    def bwd(dh=GOOD, dt=1, lddh=32, k=GOOD, kld=32, ks=GOOD, ksld=4, live=None, r=3, c=32, act=1, dz=GOOD, zt=0, lddz=64):
+        return L.mx_glu_bwd(dh, dt, lddh, k, kld, ks, ksld, live, r, c, act, dz, zt, lddz, None)
+
+    refused(bwd, [{"r": -1}, {"lddh": 31}, {"lddz": 63}, {"kld": 40}, {"ksld": 0}], [{"dt": 2}, {"zt": 2}, {"act": 9}],
+            ["dh", "k", "ks", "dz"])
+    assert bwd(live=0x10002) == mx.MX_ERR_ALIGN
+
+
+def test_router_validation(L):
+    size = L.mx_moe_route_workspace_size
+    assert size(256, 8, 2) == size(-1, 8, 2) == size(10000, 0, 1) == size(10000, 129, 1) == size(10000, 8, 9) == size(10000, 32, 17) == 0
+    need = size(10000, 8, 2)
+    assert need > 0
+
+    def fwd(x=GOOD, t=0, ld=8, mask=None, T=4, E=8, k=2, norm=1, ids=GOOD, w=GOOD, counts=GOOD, sums=GOOD, loss=GOOD, ws=None, n=0):
+        return L.mx_moe_route(x, t, ld, mask, T, E, k, norm, ids, w, counts, sums, loss, ws, n, None)
+
+    shapes = [{"T": -1}, {"E": 0}, {"E": 129, "ld": 129}, {"k": 0}, {"k": 9}, {"E": 32, "ld": 32, "k": 17}, {"ld": 7},
+              {"T": 1 << 30, "k": 2}]
+    refused(fwd, shapes, [{"t": 2}, {"norm": 2}, {"norm": -1}], ["x", "ids", "w", "counts", "sums", "loss"])
+    assert fwd(T=10000) == fwd(T=10000, ws=GOOD, n=need - 1) == mx.MX_ERR_WORKSPACE
+    assert fwd(T=10000, ws=BAD, n=need) == mx.MX_ERR_ALIGN
+
+    def bwd(x=GOOD, t=0, ld=8, mask=None, T=4, E=8, k=2, norm=1, ids=GOOD, counts=GOOD, dw=GOOD, dl=GOOD, d=GOOD, ldd=8):
+        return L.mx_moe_route_bwd(x, t, ld, mask, T, E, k, norm, ids, counts, dw, dl, d, ldd, None)
+
+    refused(bwd, shapes + [{"ldd": 7}], [{"t": 2}, {"norm": 2}], ["x", "ids", "counts", "d"], ["dw", "dl"])
+    assert bwd(T=0, x=None, d=None) == mx.MX_OK
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def matrix(rows, cols):
+    return u8(rows, -(-cols // 16) * 16), u8(rows, -(-cols // 512) * 4)
+
+
+def test_conveniences_refuse_what_the_library_cannot_see():
+    """CPU tensors, wrong types and shapes raise before the library is called."""
+    x, a = torch.zeros(2, 64), matrix(2, 64)
+    cases = [
+        (lambda: mx.gemm8(a, matrix(3, 80)), "rows of 64 codes, b of 80"),
+        (lambda: mx.gemm8((a[0].int(), a[1]), a), "uint8"),
+        (lambda: mx.gemm8((a[0], u8(3, 4)), a), "same rows"),
+        (lambda: mx.gemm8((u8(4, 64)[::2], a[1]), a), "contiguous"),
+        (lambda: mx.gemm8((u8(2, 72), a[1]), a), "do not hold"),
+        (lambda: mx.gemm8((u8(2, 640), a[1]), a), "do not hold"),
+        (lambda: mx.gemm8(a, a, workspace=u8(64, 64)[:, ::2]), "workspace must be contiguous"),
+        (lambda: mx.requantize8(a, 65), "do not hold"),
+        (lambda: mx.dequantize8(a, 513), "do not hold"),
+        (lambda: mx.quantize8(torch.zeros(64, 2).t()), "rows must be contiguous"),
+        (lambda: mx.linear8_fwd(x, torch.zeros(5, 32)), "x has 64 columns"),
+        (lambda: mx.linear8_fwd(x, matrix(5, 80)), "8-bit matrix of"),
+        (lambda: mx.linear8_fwd(x, a[:1]), "a quantized weight is"),
+        (lambda: mx.linear8_bwd(torch.zeros(2, 5), a, matrix(5, 64), 2, 5, 64), "both layouts"),
+        (lambda: mx.linear8_bwd(torch.zeros(3, 5), a, matrix(5, 64) + matrix(64, 5), 2, 5, 64), "dy must be"),
+        (lambda: mx.linear8_bwd(torch.zeros(2, 5), matrix(2, 80), matrix(5, 64) + matrix(64, 5), 2, 5, 64), "xq is not"),
+        (lambda: mx.linear8_bwd(torch.zeros(2, 5), a, matrix(5, 64) + matrix(64, 32), 2, 5, 64), "wq is not"),
+        (lambda: mx.glu(torch.zeros(3, 7)), "z must be"),
+        (lambda: mx.glu(x, rows=torch.zeros(2, dtype=torch.int64)), "one int64"),
+        (lambda: mx.glu(x, rows=torch.zeros(1, dtype=torch.int32)), "one int64"),
+        (lambda: mx.glu_quantize(x, out=(u8(2, 16), u8(3, 1))), "packed uint8"),
+        (lambda: mx.glu_quantize8(x, out=matrix(3, 32)), "out has 3 rows"),
+        (lambda: mx.glu_bwd(x, matrix(3, 64)), "kept has 3 rows"),
+        (lambda: mx.glu_bwd(x, matrix(4, 48)), "do not hold"),
+        (lambda: mx.moe_route(x, 2, mask=torch.zeros(3, dtype=torch.bool)), "mask must be bool"),
+        (lambda: mx.moe_route(x, 2, mask=torch.zeros(2)), "mask must be bool"),
+        (lambda: mx.moe_route_bwd(x, torch.zeros(2, 2), torch.zeros(65, dtype=torch.int32)), "ids must be int32"),
+        (lambda: mx.moe_route_bwd(x, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(64, dtype=torch.int32)), "counts must be"),
+        (lambda: mx.moe_route_bwd(x, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(65, dtype=torch.int32),
+                                  torch.zeros(2, 3)), "dweights must be"),
+        (lambda: mx.moe_route_bwd(x, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(65, dtype=torch.int32), None,
+                                  torch.zeros(2)), "dloss must be"),
+    ]
+    for call, message in cases:
+        with pytest.raises(ValueError, match=message):
+            call()
+
+
+def calls(stream):
+    """Every convenience that takes a stream, on tensors of the device that torch names -1."""
+    x, a, ids = torch.zeros(2, 64), matrix(2, 64), torch.zeros((2, 2), dtype=torch.int32)
+    w = matrix(5, 64) + matrix(64, 5)
+    return {"quantize8": lambda: mx.quantize8(x, stream=stream),
+            "quantize8_dual": lambda: mx.quantize8_dual(x, stream=stream),
+            "requantize8": lambda: mx.requantize8(a, stream=stream),
+            "dequantize8": lambda: mx.dequantize8(a, stream=stream),
+            "gemm8": lambda: mx.gemm8(a, a, out=torch.zeros(2, 2), stream=stream),
+            "linear8_fwd": lambda: mx.linear8_fwd(x, w, out=torch.zeros(2, 5), stream=stream),
+            "linear8_bwd": lambda: mx.linear8_bwd(torch.zeros(2, 5), a, w, 2, 5, 64, stream=stream),
+            "glu": lambda: mx.glu(x, out=torch.zeros(2, 32), stream=stream),
+            "glu_quantize": lambda: mx.glu_quantize(x, out=(u8(2, 16), u8(2, 1)), stream=stream),
+            "glu_quantize8": lambda: mx.glu_quantize8(x, out=matrix(2, 32), stream=stream),
+            "glu_bwd": lambda: mx.glu_bwd(x, matrix(4, 64), out=torch.zeros(2, 128), stream=stream),
+            "moe_route": lambda: mx.moe_route(x, 2, stream=stream),
+            "moe_route_bwd": lambda: mx.moe_route_bwd(x, ids, torch.zeros(65, dtype=torch.int32), out=torch.zeros(2, 64),
+                                                      stream=stream)}
+
+
+@pytest.mark.parametrize("name", list(calls(None)))
+def test_streams_of_another_device_are_refused(name, monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
+    other = SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0x1000)
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        calls(other)[name]()
+
+
+@pytest.mark.parametrize("name", list(calls(None)))
+def test_tensors_of_another_device_are_refused(name, monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="the current device is cuda:0"):
+        calls(None)[name]()
+
+
+RUNNER = """
+import sys
+from mxfp4_microscaling_quantization_amd import build, mx
+mx.LIB_PATH = build.SAN_LIB
+import pytest
+sys.exit(pytest.main(["-q", "-p", "no:cacheprovider", "tests/test_eight_abi_cpu.py",
+                      "-k", "validation"]))
+"""
+
+
+@pytest.mark.slow
+def test_entry_points_under_address_and_undefined_behaviour_sanitizers():
+    sanitized_library()
+    env = dict(os.environ, PYTHONPATH=ROOT, LD_PRELOAD=str(build.sanitizer_runtime()),
+               ASAN_OPTIONS="detect_leaks=0:halt_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    res = subprocess.run([sys.executable, "-c", RUNNER], cwd=ROOT, env=env, capture_output=True,
+                         text=True, timeout=600)
+    assert res.returncode == 0, res.stdout[-3000:] + res.stderr[-3000:]
+    assert "5 passed" in res.stdout and "failed" not in res.stdout
