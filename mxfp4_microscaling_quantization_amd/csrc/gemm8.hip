@@ -43,9 +43,12 @@ struct Gemm8Args {
   const uint8_t* b;
   const uint8_t* sb;
   int64_t lda, lsa, ldb, lsb, M, N, K;
-  void* c;        // output, or the partial sums of a sliced contraction [slices][M][N] float32
+  void* c;
   int64_t ldc;
-  int tiles_m, tiles_n, slices;
+  float* part;    // sums of the sliced tiles: [slices][sliced tiles][128][128]
+  int tiles_m, tiles_n;
+  int whole;      // tiles in front of the sliced ones
+  int slices;
   int64_t slice;  // contraction values a slice, a multiple of 512
   float alpha;
   bool past;      // rows of c are whole lines
@@ -146,9 +149,14 @@ __device__ __forceinline__ int64_t lmin8(int64_t a, int64_t b) { return a < b ? 
 // 64 rows at a time, in C's type, in its quarter of the idle LDS ring (16-byte chunks XORed with row & 15)
 // and stores whole row segments.  It is alone on its SIMD, and every instruction counts: with bf16 rounded by
 // integer operations after a float32 staging this took 6 of a tile's 57 us.
-template <int W, typename TY, bool SLICED>
-__device__ __forceinline__ void store_tile8(const Gemm8Args& g, v16f (&acc)[W][W], uint8_t* ring, int64_t m0,
-                                            int64_t n0, int slice) {
+struct Out8 {
+  void* c;
+  int64_t m0, n0, M, N, ldc;
+  float alpha;
+  bool past;
+};
+template <int W, typename TY>
+__device__ __forceinline__ void store_tile8(const Out8& g, v16f (&acc)[W][W], uint8_t* ring) {
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave >> 1) * W * 32, wn = (wave & 1) * W * 32;
@@ -158,9 +166,8 @@ __device__ __forceinline__ void store_tile8(const Gemm8Args& g, v16f (&acc)[W][W
   wait_vm<0>();
   __syncthreads();
   uint8_t* stg = ring + wave * 64 * RB;
-  TY* c = static_cast<TY*>(g.c) + (SLICED ? (int64_t)slice * g.M * g.N : 0);
+  TY* c = static_cast<TY*>(g.c);
   const float alpha = g.alpha;
-  const bool past = !SLICED && g.past;
 #pragma unroll
   for (int p = 0; p < W / 2; ++p) {
     auto stage = [&](auto SCALED) {
@@ -191,8 +198,8 @@ __device__ __forceinline__ void store_tile8(const Gemm8Args& g, v16f (&acc)[W][W
     for (int it = 0; it < CH; ++it) {
       const int r = it * (64 / CH) + lane / CH, at = lane % CH;
       const v4i raw = *reinterpret_cast<const v4i*>(stg + r * RB + (at ^ (r & MASK)) * 16);
-      const int64_t m = m0 + wm + p * 64 + r, n = n0 + wn + at * V;
-      if (m < g.M && n < g.N) store_run8(c + m * g.ldc + n, raw, g.N - n, past);
+      const int64_t m = g.m0 + wm + p * 64 + r, n = g.n0 + wn + at * V;
+      if (m < g.M && n < g.N) store_run8(c + m * g.ldc + n, raw, g.N - n, g.past);
     }
   }
 }
@@ -201,24 +208,47 @@ __device__ __forceinline__ void store_tile8(const Gemm8Args& g, v16f (&acc)[W][W
 // tiles go to one die; tile rows are walked four together, so that B tiles are read again from L2.
 struct Place8 {
   int64_t m0, n0, k0, klen;
-  int slice;
+  int part;  // of the sliced tiles' sums; -1: a whole tile
 };
-template <int T, bool SLICED>
-__device__ __forceinline__ Place8 place8(const Gemm8Args& g) {
-  Place8 p;
-  const int tiles = g.tiles_m * g.tiles_n, total = gridDim.x, q = total / 8, r = total % 8;
-  const int x = (int)blockIdx.x % 8;
-  int id = x * q + min(x, r) + (int)blockIdx.x / 8;
-  p.slice = SLICED ? id / tiles : 0;
-  id -= p.slice * tiles;
+template <int T>
+__device__ __forceinline__ void tile8_at(const Gemm8Args& g, int id, int64_t* m0, int64_t* n0) {
   constexpr int kRows = 4;
   const int span = kRows * g.tiles_n, first_m = id / span * kRows;
   const int gm = min(g.tiles_m - first_m, kRows);
-  p.m0 = (int64_t)(first_m + id % span % gm) * T;
-  p.n0 = (int64_t)(id % span / gm) * T;
-  p.k0 = SLICED ? p.slice * g.slice : 0;
-  p.klen = SLICED ? lmin8(g.slice, g.K - p.k0) : g.K;
+  *m0 = (int64_t)(first_m + id % span % gm) * T;
+  *n0 = (int64_t)(id % span / gm) * T;
+}
+template <int T, bool SLICED>
+__device__ __forceinline__ Place8 place8(const Gemm8Args& g) {
+  Place8 p{0, 0, 0, g.K, -1};
+  int block = blockIdx.x, total = gridDim.x, first = 0;
+  if constexpr (SLICED) {
+    if (block >= g.whole) first = g.whole, block -= first, total -= first;
+    else total = g.whole;
+  }
+  const int q = total / 8, r = total % 8, x = block % 8;
+  int id = x * q + min(x, r) + block / 8;
+  if (SLICED && first == g.whole && (int)blockIdx.x >= g.whole) {
+    const int tiles = g.tiles_m * g.tiles_n - g.whole, slice = id / tiles;
+    p.part = id;
+    id = first + id - slice * tiles;
+    p.k0 = slice * g.slice;
+    p.klen = lmin8(g.slice, g.K - p.k0);
+  }
+  tile8_at<T>(g, id, &p.m0, &p.n0);
   return p;
+}
+
+template <int W, typename TY, bool SLICED>
+__device__ __forceinline__ void finish8(const Gemm8Args& g, const Place8& at, v16f (&acc)[W][W], uint8_t* ring) {
+  constexpr int T = W * 64;
+  if constexpr (SLICED) {
+    if (at.part >= 0) {
+      store_tile8<W, float>(Out8{g.part + (int64_t)at.part * T * T, 0, 0, T, T, T, 1.0f, false}, acc, ring);
+      return;
+    }
+  }
+  store_tile8<W, TY>(Out8{g.c, at.m0, at.n0, g.M, g.N, g.ldc, g.alpha, g.past}, acc, ring);
 }
 
 // This wave's LDS reads have landed, then the workgroup's barrier.
@@ -444,7 +474,7 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm
     step(p, I0{}, No{});
     if (p + 1 < KT) step(p + 1, I1{}, No{});
   }
-  store_tile8<W, TY, SLICED>(g, acc, ring, m0, n0, at.slice);
+  finish8<W, TY, SLICED>(g, at, acc, ring);
 }
 
 // The wide kernel's loads and LDS reads: two stages as above.  (The 8-bit kernel has them in its own body:
@@ -633,34 +663,29 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_wide(const Gemm
     half(p, I0{}, No{});
     if ((int64_t)p * 128 + 64 < feed.klen) half(p, I1{}, No{});
   }
-  store_tile8<W, TY, SLICED>(g, acc, ring, at.m0, at.n0, at.slice);
+  finish8<W, TY, SLICED>(g, at, acc, ring);
 }
 
-// C = alpha times the slices' sums, in their order.
+// The sliced tiles of C: alpha times their slices' sums, in their order.  Eight rows a workgroup.
 template <typename TY>
-__global__ __launch_bounds__(256) void k_gemm8_sum(const float* __restrict__ part, int slices, int64_t M,
-                                                   int64_t N, int64_t runs, float alpha, TY* __restrict__ c,
-                                                   int64_t ldc) {
-  const int64_t total = M * runs;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / runs, n = i % runs * 4;
-    const int left = (int)lmin8(4, N - n);
-    float s[4] = {};
-    for (int k = 0; k < slices; ++k) {
-      const float* p = part + ((int64_t)k * M + m) * N + n;
-      if (left == 4) {
-        float v[4];
-        __builtin_memcpy(v, p, 16);
+__global__ __launch_bounds__(256) void k_gemm8_sum(const Gemm8Args g) {
+  constexpr int T = 128;
+  const int tiles = g.tiles_m * g.tiles_n - g.whole, tile = (int)blockIdx.x / 16;
+  const int row = (int)blockIdx.x % 16 * 8 + (int)threadIdx.x / 32, col = (int)threadIdx.x % 32 * 4;
+  int64_t m, n;
+  tile8_at<T>(g, g.whole + tile, &m, &n);
+  m += row;
+  n += col;
+  if (m >= g.M || n >= g.N) return;
+  const float* p = g.part + ((int64_t)tile * T + row) * T + col;
+  const int64_t step = (int64_t)tiles * T * T;
+  v4f s = *reinterpret_cast<const v4f*>(p);
+#pragma unroll 4
+  for (int k = 1; k < g.slices; ++k) s += *reinterpret_cast<const v4f*>(p + k * step);
+  float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = k ? s[e] + v[e] : v[e];
-      } else {
-        for (int e = 0; e < left; ++e) s[e] = k ? s[e] + p[e] : p[e];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] *= alpha;
-    store_four8(c + m * ldc + n, s, N - n, false);
-  }
+  for (int e = 0; e < 4; ++e) v[e] = s[e] * g.alpha;
+  store_four8(static_cast<TY*>(g.c) + m * g.ldc + n, v, g.N - n, false);
 }
 
 // ============================================================== few rows
@@ -824,6 +849,7 @@ __global__ __launch_bounds__(256) void k_gemm8_zero(int64_t M, int64_t N, TY* __
 // ============================================================== launches
 struct Plan8 {
   bool rows, big;
+  int64_t whole;  // slices > 1: tiles of 128 in front of the sliced ones
   int slices;
   int64_t slice;
 };
@@ -831,48 +857,67 @@ struct Plan8 {
 // What a product takes in tiles of 256 (one workgroup a compute unit) and of 128 (two), by rounds of
 // workgroups over 256 compute units, in us: a round's own cost and that of 1024 values of K.  Measured,
 // bf16 C: 4096^3 60 us in tiles of 256, 72 in tiles of 128; 12608x1536x384 37 and 22; 6000x3000x1024 47 and
-// 36; 4093x2880x5760 68 and 85; float32 C: 4096^3 113 and 124, 5760x2880x4096 197 and 143.
+// 36; 4093x2880x5760 68 and 85; float32 C: 4096^3 106 and 124, 5760x2880x4096 197 and 135 (125 with slices).
+// The last tiles of 128, behind the full rounds, are sliced along K if that costs less: one or two workgroups a
+// compute unit take step1 and step2 for 128 values of K, the launch that adds the slices up kSum8, a slice of a
+// tile written and read kPart8.  Measured, unsliced and in slices of n: float32 C: 36 tiles of K 12608 86 us,
+// (n 5) 27.6, (7) 27.0, (9) 34; 100 of 4096 31.6, (2) 27.2, (4) 28.1; 196 of 2048 20.0, (2) 28.5; 512 + 17 of
+// 4096 135, (8) 124; bf16 C: 36 of 12608 54, (5) 20.3, (7) 21.2; 100 of 4096 18.1, (2) 19.5; 512 + 17 of 4096
+// 78, (8) 76; 512 + 98 of 2048 27, (2) 29.
 struct Cost8 {
-  float round256, k256, round128, k128;
+  float round256, k256, round128, k128, step1, step2;
 };
-constexpr Cost8 kCost8 = {12.0f, 11.0f, 3.0f, 8.2f}, kCost8Wide = {12.0f, 24.0f, 3.0f, 15.0f};
+constexpr Cost8 kCost8 = {12.0f, 11.0f, 3.0f, 8.2f, 0.5f, 0.85f}, kCost8Wide = {12.0f, 24.0f, 3.0f, 15.0f, 1.0f, 1.6f};
+constexpr float kSum8 = 5.0f, kPart8 = 0.018f;
 
-// Few rows take the wave-per-column kernel.  Else tiles by their cost, and the contraction sliced where
-// even tiles of 128 leave compute units idle.
+// Few rows take the wave-per-column kernel.  Else tiles by their cost.
 static Plan8 gemm8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
-  Plan8 p{M <= 64, false, 1, K};
+  Plan8 p{M <= 64, false, 0, 1, K};
   if (p.rows) return p;
-  const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
+  const int64_t tiles = cdiv(M, 128) * cdiv(N, 128), tail = tiles % 512;
   const Cost8& c = wide ? kCost8Wide : kCost8;
-  const float k = (float)K / 1024.0f;
-  p.big = tiles > 256 && (float)cdiv(cdiv(M, 256) * cdiv(N, 256), 256) * (c.round256 + c.k256 * k) <
-                             (float)cdiv(tiles, 512) * (c.round128 + c.k128 * k);
-  if (p.big || tiles >= 256 || K < 2048) return p;
-  const int64_t n = hmin(hmin(cdiv(512, tiles), K / 1024), 64);
-  if (n < 2) return p;
-  p.slice = cdiv(cdiv(K, n), 512) * 512;
-  p.slices = (int)cdiv(K, p.slice);
-  if (p.slices < 2) p.slices = 1, p.slice = K;
+  const float k = (float)K / 1024.0f, round = c.round128 + c.k128 * k;
+  float last = tail == 0 ? 0.f : (tail <= 256 ? c.round128 + c.step1 * (float)cdiv(K, 128) : round);
+  for (int per = 1; per <= 2 && tail > 0 && tail < 256; ++per) {
+    const int64_t n = hmin(per * 256 / tail, K / 512);
+    if (n < 2) continue;
+    const int64_t slice = cdiv(cdiv(K, n), 512) * 512, slices = cdiv(K, slice);
+    const float cost = c.round128 + (per == 1 ? c.step1 : c.step2) * (float)(slice / 128) + kSum8 +
+                       kPart8 * (float)(tail * slices);
+    if (slices > 1 && cost < last) last = cost, p.slice = slice, p.slices = (int)slices, p.whole = tiles - tail;
+  }
+  if (tiles > 256 && (float)cdiv(cdiv(M, 256) * cdiv(N, 256), 256) * (c.round256 + c.k256 * k) <
+                         (float)(tiles / 512) * round + last)
+    return Plan8{false, true, 0, 1, K};
   return p;
 }
 
+static size_t plan8_bytes(const Plan8& p, int64_t M, int64_t N) {
+  return p.slices > 1 ? (size_t)(cdiv(M, 128) * cdiv(N, 128) - p.whole) * p.slices * 128 * 128 * sizeof(float) : 0;
+}
 size_t gemm8_workspace(int64_t M, int64_t N, int64_t K) {  // for C of either type
-  const Plan8 p = gemm8_plan(M, N, round16(K), false), q = gemm8_plan(M, N, round16(K), true);
-  const int slices = p.slices > q.slices ? p.slices : q.slices;
-  return slices > 1 ? (size_t)slices * M * N * sizeof(float) : 0;
+  const size_t a = plan8_bytes(gemm8_plan(M, N, round16(K), false), M, N);
+  const size_t b = plan8_bytes(gemm8_plan(M, N, round16(K), true), M, N);
+  return a > b ? a : b;
 }
 
 template <int T, typename TY, bool SLICED, bool WIDE>
-static int launch_tiles(Gemm8Args g, hipStream_t st) {
-  const int64_t tm = cdiv(g.M, T), tn = cdiv(g.N, T);
-  if (tm * tn * g.slices > 0x7FFFFFFFll / 256) return MX_ERR_SHAPE;
+static int launch_tiles(Gemm8Args g, int64_t whole, hipStream_t st) {
+  const int64_t tm = cdiv(g.M, T), tn = cdiv(g.N, T), tail = SLICED ? tm * tn - whole : 0;
+  const int64_t blocks = tm * tn - tail + tail * g.slices;
+  if (blocks > 0x7FFFFFFFll / 256) return MX_ERR_SHAPE;
   g.tiles_m = (int)tm;
   g.tiles_n = (int)tn;
-  const dim3 grid((unsigned)(tm * tn * g.slices));
+  g.whole = (int)whole;
+  const dim3 grid((unsigned)blocks);
   if constexpr (!WIDE) {
     k_gemm8_tile<T, TY, SLICED><<<grid, 256, 0, st>>>(g);
   } else {
     k_gemm8_wide<T, TY, SLICED><<<grid, 256, 0, st>>>(g);
+  }
+  if constexpr (SLICED) {
+    if (const int s = launch_status()) return s;
+    k_gemm8_sum<TY><<<dim3((unsigned)tail * 16), 256, 0, st>>>(g);
   }
   return launch_status();
 }
@@ -894,9 +939,8 @@ static int launch_rows(const Gemm8Args& g, hipStream_t st) {
 
 template <typename TY>
 static int gemm8_launch(Gemm8Args g, void* workspace, hipStream_t st) {
-  const int64_t threads = g.M * cdiv(g.N, 4);
-  const dim3 flat((unsigned)hmin(cdiv(threads, 256), 4096));
   if (g.K == 0) {
+    const dim3 flat((unsigned)hmin(cdiv(g.M * cdiv(g.N, 4), 256), 4096));
     k_gemm8_zero<TY><<<flat, 256, 0, st>>>(g.M, g.N, static_cast<TY*>(g.c), g.ldc);
     return launch_status();
   }
@@ -916,24 +960,17 @@ static int gemm8_launch(Gemm8Args g, void* workspace, hipStream_t st) {
     return MX_ROWS8(8);
 #undef MX_ROWS8
   }
-  if (p.big) return launch_tiles<256, TY, false, kWide>(g, st);
-  if (p.slices == 1) return launch_tiles<128, TY, false, kWide>(g, st);
-  Gemm8Args part = g;
-  part.c = workspace;
-  part.ldc = g.N;
-  part.alpha = 1.0f;
-  const int s = launch_tiles<128, float, true, kWide>(part, st);
-  if (s != MX_OK) return s;
-  k_gemm8_sum<TY><<<flat, 256, 0, st>>>(static_cast<const float*>(workspace), p.slices, g.M, g.N, cdiv(g.N, 4),
-                                        g.alpha, static_cast<TY*>(g.c), g.ldc);
-  return launch_status();
+  if (p.big) return launch_tiles<256, TY, false, kWide>(g, 0, st);
+  if (p.slices == 1) return launch_tiles<128, TY, false, kWide>(g, 0, st);
+  g.part = static_cast<float*>(workspace);
+  return launch_tiles<128, TY, true, kWide>(g, p.whole, st);
 }
 
 int gemm8_impl(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t lsa, const uint8_t* b, int64_t ldb,
                const uint8_t* sb, int64_t lsb, int64_t M, int64_t N, int64_t K, float alpha, void* c,
                int c_dtype, int64_t ldc, void* workspace, hipStream_t st) {
   if (M == 0 || N == 0) return MX_OK;
-  const Gemm8Args g{a, sa, b, sb, lda, lsa, ldb, lsb, M, N, round16(K), c, ldc, 0, 0, 1, 0, alpha,
+  const Gemm8Args g{a, sa, b, sb, lda, lsa, ldb, lsb, M, N, round16(K), c, ldc, nullptr, 0, 0, 0, 1, 0, alpha,
                     ((uintptr_t)c | ldc * (c_dtype == MX_F32 ? 4 : 2)) % 128 == 0};
   return c_dtype == MX_F32 ? gemm8_launch<float>(g, workspace, st) : gemm8_launch<uint16_t>(g, workspace, st);
 }

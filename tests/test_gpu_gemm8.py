@@ -89,6 +89,23 @@ def test_large_tiles_and_long_contractions(M, N, K):
     check(got[:, torch.from_numpy(c).to(DEV)], want, mag, K, "f32")
 
 
+@pytest.mark.parametrize("M,N,K", [(3400, 2400, 4112), (3330, 2433, 4100), (260, 130, 70000)])
+def test_last_tiles_in_slices(M, N, K):
+    """A few tiles behind a full round, which share their contraction: sampled rows and columns, those of
+    the last tile rows all, into rows with a pitch; alpha once."""
+    rng = np.random.default_rng(K)
+    a, b = matrix(rng, M, K), matrix(rng, N, K)
+    r, c = np.r_[0, rng.integers(0, M, 20), M - 140:M], np.r_[0, rng.integers(0, N, 20), N - 40:N]
+    for y_type in ("f32", "bf16"):
+        out = torch.full((M + 1, N + 7), 7.0, dtype=torch_type(y_type), device=DEV)
+        got = mx.gemm8(dev(a), dev(b), alpha=0.75, out=out[:M, :N])
+        want, mag = O.gemm8((a[0][r], a[1][r]), b, 0.75)
+        check(got[torch.from_numpy(r).to(DEV)], want, mag, K, y_type)
+        want, mag = O.gemm8(a, (b[0][c], b[1][c]), 0.75)
+        check(got[:, torch.from_numpy(c).to(DEV)], want, mag, K, y_type)
+        assert torch.all(out[M:] == 7.0) and torch.all(out[:, N:] == 7.0)
+
+
 @pytest.mark.parametrize("M", [1, 40, 130, 3600])
 def test_strides_alpha_and_what_lies_outside(M):
     N, K = (3590, 96) if M == 3600 else (75, 700)
