@@ -77,10 +77,16 @@ extern "C" int mx_linear8_fwd(const void* x, int x_dtype, int64_t ldx, const voi
   }
   const hipStream_t st = as_stream(stream);
   const int64_t ldk = round16(K), lsk = scale8_pitch(K);
-  int s = quant8_row_impl(x, x_dtype, ldx, M, K, xq_codes, ldk, xq_scales, lsk, st);
-  if (s == MX_OK && w)
-    s = quant8_tile_impl(w, w_dtype, ldw, N, K, true, wq_codes, ldk, wq_scales, lsk, wt_codes, round16(N), wt_scales,
-                         scale8_pitch(N), st);
+  int s;
+  if (w && M && N && K) {
+    s = quant8_forward_impl(x, x_dtype, ldx, M, w, w_dtype, ldw, N, K, xq_codes, xq_scales, wq_codes, wq_scales,
+                            wt_codes, wt_scales, st);
+  } else {
+    s = quant8_row_impl(x, x_dtype, ldx, M, K, xq_codes, ldk, xq_scales, lsk, st);
+    if (s == MX_OK && w)
+      s = quant8_tile_impl(w, w_dtype, ldw, N, K, true, wq_codes, ldk, wq_scales, lsk, wt_codes, round16(N), wt_scales,
+                           scale8_pitch(N), st);
+  }
   if (s != MX_OK) return s;
   return gemm8_impl(xq_codes, ldk, xq_scales, lsk, wq_codes, ldk, wq_scales, lsk, M, N, K, 1.0f, y, y_dtype, ldy,
                     workspace, st);
@@ -111,10 +117,8 @@ extern "C" int mx_linear8_bwd(const void* dy, int dy_dtype, int64_t lddy, int64_
   MX_REQUIRE(workspace && workspace_bytes >= (size_t)l.total, MX_ERR_WORKSPACE);
   MX_REQUIRE(aligned16(workspace), MX_ERR_ALIGN);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int s = quant8_tile_impl(dy, dy_dtype, lddy, M, N, false, ws + l.dy, l.ld_n, ws + l.dys, l.ls_n, ws + l.dyt,
-                           l.ld_m, ws + l.dyts, l.ls_m, st);
-  if (s != MX_OK) return s;
-  s = requant8_impl(xq_codes, round16(K), xq_scales, scale8_pitch(K), M, K, ws + l.xt, l.ld_m, ws + l.xts, l.ls_m, st);
+  int s = quant8_backward_impl(dy, dy_dtype, lddy, M, N, xq_codes, xq_scales, K, ws + l.dy, ws + l.dys, ws + l.dyt,
+                               ws + l.dyts, ws + l.xt, ws + l.xts, st);
   if (s != MX_OK) return s;
   s = gemm8_impl(ws + l.dy, l.ld_n, ws + l.dys, l.ls_n, wt_codes, round16(N), wt_scales, scale8_pitch(N), M, K, N,
                  1.0f, dx, dx_dtype, lddx, ws + l.part, st);

@@ -27,6 +27,15 @@ int quant8_tile_impl(const void* x, int dtype, int64_t ldx, int64_t rows, int64_
 int requant8_impl(const uint8_t* codes, int64_t ld, const uint8_t* scales, int64_t scale_ld,
                   int64_t rows, int64_t cols, uint8_t* codes_t, int64_t ld_t, uint8_t* scales_t,
                   int64_t scale_ld_t, hipStream_t st);
+// The 8-bit linear layer's operands, each pair in one launch; M, N, K > 0.
+// Forward: x [M, K] in 1x128 blocks, w [N, K] in tiles (wt: its transpose, or NULL).
+int quant8_forward_impl(const void* x, int x_dtype, int64_t ldx, int64_t M, const void* w, int w_dtype,
+                        int64_t ldw, int64_t N, int64_t K, uint8_t* xq, uint8_t* xs, uint8_t* wq, uint8_t* ws,
+                        uint8_t* wt, uint8_t* wts, hipStream_t st);
+// Backward: dy [M, N] by rows (q, s) and by columns (qt, qts), the 8-bit x [M, K] by columns (xt, xts).
+int quant8_backward_impl(const void* dy, int dtype, int64_t lddy, int64_t M, int64_t N, const uint8_t* xq,
+                         const uint8_t* xs, int64_t K, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* qts,
+                         uint8_t* xt, uint8_t* xts, hipStream_t st);
 size_t gemm8_workspace(int64_t M, int64_t N, int64_t K);
 int gemm8_impl(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t lsa, const uint8_t* b,
                int64_t ldb, const uint8_t* sb, int64_t lsb, int64_t M, int64_t N, int64_t K,

@@ -4,7 +4,11 @@
 // Rows alone (activations in the forward pass) are read, scaled and written by 16 lanes a block.
 // Everything that has columns goes through a 128x128 tile a workgroup: rows and columns come from
 // one read (the two operands that a gradient dY gives, the two layouts of a weight).  All of it
-// moves bytes and computes little: HBM bandwidth bounds it.
+// moves bytes and computes little: HBM bandwidth bounds it (a large copy moves 4.8 TB/s, read and
+// written).  8192x8192, bf16 and float32: rows 32 and 55 us (6.2 TB/s: three or five parts in six are
+// reads), columns 32 and 66, both 49 and 82 (5.5 and 4.9), a weight's tiles in both layouts 47 and 80,
+// the codes' second quantization 30 (4.5).  Rows that do not start at 16 bytes load twice as much a
+// run: 8192x8191 takes 64 and 118 us by rows, 74 and 130 both ways.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -44,6 +48,7 @@ __global__ __launch_bounds__(256) void k_quant8_row(const T* __restrict__ x, int
 // Source of a tile's values: an unquantized matrix, or an 8-bit one by its exact values.
 template <typename T, bool ODD>
 struct Source8 {
+  static constexpr bool kOdd = ODD;
   using Run = Run8<T>;
   const T* x;
   int64_t ld;
@@ -81,18 +86,39 @@ struct Codes8 {  // the codes' columns past cols, up to a multiple of 16, are 0
 // neighbouring rows, and leaves it in 16-byte pieces, 128 bytes of an output row at a time.
 constexpr int kTile8Pitch = 128 + 8;
 
-template <typename SRC, bool TILE>
-__global__ __launch_bounds__(256) void k_quant8_tile(const SRC src, int64_t rows, int64_t cols,
-                                                     int64_t tiles_c, uint8_t* __restrict__ codes,
-                                                     int64_t ld, uint8_t* __restrict__ scales,
-                                                     int64_t scale_ld, uint8_t* __restrict__ codes_t,
-                                                     int64_t ld_t, uint8_t* __restrict__ scales_t,
-                                                     int64_t scale_ld_t) {
-  __shared__ __align__(16) uint8_t s_t[128 * kTile8Pitch];
-  __shared__ uint32_t s_max[4][128];
-  __shared__ uint32_t s_tile[4];
+struct Tile8Lds {
+  __align__(16) uint8_t t[128 * kTile8Pitch];
+  uint32_t max[4][128];
+  uint32_t tile[4];
+};
+
+// What a launch makes of a source: its rows' codes and scales, its columns', or both.
+template <typename SRC>
+struct Tiles8 {
+  SRC src;
+  int64_t rows, cols;
+  uint8_t* codes;
+  int64_t ld;
+  uint8_t* scales;
+  int64_t scale_ld;
+  uint8_t* codes_t;
+  int64_t ld_t;
+  uint8_t* scales_t;
+  int64_t scale_ld_t;
+};
+
+template <bool TILE, typename SRC>
+__device__ __forceinline__ void quant8_tile(const Tiles8<SRC>& q, unsigned block, Tile8Lds& lds) {
+  auto& s_t = lds.t;
+  auto& s_max = lds.max;
+  auto& s_tile = lds.tile;
+  const SRC& src = q.src;
+  const int64_t rows = q.rows, cols = q.cols, ld = q.ld, scale_ld = q.scale_ld, ld_t = q.ld_t, scale_ld_t = q.scale_ld_t;
+  uint8_t *const __restrict__ codes = q.codes, *const __restrict__ scales = q.scales;
+  uint8_t *const __restrict__ codes_t = q.codes_t, *const __restrict__ scales_t = q.scales_t;
+  const unsigned tiles_c = (unsigned)((cols + 127) / 128);
   const int tid = threadIdx.x, c = tid & 15, rg = tid >> 4, wave = tid >> 6;
-  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;
+  const int64_t tr = block / tiles_c, tc = block % tiles_c;
   const int64_t row0 = tr * 128 + rg * 8, col0 = tc * 128 + c * 8;
   float v[8][8];
   {
@@ -181,6 +207,23 @@ __global__ __launch_bounds__(256) void k_quant8_tile(const SRC src, int64_t rows
   }
 }
 
+template <typename SRC, bool TILE>
+__global__ __launch_bounds__(256) void k_quant8_tile(const Tiles8<SRC> q) {
+  __shared__ Tile8Lds lds;
+  quant8_tile<TILE>(q, blockIdx.x, lds);
+}
+
+// Two matrices in one launch, the first's tiles in front: what the linear layer quantizes at a time.  A weight
+// of 1536x384 has 36 tiles, a twentieth of what the device holds at once (12608 rows, forward and backward,
+// 32.6 and 69 us with a launch each, 29.0 and 63 so; 500x384x384 13.7 and 25, 11.4 and 20.5).  At 128 registers
+// for a fourth wave a SIMD the float32 tile spills: 8192x8192 both ways 82 us, 116.
+template <typename A, bool TILE_A, typename B, bool TILE_B>
+__global__ __launch_bounds__(256) void k_quant8_two(const Tiles8<A> a, const Tiles8<B> b, unsigned first) {
+  __shared__ Tile8Lds lds;
+  if (blockIdx.x < first) quant8_tile<TILE_A>(a, blockIdx.x, lds);
+  else quant8_tile<TILE_B>(b, blockIdx.x - first, lds);
+}
+
 // ============================================================== values
 template <typename T>
 __global__ __launch_bounds__(256) void k_dequant8(const Codes8 src, int64_t rows, int64_t cols, int per,
@@ -199,6 +242,15 @@ __global__ __launch_bounds__(256) void k_dequant8(const Codes8 src, int64_t rows
 }
 
 // ============================================================== launches
+// f(the source of a matrix of this type and number of columns)
+template <typename F>
+static int with_source8(const void* x, int dtype, int64_t ldx, int64_t cols, F f) {
+  const float* p = static_cast<const float*>(x);
+  const uint16_t* h = static_cast<const uint16_t*>(x);
+  if (dtype == MX_F32) return cols % 8 ? f(Source8<float, true>{p, ldx}) : f(Source8<float, false>{p, ldx});
+  return cols % 8 ? f(Source8<uint16_t, true>{h, ldx}) : f(Source8<uint16_t, false>{h, ldx});
+}
+
 static unsigned flat_grid(int64_t threads) {
   return (unsigned)hmin(cdiv(threads, 256), (int64_t)device_cu_count() * 64);
 }
@@ -222,36 +274,66 @@ int quant8_row_impl(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t
   return launch_status();
 }
 
+template <typename SRC>
+static int64_t tiles8(const Tiles8<SRC>& q) { return blocks8(q.rows) * blocks8(q.cols); }
+constexpr int64_t kMaxTiles8 = 0xFFFFFFFFll / 256;  // the work-items of a dispatch
+
 template <bool TILE, typename SRC>
-static int launch_tile(const SRC& src, int64_t rows, int64_t cols, uint8_t* codes, int64_t ld, uint8_t* scales,
-                       int64_t scale_ld, uint8_t* codes_t, int64_t ld_t, uint8_t* scales_t, int64_t scale_ld_t,
-                       hipStream_t st) {
-  if (rows == 0 || cols == 0) return MX_OK;
-  const int64_t tiles_c = blocks8(cols), tiles = blocks8(rows) * tiles_c;
-  if (tiles > 0xFFFFFFFFll / 256) return MX_ERR_SHAPE;  // the work-items of a dispatch
-  k_quant8_tile<SRC, TILE><<<dim3((unsigned)tiles), 256, 0, st>>>(src, rows, cols, tiles_c, codes, ld, scales,
-                                                                  scale_ld, codes_t, ld_t, scales_t, scale_ld_t);
+static int launch_tile(const Tiles8<SRC>& q, hipStream_t st) {
+  if (q.rows == 0 || q.cols == 0) return MX_OK;
+  if (tiles8(q) > kMaxTiles8) return MX_ERR_SHAPE;
+  k_quant8_tile<SRC, TILE><<<dim3((unsigned)tiles8(q)), 256, 0, st>>>(q);
+  return launch_status();
+}
+
+template <bool TILE_A, bool TILE_B, typename A, typename B>
+static int launch_two(const Tiles8<A>& a, const Tiles8<B>& b, hipStream_t st) {
+  const int64_t first = tiles8(a), blocks = first + tiles8(b);
+  if (blocks > kMaxTiles8) return MX_ERR_SHAPE;
+  k_quant8_two<A, TILE_A, B, TILE_B><<<dim3((unsigned)blocks), 256, 0, st>>>(a, b, (unsigned)first);
   return launch_status();
 }
 
 int quant8_tile_impl(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t cols, bool tile,
                      uint8_t* codes, int64_t ld, uint8_t* scales, int64_t scale_ld, uint8_t* codes_t,
                      int64_t ld_t, uint8_t* scales_t, int64_t scale_ld_t, hipStream_t st) {
-#define MX_TILE8_ODD(T, TILE, ODD)                                                                        \
-  launch_tile<TILE>(Source8<T, ODD>{static_cast<const T*>(x), ldx}, rows, cols, codes, ld, scales, scale_ld, \
-                    codes_t, ld_t, scales_t, scale_ld_t, st)
-#define MX_TILE8(T, TILE) (cols % 8 ? MX_TILE8_ODD(T, TILE, true) : MX_TILE8_ODD(T, TILE, false))
-  if (dtype == MX_F32) return tile ? MX_TILE8(float, true) : MX_TILE8(float, false);
-  return tile ? MX_TILE8(uint16_t, true) : MX_TILE8(uint16_t, false);
-#undef MX_TILE8
-#undef MX_TILE8_ODD
+  auto run = [&](auto src) {
+    const Tiles8<decltype(src)> q{src, rows, cols, codes, ld, scales, scale_ld, codes_t, ld_t, scales_t, scale_ld_t};
+    return tile ? launch_tile<true>(q, st) : launch_tile<false>(q, st);
+  };
+  return with_source8(x, dtype, ldx, cols, run);
 }
 
 int requant8_impl(const uint8_t* codes, int64_t ld, const uint8_t* scales, int64_t scale_ld, int64_t rows,
                   int64_t cols, uint8_t* codes_t, int64_t ld_t, uint8_t* scales_t, int64_t scale_ld_t,
                   hipStream_t st) {
-  return launch_tile<false>(Codes8{codes, scales, ld, scale_ld}, rows, cols, nullptr, 0, nullptr, 0, codes_t,
-                            ld_t, scales_t, scale_ld_t, st);
+  return launch_tile<false>(Tiles8<Codes8>{{codes, scales, ld, scale_ld}, rows, cols, nullptr, 0, nullptr, 0, codes_t,
+                                           ld_t, scales_t, scale_ld_t}, st);
+}
+
+int quant8_forward_impl(const void* x, int x_dtype, int64_t ldx, int64_t M, const void* w, int w_dtype, int64_t ldw,
+                        int64_t N, int64_t K, uint8_t* xq, uint8_t* xs, uint8_t* wq, uint8_t* ws, uint8_t* wt,
+                        uint8_t* wts, hipStream_t st) {
+  const int64_t ld = round16(K), ls = scale8_pitch(K);
+  return with_source8(w, w_dtype, ldw, K, [&](auto sw) {
+    return with_source8(x, x_dtype, ldx, K, [&](auto sx) {
+      if constexpr (decltype(sw)::kOdd != decltype(sx)::kOdd) return (int)MX_ERR_SHAPE;
+      else return launch_two<true, false>(
+          Tiles8<decltype(sw)>{sw, N, K, wq, ld, ws, ls, wt, round16(N), wts, scale8_pitch(N)},
+          Tiles8<decltype(sx)>{sx, M, K, xq, ld, xs, ls, nullptr, 0, nullptr, 0}, st);
+    });
+  });
+}
+
+int quant8_backward_impl(const void* dy, int dtype, int64_t lddy, int64_t M, int64_t N, const uint8_t* xq,
+                         const uint8_t* xs, int64_t K, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* qts, uint8_t* xt,
+                         uint8_t* xts, hipStream_t st) {
+  return with_source8(dy, dtype, lddy, N, [&](auto src) {
+    return launch_two<false, false>(
+        Tiles8<decltype(src)>{src, M, N, q, round16(N), s, scale8_pitch(N), qt, round16(M), qts, scale8_pitch(M)},
+        Tiles8<Codes8>{{xq, xs, round16(K), scale8_pitch(K)}, M, K, nullptr, 0, nullptr, 0, xt, round16(M), xts,
+                       scale8_pitch(M)}, st);
+  });
 }
 
 }  // namespace mx
