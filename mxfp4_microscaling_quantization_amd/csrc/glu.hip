@@ -25,6 +25,29 @@ __device__ __forceinline__ int64_t live_rows(const int64_t* __restrict__ live, i
   return n < 0 ? 0 : (n < rows ? n : rows);
 }
 
+// Phi(g), and e^(-g^2/2).  With a = |g|, Phi(-a) = e^(-a^2/2) t Q(t), t = 1 / (1 + 0.35 a): Q is the polynomial of
+// degree 8 with the smallest relative error at the Chebyshev points of a <= 15 (weighted least squares with
+// Lawson's weights), 3.2e-8, and with these rounded coefficients 7 * 2^-24 in Phi.  a^2 is carried to its
+// last bit into the exponential.  Beyond a of 15 both are 0.  The library's erfcf with an exponential of its own took
+// 397 us for the gradient of 65536x2880 where SILU takes 283; 302 so.
+__device__ __forceinline__ float normal_below(float g, float* e) {
+  const float a = fminf(fabsf(g), 30.0f), t = __builtin_amdgcn_rcpf(fmaf(a, 0.35f, 1.0f));
+  float q = -0.0291638058f;
+  q = fmaf(q, t, 0.144060239f);
+  q = fmaf(q, t, -0.255900741f);
+  q = fmaf(q, t, 0.159391701f);
+  q = fmaf(q, t, -0.0232630335f);
+  q = fmaf(q, t, 0.105574481f);
+  q = fmaf(q, t, 0.119815573f);
+  q = fmaf(q, t, 0.139864326f);
+  q = fmaf(q, t, 0.139621258f);
+  const float square = a * a, rest = fmaf(a, a, -square);
+  *e = expf(-0.5f * square);
+  *e = fmaf(*e, -0.5f * rest, *e);
+  const float below = q * t * *e;
+  return g < 0.0f ? below : 1.0f - below;
+}
+
 // act(g); with D also its derivative.
 template <bool D>
 __device__ __forceinline__ float activate(float g, int act, float* d) {
@@ -33,8 +56,9 @@ __device__ __forceinline__ float activate(float g, int act, float* d) {
     if (D) *d = s + s * (g * (1.0f - s));
     return g * s;
   }
-  const float phi = 0.5f * erfcf(g * -0.70710678118654752f);
-  if (D) *d = phi + g * (0.39894228040143268f * expf(-0.5f * (g * g)));
+  float e;
+  const float phi = normal_below(g, &e);
+  if (D) *d = phi + g * (0.39894228040143268f * e);
   return g * phi;
 }
 

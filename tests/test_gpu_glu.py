@@ -83,6 +83,19 @@ def test_forward_checkpoint_and_backward(rows, cols, z_type, h_type, act):
 
 
 @pytest.mark.parametrize("act", [O.SILU, O.GELU])
+def test_gates_of_every_size(act):
+    """A fine grid of gates through both tails, and one through the exponents, with up values of 1."""
+    g = np.concatenate((np.linspace(-20, 20, 60001), np.ldexp(np.linspace(1, 2, 17), np.arange(-149, 127)[:, None]).ravel()))
+    g = np.concatenate((g, -g)).astype(np.float32).astype(np.float64)[None]
+    with np.errstate(over="ignore"):
+        want = O.glu(np.concatenate((g, np.ones_like(g)), axis=1), act)
+        error = gate_error(g, act)
+    h = mx.glu(to_dev_f32(np.concatenate((g, np.ones_like(g)), axis=1)), act)
+    far = np.abs(g) > 1e6      # the limits: g and 0 (the bound above takes g^2 past what it means)
+    within(h, want, np.where(far, 0.0, error) * np.abs(want) + U * np.abs(want) + TINY)
+
+
+@pytest.mark.parametrize("act", [O.SILU, O.GELU])
 def test_packed_outputs_are_those_of_the_quantizers(act):
     for rows, cols in ((1, 32), (5, 96), (130, 288), (3, 2880), (64, 1536)):
         z = to_dev_f32(inputs(np.random.default_rng(cols), rows, cols))
