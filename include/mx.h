@@ -467,9 +467,10 @@ int mx_dequantize8(const uint8_t* codes, int64_t ld, const uint8_t* scales, int6
  * in a fixed order, one rounding to nearest even gives a bf16 C.  For a float32 C the products
  * are exact too (of values used down to bits of 2^-133).  A bf16 C takes the 8-bit matrix
  * instructions, at twice the rate: they add the products of eight neighbouring k with 13
- * bits below the largest of them (2e-5 of C's norm for normal operands).  Scale byte 0xFF makes its row's or column's sums NaN.  Up to 64 rows
- * of A the weights B are read once.  workspace: at least mx_gemm8_workspace_size bytes (the partial sums of a sliced
- * contraction; 0: may be NULL), 16-byte aligned. */
+ * bits below the largest of them (2e-5 of C's norm for normal operands).  Scale byte 0xFF makes its
+ * row's or column's sums NaN.  Up to 64 rows of A the weights B are read once.  workspace: at
+ * least mx_gemm8_workspace_size bytes (the partial sums of sliced contractions; 0: may be
+ * NULL), 16-byte aligned. */
 size_t mx_gemm8_workspace_size(int64_t M, int64_t N, int64_t K);
 int mx_gemm8(const uint8_t* a_codes, int64_t lda, const uint8_t* a_scales, int64_t a_scale_ld,
              const uint8_t* b_codes, int64_t ldb, const uint8_t* b_scales, int64_t b_scale_ld,

@@ -227,17 +227,18 @@ __device__ __forceinline__ void tile8_at(const Gemm8Args& g, int id, int64_t* m0
 template <int T, bool SLICED>
 __device__ __forceinline__ Place8 place8(const Gemm8Args& g) {
   Place8 p{0, 0, 0, g.K, -1};
-  int block = blockIdx.x, total = gridDim.x, first = 0;
-  if constexpr (SLICED) {
-    if (block >= g.whole) first = g.whole, block -= first, total -= first;
-    else total = g.whole;
+  int block = blockIdx.x, total = gridDim.x;
+  const bool sliced = SLICED && block >= g.whole;
+  if (SLICED) {
+    block -= sliced ? g.whole : 0;
+    total = sliced ? total - g.whole : g.whole;
   }
   const int q = total / 8, r = total % 8, x = block % 8;
   int id = x * q + min(x, r) + block / 8;
-  if (SLICED && first == g.whole && (int)blockIdx.x >= g.whole) {
+  if (sliced) {
     const int tiles = g.tiles_m * g.tiles_n - g.whole, slice = id / tiles;
     p.part = id;
-    id = first + id - slice * tiles;
+    id += g.whole - slice * tiles;
     p.k0 = slice * g.slice;
     p.klen = lmin8(g.slice, g.K - p.k0);
   }
@@ -699,7 +700,7 @@ __global__ __launch_bounds__(256) void k_gemm8_sum(const Gemm8Args g) {
 // all rows (8 XD of them) and a part of K, and streams both operands through a ring of its own in LDS, four
 // steps of 128 deep: no barrier until the waves' sums meet.  The detour keeps loads whole: eight lanes take a
 // line of 128 bytes (into the operand registers directly, neighbouring lanes take different rows, 16 bytes a
-// clock: one row of 14336x4096 14.8 us, 12.1 so, 47 of 4096x14336 35 us, 22 so), and holds what is
+// clock: one row of 14336x4096 14.8 us, 12.1 so, 47 of 4096x14336 35 us, 17 so), and holds what is
 // in flight, 4 KB a step and up.  Layout of a step as in the tiles: row r's chunks in the order c ^ ((r >> 1) & 7).
 constexpr int kRowsDepth = 4;
 constexpr int rows8_step(int xd, int nt) { return (2 * nt + xd) * 1024; }         // bytes in LDS
@@ -907,11 +908,13 @@ size_t gemm8_workspace(int64_t M, int64_t N, int64_t K) {  // for C of either ty
   return a > b ? a : b;
 }
 
+constexpr int64_t kMaxItems8 = 0xFFFFFFFFll;  // the work-items of a dispatch
+
 template <int T, typename TY, bool SLICED, bool WIDE>
 static int launch_tiles(Gemm8Args g, int64_t whole, hipStream_t st) {
   const int64_t tm = cdiv(g.M, T), tn = cdiv(g.N, T), tail = SLICED ? tm * tn - whole : 0;
   const int64_t blocks = tm * tn - tail + tail * g.slices;
-  if (blocks > 0x7FFFFFFFll / 256) return MX_ERR_SHAPE;
+  if (blocks > kMaxItems8 / 256) return MX_ERR_SHAPE;
   g.tiles_m = (int)tm;
   g.tiles_n = (int)tn;
   g.whole = (int)whole;
@@ -939,6 +942,7 @@ static int launch_rows(const Gemm8Args& g, hipStream_t st) {
   const int64_t most = hmin(hmin(room / kWave, 8), units), per = cdiv(units, most);
   const Rows8Args r{g, (int)steps, (int)per * 4};
   const unsigned waves = (unsigned)cdiv(units, per);
+  if (tiles > kMaxItems8 / (waves * 64)) return MX_ERR_SHAPE;
   k_gemm8_rows<XD, NT, TY><<<dim3((unsigned)tiles), waves * 64, waves * rows8_lds(XD, NT), st>>>(r);
   return launch_status();
 }

@@ -1046,7 +1046,7 @@ def linear8_bwd(dy: torch.Tensor, xq, wq, M, N, K, dx_dtype=torch.float32, works
 
 # ------------------------------------------------------------------ gated activation
 def _glu_rows(rows) -> None:
-    if rows is not None and (rows.dtype != torch.int64 or rows.numel() != 1):
+    if rows is not None and (not isinstance(rows, torch.Tensor) or rows.dtype != torch.int64 or rows.numel() != 1):
         raise ValueError("rows must be one int64 on the device (moe_plan's offs[-1:])")
 
 

@@ -73,6 +73,9 @@ def test_product_validation(L):
     assert call(K=0, lda=0, ldb=0, lsa=0, lsb=0, a=None, b=None, c=None) == mx.MX_ERR_NULL
     size = L.mx_gemm8_workspace_size
     assert size(-1, 4, 4) == size(4, 4, -1) == size(64, 4096, 14336) == size(0, 4, 4096) == size(8192, 14336, 4096) == 0
+    # more work-items than a dispatch can have: of tiles, and of few rows with a long contraction
+    assert call(M=BIG - 1, N=1 << 12, ldc=1 << 12) == call(M=1 << 20, N=1 << 23, ldc=1 << 23) == mx.MX_ERR_SHAPE
+    assert call(M=1, N=BIG - 1, ldc=BIG, K=8192, lda=8192, ldb=8192, lsa=64, lsb=64) == mx.MX_ERR_SHAPE
     need = size(128, 128, 8192)
     assert need >= 2 * 128 * 128 * 4
     long = {"M": 128, "N": 128, "K": 8192, "lda": 8192, "ldb": 8192, "lsa": 64, "lsb": 64, "ldc": 128}
@@ -189,6 +192,7 @@ def test_conveniences_refuse_what_the_library_cannot_see():
         (lambda: mx.glu(torch.zeros(3, 7)), "z must be"),
         (lambda: mx.glu(x, rows=torch.zeros(2, dtype=torch.int64)), "one int64"),
         (lambda: mx.glu(x, rows=torch.zeros(1, dtype=torch.int32)), "one int64"),
+        (lambda: mx.glu(x, rows=2), "one int64"),
         (lambda: mx.glu_quantize(x, out=(u8(2, 16), u8(3, 1))), "packed uint8"),
         (lambda: mx.glu_quantize8(x, out=matrix(3, 32)), "out has 3 rows"),
         (lambda: mx.glu_bwd(x, matrix(3, 64)), "kept has 3 rows"),

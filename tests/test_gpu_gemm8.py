@@ -275,3 +275,82 @@ def test_layer_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), k
+
+
+# ------------------------------------------------------------------ what a caller may also do
+@pytest.mark.parametrize("M", [5, 40, 100, 300])
+def test_code_rows_with_a_pitch(M):
+    """Code rows longer than K rounded up: what lies behind is not looked at (NaN codes, NaN scales)."""
+    N, K, ld = 70, 1210, 1536
+    rng = np.random.default_rng(M)
+    a, b = matrix(rng, M, K), matrix(rng, N, K)
+    want, mag = O.gemm8(a, b)
+    operands = []
+    for q in (a, b):
+        codes = np.full((len(q[0]), ld), 0x7F, np.uint8)
+        codes[:, :1216] = 0
+        codes[:, :K] = q[0]
+        scales = np.full((len(q[0]), 16), 0xFF, np.uint8)
+        scales[:, :q[1].shape[1]] = q[1]
+        operands.append((to_dev_u8(codes), to_dev_u8(scales)))
+    (ca, sa), (cb, sb) = operands
+    size = mx.mx_gemm8_workspace_size(M, N, K)
+    for y_type in ("f32", "bf16"):
+        c = torch.empty((M, N), dtype=torch_type(y_type), device=DEV)
+        ws = torch.empty(max(size, 1), dtype=torch.uint8, device=DEV)
+        mx.mx_gemm8(ca, ld, sa, 16, cb, ld, sb, 16, M, N, K, 1.0, c, mx.dtype_code(c), N, ws, size)
+        check(c, want, mag, K, y_type, M)
+
+
+def random_matrix(rows, K, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return mx.quantize8(torch.randn((rows, K), generator=g, device=DEV, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("M", [3, 130])
+def test_operand_past_2_31_bytes(M):
+    """The first and last rows of a weight of 2.5 GB, as either operand."""
+    K, N = 4096, 620000
+    a, b = random_matrix(M, K, 1), random_matrix(N, K, 2)
+    plain = lambda q: tuple(host(t) for t in q)  # noqa: E731
+    for rows in (slice(0, 256), slice(N - 256, N)):
+        want, mag = O.gemm8(plain(a), plain(t[rows] for t in b))
+        for y_type in ("f32", "bf16"):
+            check(mx.gemm8(a, b, out_dtype=torch_type(y_type))[:, rows], want, mag, K, y_type)
+            if M == 3:
+                check(mx.gemm8(b, a, out_dtype=torch_type(y_type))[rows], want.T, mag.T, K, y_type)
+
+
+def test_output_past_2_31_elements():
+    M, N, K = 40000, 60000, 48
+    a, b = random_matrix(M, K, 3), random_matrix(N, K, 4)
+    got = mx.gemm8(a, b, out_dtype=torch.bfloat16)
+    want, mag = O.gemm8(*((host(c)[-60:, :K], host(s)[-60:, :1]) for c, s in (a, b)))
+    check(got[-60:, -60:], want, mag, K, "bf16")
+
+
+def test_two_calls_at_once_and_a_workspace_shared_in_order():
+    """A sliced product on two streams at once, each with the workspace that its call allocates; then in two
+    graphs that share one and are replayed in turn."""
+    K = 8192
+    a, b = random_matrix(150, K, 5), random_matrix(140, K, 6)
+    want = mx.gemm8(a, b)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [mx.gemm8(a, b, stream=s) for _ in range(8) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    ws = torch.empty(mx.mx_gemm8_workspace_size(150, 140, K), dtype=torch.uint8, device=DEV)
+    assert ws.numel()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], [torch.empty_like(want) for _ in range(2)]
+    for g, out, alpha in zip(graphs, outs, (1.0, -2.0)):
+        with torch.cuda.graph(g):
+            mx.gemm8(a, b, alpha=alpha, out=out, workspace=ws)
+    for _ in range(3):
+        ws.fill_(0xFF)
+        for out in outs:
+            out.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], -2.0 * want)
