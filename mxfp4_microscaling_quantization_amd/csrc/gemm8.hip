@@ -225,9 +225,8 @@ __device__ __forceinline__ void tile8_at(const Gemm8Args& g, int id, int64_t* m0
   *n0 = (int64_t)(id % span / gm) * T;
 }
 template <int T, bool SLICED>
-__device__ __forceinline__ Place8 place8(const Gemm8Args& g) {
+__device__ __forceinline__ Place8 place8(const Gemm8Args& g, int block, int total) {
   Place8 p{0, 0, 0, g.K, -1};
-  int block = blockIdx.x, total = gridDim.x;
   const bool sliced = SLICED && block >= g.whole;
   if (SLICED) {
     block -= sliced ? g.whole : 0;
@@ -288,17 +287,15 @@ constexpr int due8(int at, int turns, int n) { return at <= 0 ? 0 : (at >= turns
 // Everything is on its way for a step at least before the barrier in front of its first read, where
 // its wave waits for it.  Between two products of a wave there is room for a read or a load: 64 cycles.
 template <int T, typename TY, bool SLICED>
-__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm8Args g) {
+__device__ __forceinline__ void tile8(const Gemm8Args& g, int block, int blocks, uint8_t* ring, uint32_t (&s_scale)[2][2 * T]) {
   constexpr int W = T / 64;
   constexpr int LA = T / 32;                   // A loads a wave and step (8 rows each)
   constexpr int NB = W / 2 + 1;                // B tiles loaded in the second half of a step (2 loads each)
   constexpr int kFirst = 2 * (W - NB) + LA, kSecond = 2 * NB;
   constexpr int LS = T / 128;                  // scale loads a wave and four steps (64 rows each)
   constexpr int STAGE = 2 * T * 128;
-  __shared__ __align__(16) uint8_t ring[2 * STAGE];
-  __shared__ __align__(16) uint32_t s_scale[2][2 * T];
 
-  const Place8 at = place8<T, SLICED>(g);
+  const Place8 at = place8<T, SLICED>(g, block, blocks);
   const int64_t m0 = at.m0, n0 = at.n0, klen = at.klen;
   const int KT = (int)((klen + 127) / 128);
   const int tid = threadIdx.x, lane = tid & 63;
@@ -588,13 +585,11 @@ struct Feed8 {
 // barrier a step, in front of its second half: by then every wave has that half in registers, so the step's
 // stage is free for the loads of step p + 2, and the loads of step p + 1, issued a step ago, have landed.
 template <int T, typename TY, bool SLICED>
-__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_wide(const Gemm8Args g) {
+__device__ __forceinline__ void wide8(const Gemm8Args& g, int block, int blocks, uint8_t* ring, uint32_t (&s_scale)[2][2 * T]) {
   using Feed = Feed8<T>;
   constexpr int W = Feed::W, L = Feed::LA + Feed::LB;
-  __shared__ __align__(16) uint8_t ring[2 * Feed::STAGE];
-  __shared__ __align__(16) uint32_t s_scale[2 * 2 * T];
-  const Place8 at = place8<T, SLICED>(g);
-  const Feed feed(g, at, ring, s_scale);
+  const Place8 at = place8<T, SLICED>(g, block, blocks);
+  const Feed feed(g, at, ring, s_scale[0]);
   const int KT = feed.KT;
 
   v16f acc[W][W];
@@ -671,6 +666,38 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_wide(const Gemm
     if ((int64_t)p * 128 + 64 < feed.klen) half(p, I1{}, No{});
   }
   finish8<W, TY, SLICED>(g, at, acc, ring);
+}
+
+template <int T, typename TY, bool SLICED>
+__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_tile(const Gemm8Args g) {
+  __shared__ __align__(16) uint8_t ring[4 * T * 128];
+  __shared__ __align__(16) uint32_t s_scale[2][2 * T];
+  tile8<T, TY, SLICED>(g, blockIdx.x, gridDim.x, ring, s_scale);
+}
+template <int T, typename TY, bool SLICED>
+__global__ __launch_bounds__(256, T == 256 ? 1 : 2) void k_gemm8_wide(const Gemm8Args g) {
+  __shared__ __align__(16) uint8_t ring[4 * T * 128];
+  __shared__ __align__(16) uint32_t s_scale[2][2 * T];
+  wide8<T, TY, SLICED>(g, blockIdx.x, gridDim.x, ring, s_scale);
+}
+
+// Two products in one launch in tiles of 128, x's C of type TY and w's float32: w's workgroups in front, or
+// behind x's.  The second's begin at a multiple of 8, so that each die has whole runs of either's tiles.  One's
+// last, partial round of workgroups runs beside the other's first (the layer's backward, 12608x1536x384 64.1 us
+// by a launch each, 55.5 so; 2048x2048x2048 49 and 41.5; 500x384x384 20.2 and 15.4; 4096x2048x2048 float32 72 and 64).
+template <typename TY>
+__global__ __launch_bounds__(256, 2) void k_gemm8_two(const Gemm8Args x, int x_blocks, const Gemm8Args w, int w_blocks,
+                                                      int w_front) {
+  constexpr int T = 128;
+  __shared__ __align__(16) uint8_t ring[4 * T * 128];
+  __shared__ __align__(16) uint32_t s_scale[2][2 * T];
+  const int front = ((w_front ? w_blocks : x_blocks) + 7) & ~7;
+  const bool behind = (int)blockIdx.x >= front, of_w = behind != (bool)w_front;
+  const int block = behind ? (int)blockIdx.x - front : (int)blockIdx.x, blocks = of_w ? w_blocks : x_blocks;
+  if (block >= blocks) return;
+  if (of_w) wide8<T, float, true>(w, block, blocks, ring, s_scale);
+  else if constexpr (sizeof(TY) == 4) wide8<T, TY, true>(x, block, blocks, ring, s_scale);
+  else tile8<T, TY, true>(x, block, blocks, ring, s_scale);
 }
 
 // The sliced tiles of C: alpha times their slices' sums, in their order.  Eight rows a workgroup.
@@ -856,7 +883,7 @@ __global__ __launch_bounds__(256) void k_gemm8_zero(int64_t M, int64_t N, TY* __
 // ============================================================== launches
 struct Plan8 {
   bool rows, big;
-  int64_t whole;  // slices > 1: tiles of 128 in front of the sliced ones
+  int64_t whole;  // tiles of 128 in front of the sliced ones
   int slices;
   int64_t slice;
 };
@@ -879,7 +906,7 @@ constexpr float kSum8 = 5.0f, kPart8 = 0.018f;
 
 // Few rows take the wave-per-column kernel.  Else tiles by their cost.
 static Plan8 gemm8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
-  Plan8 p{M <= 64, false, 0, 1, K};
+  Plan8 p{M <= 64, false, cdiv(M, 128) * cdiv(N, 128), 1, K};
   if (p.rows) return p;
   const int64_t tiles = cdiv(M, 128) * cdiv(N, 128), tail = tiles % 512;
   const Cost8& c = wide ? kCost8Wide : kCost8;
@@ -910,14 +937,27 @@ size_t gemm8_workspace(int64_t M, int64_t N, int64_t K) {  // for C of either ty
 
 constexpr int64_t kMaxItems8 = 0xFFFFFFFFll;  // the work-items of a dispatch
 
-template <int T, typename TY, bool SLICED, bool WIDE>
-static int launch_tiles(Gemm8Args g, int64_t whole, hipStream_t st) {
-  const int64_t tm = cdiv(g.M, T), tn = cdiv(g.N, T), tail = SLICED ? tm * tn - whole : 0;
-  const int64_t blocks = tm * tn - tail + tail * g.slices;
-  if (blocks > kMaxItems8 / 256) return MX_ERR_SHAPE;
+// The grid of a product in tiles of T, its tiles from `whole` on in slices; 0: too many.
+template <int T>
+static int64_t place_tiles(Gemm8Args& g, int64_t whole) {
+  const int64_t tm = cdiv(g.M, T), tn = cdiv(g.N, T), blocks = whole + (tm * tn - whole) * g.slices;
+  if (blocks > kMaxItems8 / 256) return 0;
   g.tiles_m = (int)tm;
   g.tiles_n = (int)tn;
   g.whole = (int)whole;
+  return blocks;
+}
+
+template <typename TY>
+static int launch_sum(const Gemm8Args& g, hipStream_t st) {
+  k_gemm8_sum<TY><<<dim3((unsigned)(g.tiles_m * g.tiles_n - g.whole) * 16), 256, 0, st>>>(g);
+  return launch_status();
+}
+
+template <int T, typename TY, bool SLICED, bool WIDE>
+static int launch_tiles(Gemm8Args g, int64_t whole, hipStream_t st) {
+  const int64_t blocks = place_tiles<T>(g, whole);
+  if (!blocks) return MX_ERR_SHAPE;
   const dim3 grid((unsigned)blocks);
   if constexpr (!WIDE) {
     k_gemm8_tile<T, TY, SLICED><<<grid, 256, 0, st>>>(g);
@@ -926,7 +966,7 @@ static int launch_tiles(Gemm8Args g, int64_t whole, hipStream_t st) {
   }
   if constexpr (SLICED) {
     if (const int s = launch_status()) return s;
-    k_gemm8_sum<TY><<<dim3((unsigned)tail * 16), 256, 0, st>>>(g);
+    return launch_sum<TY>(g, st);
   }
   return launch_status();
 }
@@ -976,13 +1016,44 @@ static int gemm8_launch(Gemm8Args g, void* workspace, hipStream_t st) {
   return launch_tiles<128, TY, true, kWide>(g, p.whole, st);
 }
 
-int gemm8_impl(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t lsa, const uint8_t* b, int64_t ldb,
-               const uint8_t* sb, int64_t lsb, int64_t M, int64_t N, int64_t K, float alpha, void* c,
-               int c_dtype, int64_t ldc, void* workspace, hipStream_t st) {
-  if (M == 0 || N == 0) return MX_OK;
-  const Gemm8Args g{a, sa, b, sb, lda, lsa, ldb, lsb, M, N, round16(K), c, ldc, nullptr, 0, 0, 0, 1, 0, alpha,
-                    ((uintptr_t)c | ldc * (c_dtype == MX_F32 ? 4 : 2)) % 128 == 0};
-  return c_dtype == MX_F32 ? gemm8_launch<float>(g, workspace, st) : gemm8_launch<uint16_t>(g, workspace, st);
+static Gemm8Args args8(const Product8& p) {
+  return {p.a, p.sa, p.b, p.sb, p.lda, p.lsa, p.ldb, p.lsb, p.M, p.N, round16(p.K), p.c, p.ldc, nullptr, 0, 0, 0, 1, 0, p.alpha,
+          ((uintptr_t)p.c | p.ldc * (p.c_dtype == MX_F32 ? 4 : 2)) % 128 == 0};
+}
+
+int gemm8_impl(const Product8& p, void* workspace, hipStream_t st) {
+  if (p.M == 0 || p.N == 0) return MX_OK;
+  return p.c_dtype == MX_F32 ? gemm8_launch<float>(args8(p), workspace, st) : gemm8_launch<uint16_t>(args8(p), workspace, st);
+}
+
+size_t gemm8_two_workspace(int64_t Mx, int64_t Nx, int64_t Kx, int64_t Mw, int64_t Nw, int64_t Kw) {
+  return gemm8_workspace(Mx, Nx, Kx) + gemm8_workspace(Mw, Nw, Kw);  // whole tiles of 64 KB
+}
+
+template <typename TY>
+static int launch_two(Gemm8Args x, const Plan8& px, Gemm8Args w, const Plan8& pw, hipStream_t st) {
+  const int64_t bx = place_tiles<128>(x, px.whole), bw = place_tiles<128>(w, pw.whole);
+  const bool front = pw.slice > px.slice;  // the longer workgroups first
+  const int64_t blocks = cdiv(front ? bw : bx, 8) * 8 + (front ? bx : bw);
+  if (!bx || !bw || blocks > kMaxItems8 / 256) return MX_ERR_SHAPE;
+  k_gemm8_two<TY><<<dim3((unsigned)blocks), 256, 0, st>>>(x, (int)bx, w, (int)bw, front);
+  int s = launch_status();
+  if (s == MX_OK && px.slices > 1) s = launch_sum<TY>(x, st);
+  if (s == MX_OK && pw.slices > 1) s = launch_sum<float>(w, st);
+  return s;
+}
+
+int gemm8_two_impl(const Product8& x, const Product8& w, void* workspace, hipStream_t st) {
+  const Plan8 px = gemm8_plan(x.M, x.N, round16(x.K), x.c_dtype == MX_F32), pw = gemm8_plan(w.M, w.N, round16(w.K), true);
+  void* after = static_cast<uint8_t*>(workspace) + gemm8_workspace(x.M, x.N, x.K);
+  if (px.rows || px.big || pw.rows || pw.big) {
+    const int s = gemm8_impl(x, workspace, st);
+    return s == MX_OK ? gemm8_impl(w, after, st) : s;
+  }
+  Gemm8Args gx = args8(x), gw = args8(w);
+  gx.slices = px.slices, gx.slice = px.slice, gx.part = static_cast<float*>(workspace);
+  gw.slices = pw.slices, gw.slice = pw.slice, gw.part = static_cast<float*>(after);
+  return x.c_dtype == MX_F32 ? launch_two<float>(gx, px, gw, pw, st) : launch_two<uint16_t>(gx, px, gw, pw, st);
 }
 
 }  // namespace mx
@@ -1013,6 +1084,6 @@ extern "C" int mx_gemm8(const uint8_t* a_codes, int64_t lda, const uint8_t* a_sc
     MX_REQUIRE(workspace && workspace_bytes >= need, MX_ERR_WORKSPACE);
     MX_REQUIRE(aligned16(workspace), MX_ERR_ALIGN);
   }
-  return gemm8_impl(a_codes, lda, a_scales, a_scale_ld, b_codes, ldb, b_scales, b_scale_ld, M, N, K, alpha, c,
-                    c_dtype, ldc, workspace, as_stream(stream));
+  return gemm8_impl({a_codes, a_scales, b_codes, b_scales, lda, a_scale_ld, ldb, b_scale_ld, M, N, K, alpha, c, c_dtype, ldc},
+                    workspace, as_stream(stream));
 }

@@ -12,7 +12,7 @@ namespace mx {
 static int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // The backward's operands in its workspace: dY by rows and by columns, X by columns, the
-// products' partial sums (they run one after the other and share the room).
+// products' partial sums.
 struct Linear8Layout {
   int64_t ld_n, ld_m, ls_n, ls_m;
   int64_t dy, dys, dyt, dyts, xt, xts, part, total;
@@ -30,8 +30,7 @@ static Linear8Layout linear8_layout(int64_t M, int64_t N, int64_t K) {
   l.dy = take(M * l.ld_n), l.dys = take(M * l.ls_n);
   l.dyt = take(N * l.ld_m), l.dyts = take(N * l.ls_m);
   l.xt = take(K * l.ld_m), l.xts = take(K * l.ls_m);
-  const size_t a = gemm8_workspace(M, K, N), b = gemm8_workspace(N, K, M);
-  l.part = take((int64_t)(a > b ? a : b));
+  l.part = take((int64_t)gemm8_two_workspace(M, K, N, N, K, M));
   l.total = at;
   return l;
 }
@@ -88,7 +87,7 @@ extern "C" int mx_linear8_fwd(const void* x, int x_dtype, int64_t ldx, const voi
                            scale8_pitch(N), st);
   }
   if (s != MX_OK) return s;
-  return gemm8_impl(xq_codes, ldk, xq_scales, lsk, wq_codes, ldk, wq_scales, lsk, M, N, K, 1.0f, y, y_dtype, ldy,
+  return gemm8_impl({xq_codes, xq_scales, wq_codes, wq_scales, ldk, lsk, ldk, lsk, M, N, K, 1.0f, y, y_dtype, ldy},
                     workspace, st);
 }
 
@@ -107,8 +106,9 @@ extern "C" int mx_linear8_bwd(const void* dy, int dy_dtype, int64_t lddy, int64_
   MX_REQUIRE((M == 0 || dx) && (N == 0 || dw), MX_ERR_NULL);
   MX_REQUIRE(aligned16(dx) && aligned16(dw), MX_ERR_ALIGN);
   if (M == 0 || N == 0) {  // an empty contraction: the other gradient has no entries
-    if (M) return gemm8_impl(nullptr, 0, nullptr, 0, nullptr, 0, nullptr, 0, M, K, 0, 1.0f, dx, dx_dtype, lddx, nullptr, st);
-    return gemm8_impl(nullptr, 0, nullptr, 0, nullptr, 0, nullptr, 0, N, K, 0, 1.0f, dw, MX_F32, lddw, nullptr, st);
+    const Product8 none = {nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, M ? M : N, K, 0, 1.0f, M ? dx : dw,
+                           M ? dx_dtype : MX_F32, M ? lddx : lddw};
+    return gemm8_impl(none, nullptr, st);
   }
   MX_REQUIRE(dy && xq_codes && xq_scales && wt_codes && wt_scales, MX_ERR_NULL);
   MX_REQUIRE(aligned16(dy) && aligned16(xq_codes) && aligned16(xq_scales) && aligned16(wt_codes) &&
@@ -120,9 +120,9 @@ extern "C" int mx_linear8_bwd(const void* dy, int dy_dtype, int64_t lddy, int64_
   int s = quant8_backward_impl(dy, dy_dtype, lddy, M, N, xq_codes, xq_scales, K, ws + l.dy, ws + l.dys, ws + l.dyt,
                                ws + l.dyts, ws + l.xt, ws + l.xts, st);
   if (s != MX_OK) return s;
-  s = gemm8_impl(ws + l.dy, l.ld_n, ws + l.dys, l.ls_n, wt_codes, round16(N), wt_scales, scale8_pitch(N), M, K, N,
-                 1.0f, dx, dx_dtype, lddx, ws + l.part, st);
-  if (s != MX_OK) return s;
-  return gemm8_impl(ws + l.dyt, l.ld_m, ws + l.dyts, l.ls_m, ws + l.xt, l.ld_m, ws + l.xts, l.ls_m, N, K, M, 1.0f,
-                    dw, MX_F32, lddw, ws + l.part, st);
+  return gemm8_two_impl({ws + l.dy, ws + l.dys, wt_codes, wt_scales, l.ld_n, l.ls_n, round16(N), scale8_pitch(N), M, K, N, 1.0f,
+                         dx, dx_dtype, lddx},
+                        {ws + l.dyt, ws + l.dyts, ws + l.xt, ws + l.xts, l.ld_m, l.ls_m, l.ld_m, l.ls_m, N, K, M, 1.0f, dw,
+                         MX_F32, lddw},
+                        ws + l.part, st);
 }

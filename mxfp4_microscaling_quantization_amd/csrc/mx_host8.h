@@ -37,8 +37,17 @@ int quant8_backward_impl(const void* dy, int dtype, int64_t lddy, int64_t M, int
                          const uint8_t* xs, int64_t K, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* qts,
                          uint8_t* xt, uint8_t* xts, hipStream_t st);
 size_t gemm8_workspace(int64_t M, int64_t N, int64_t K);
-int gemm8_impl(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t lsa, const uint8_t* b,
-               int64_t ldb, const uint8_t* sb, int64_t lsb, int64_t M, int64_t N, int64_t K,
-               float alpha, void* c, int c_dtype, int64_t ldc, void* workspace, hipStream_t st);
+struct Product8 {  // c = alpha a b^T
+  const uint8_t *a, *sa, *b, *sb;
+  int64_t lda, lsa, ldb, lsb, M, N, K;
+  float alpha;
+  void* c;
+  int c_dtype;
+  int64_t ldc;
+};
+int gemm8_impl(const Product8& p, void* workspace, hipStream_t st);
+// Two products (w's C is float32), in one launch where both take tiles of 128; M, N, K > 0.
+size_t gemm8_two_workspace(int64_t Mx, int64_t Nx, int64_t Kx, int64_t Mw, int64_t Nw, int64_t Kw);
+int gemm8_two_impl(const Product8& x, const Product8& w, void* workspace, hipStream_t st);
 
 }  // namespace mx

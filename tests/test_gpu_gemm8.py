@@ -179,6 +179,21 @@ def test_layer(M, N, K, x_type, w_type, y_type):
     check(gdw, dw, dwm, M, "f32", "dw")
 
 
+@pytest.mark.parametrize("M,N,K", [(130, 5000, 70), (5000, 130, 70), (3000, 2900, 100), (66, 4200, 300), (4200, 66, 300)])
+def test_backward_products_in_slices(M, N, K):
+    """Contractions of dX, of dW and of both that are shared between workgroups: every output."""
+    rng = np.random.default_rng(M)
+    x, w, dy = (stored(grid(rng, s, 1.0), "bf16") for s in ((M, K), (N, K), (M, N)))
+    vx, vw, vd = (oracle_input(t, "bf16") for t in (x, w, dy))
+    (_, _), xq, wq = O.linear8_fwd(vx, vw)
+    (dx, dxm), (dw, dwm) = O.linear8_bwd(vd, xq, wq)
+    _, gx, gw = mx.linear8_fwd(upload(x, "bf16"), upload(w, "bf16"))
+    for y_type in ("f32", "bf16"):
+        gdx, gdw = mx.linear8_bwd(upload(dy, "bf16"), gx, gw, M, N, K, dx_dtype=torch_type(y_type))
+        check(gdx, dx, dxm, N, y_type, "dx")
+        check(gdw, dw, dwm, M, "f32", "dw")
+
+
 def test_layer_of_a_kept_weight_and_without_a_backward():
     rng = np.random.default_rng(0)
     x, w = to_dev_f32(grid(rng, (20, 200), 1.0)), to_dev_f32(grid(rng, (60, 200), 0.02))
