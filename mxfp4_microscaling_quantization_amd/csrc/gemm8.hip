@@ -57,7 +57,6 @@ struct Gemm8Args {
   int slices;
   int64_t slice;  // contraction values a slice, a multiple of 512
   float alpha;
-  bool past;      // rows of c are whole lines
 };
 
 // Eight codes times a scale (0xFF: +Inf, which gives NaN), as bf16.
@@ -72,17 +71,16 @@ __device__ __forceinline__ v8bf widen8(uint32_t lo, uint32_t hi, float scale) {
   return v;
 }
 
-// The first n of a run of consecutive outputs (RAW: their 8 or 16 bytes) at T's alignment.  past: they go past
-// the caches' replacement (nontemporal), for outputs that the next launch does not read and that come in whole
-// lines: 6385x11264 of K 32 38.6 us, by ordinary stores 40.2, but 6385x11240, whose rows start within lines,
-// 68 and 41.5.
+// The first n of a run of consecutive outputs (RAW: their 8 or 16 bytes) at T's alignment.  Nontemporal stores
+// of whole lines take as long (8192x14336x4096 380 us, 12608x1536x384 20) and the next launch a little longer
+// (with the gate of C behind it 445 and 441 us); of rows that start within lines, much longer (6385x11240 of
+// K 32 68 and 41.5).
 template <typename T, typename RAW>
-__device__ __forceinline__ void store_run8(T* p, const RAW& raw, int64_t n, bool past) {
+__device__ __forceinline__ void store_run8(T* p, const RAW& raw, int64_t n) {
   typedef RAW avec __attribute__((aligned(sizeof(T))));
   constexpr int V = sizeof(RAW) / sizeof(T);
   if (n >= V) {
-    if (past) __builtin_nontemporal_store(raw, reinterpret_cast<avec*>(p));
-    else *reinterpret_cast<avec*>(p) = raw;
+    *reinterpret_cast<avec*>(p) = raw;
   } else {
     T v[V];
     __builtin_memcpy(v, &raw, sizeof(raw));
@@ -92,13 +90,13 @@ __device__ __forceinline__ void store_run8(T* p, const RAW& raw, int64_t n, bool
   }
 }
 template <typename T>
-__device__ __forceinline__ void store_four8(T* p, const float* v, int64_t n, bool past) {
+__device__ __forceinline__ void store_four8(T* p, const float* v, int64_t n) {
   if constexpr (sizeof(T) == 2) {
     const v2i raw = {(int)bf16_pair(v[0], v[1]), (int)bf16_pair(v[2], v[3])};
-    store_run8(p, raw, n, past);
+    store_run8(p, raw, n);
   } else {
     const v4f raw = {v[0], v[1], v[2], v[3]};
-    store_run8(p, raw, n, past);
+    store_run8(p, raw, n);
   }
 }
 
@@ -159,7 +157,6 @@ struct Out8 {
   void* c;
   int64_t m0, n0, M, N, ldc;
   float alpha;
-  bool past;
 };
 template <int W, typename TY>
 __device__ __forceinline__ void store_tile8(const Out8& g, v16f (&acc)[W][W], uint8_t* ring) {
@@ -205,7 +202,7 @@ __device__ __forceinline__ void store_tile8(const Out8& g, v16f (&acc)[W][W], ui
       const int r = it * (64 / CH) + lane / CH, at = lane % CH;
       const v4i raw = *reinterpret_cast<const v4i*>(stg + r * RB + (at ^ (r & MASK)) * 16);
       const int64_t m = g.m0 + wm + p * 64 + r, n = g.n0 + wn + at * V;
-      if (m < g.M && n < g.N) store_run8(c + m * g.ldc + n, raw, g.N - n, g.past);
+      if (m < g.M && n < g.N) store_run8(c + m * g.ldc + n, raw, g.N - n);
     }
   }
 }
@@ -250,11 +247,11 @@ __device__ __forceinline__ void finish8(const Gemm8Args& g, const Place8& at, v1
   constexpr int T = W * 64;
   if constexpr (SLICED) {
     if (at.part >= 0) {
-      store_tile8<W, float>(Out8{g.part + (int64_t)at.part * T * T, 0, 0, T, T, T, 1.0f, false}, acc, ring);
+      store_tile8<W, float>(Out8{g.part + (int64_t)at.part * T * T, 0, 0, T, T, T, 1.0f}, acc, ring);
       return;
     }
   }
-  store_tile8<W, TY>(Out8{g.c, at.m0, at.n0, g.M, g.N, g.ldc, g.alpha, g.past}, acc, ring);
+  store_tile8<W, TY>(Out8{g.c, at.m0, at.n0, g.M, g.N, g.ldc, g.alpha}, acc, ring);
 }
 
 // This wave's LDS reads have landed, then the workgroup's barrier.
@@ -719,7 +716,7 @@ __global__ __launch_bounds__(256) void k_gemm8_sum(const Gemm8Args g) {
   float v[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = s[e] * g.alpha;
-  store_four8(static_cast<TY*>(g.c) + m * g.ldc + n, v, g.N - n, false);
+  store_four8(static_cast<TY*>(g.c) + m * g.ldc + n, v, g.N - n);
 }
 
 // ============================================================== few rows
@@ -866,7 +863,7 @@ __global__ __launch_bounds__(512) void k_gemm8_rows(const Rows8Args r) {
     float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = sum[e] * g.alpha;
-    if (m < g.M && n < g.N) store_four8(static_cast<TY*>(g.c) + m * g.ldc + n, v, g.N - n, false);
+    if (m < g.M && n < g.N) store_four8(static_cast<TY*>(g.c) + m * g.ldc + n, v, g.N - n);
   }
 }
 
@@ -876,7 +873,7 @@ __global__ __launch_bounds__(256) void k_gemm8_zero(int64_t M, int64_t N, TY* __
   const int64_t runs = (N + 3) / 4, total = M * runs;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const float zero[4] = {};
-    store_four8(c + i / runs * ldc + i % runs * 4, zero, N - i % runs * 4, false);
+    store_four8(c + i / runs * ldc + i % runs * 4, zero, N - i % runs * 4);
   }
 }
 
@@ -1017,8 +1014,7 @@ static int gemm8_launch(Gemm8Args g, void* workspace, hipStream_t st) {
 }
 
 static Gemm8Args args8(const Product8& p) {
-  return {p.a, p.sa, p.b, p.sb, p.lda, p.lsa, p.ldb, p.lsb, p.M, p.N, round16(p.K), p.c, p.ldc, nullptr, 0, 0, 0, 1, 0, p.alpha,
-          ((uintptr_t)p.c | p.ldc * (p.c_dtype == MX_F32 ? 4 : 2)) % 128 == 0};
+  return {p.a, p.sa, p.b, p.sb, p.lda, p.lsa, p.ldb, p.lsb, p.M, p.N, round16(p.K), p.c, p.ldc, nullptr, 0, 0, 0, 1, 0, p.alpha};
 }
 
 int gemm8_impl(const Product8& p, void* workspace, hipStream_t st) {
