@@ -12,7 +12,7 @@
 // 16 lanes hold a token, expert e in lane e % 16, so that sums and maxima stay within a row of
 // lanes; a wave takes 4 tokens.  There is little to read (2 MB for 16384 tokens of 32 experts, 0.5 us):
 // the launches and the chain of top_k selections bound it.  16384 tokens of 32 experts, four each, float32: 5.6 us,
-// the sums 3.3, backward 4.8; 5000 of 128, eight each, bf16: 10.6, 5.2 and 7.2; one launch of 3 to 4 us for a
+// the sums 3.3, backward 4.6; 5000 of 128, eight each, bf16: 7.6, 5.4 and 6.9; one launch of 3 to 4 us for a
 // batch of decoding.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -24,7 +24,15 @@ namespace mx {
 
 constexpr int kRouteMaxK = 16;       // slot j's choice is kept by lane j
 constexpr int kRouteGroups = 256;    // workgroups whose sums the second launch adds up
-constexpr int kRouteAlone = 256;     // up to so many tokens one workgroup does all
+// Up to so many tokens one workgroup does all: 64 tokens of 32 experts, four each, 5.0 us and in two launches 6.8,
+// 128 7.3 and 6.9; 64 of 128 experts, eight each, 9.6 and 11.4, 256 29 and 12.
+constexpr int kRouteAlone = 64;
+// Threads of a workgroup: as many as its tokens, or those of 256 workgroups, have lanes for, 512 or 1024 (24 tokens of
+// 128 experts 6.7 and 9.4 us; 8192 12.8 and 15.2, 65536 42 and 37).
+static int route_threads(int64_t tokens) {
+  return tokens <= 32 || (tokens > kRouteAlone && tokens <= 32 * kRouteGroups) ? 512 : 1024;
+}
+static int64_t route_groups(int64_t tokens) { return hmin(cdiv(tokens, route_threads(tokens) / 16), kRouteGroups); }
 
 // Sums and extremes over the 16 lanes of a row, the same bits in each: neighbours, pairs, halves
 // and the row are mirrored onto each other.
@@ -165,21 +173,20 @@ __device__ __forceinline__ void route_loss(int experts, int top_k, const double*
   }
 }
 
-template <typename T, int EPL, bool ALONE>
-__global__ __launch_bounds__(1024) void k_route(const RouteArgs a, int32_t* __restrict__ ids,
+template <typename T, int EPL, int THREADS, bool ALONE>
+__global__ __launch_bounds__(THREADS) void k_route(const RouteArgs a, int32_t* __restrict__ ids,
                                                               float* __restrict__ p, float* __restrict__ part_sum,
                                                               int32_t* __restrict__ part_cnt,
                                                               int32_t* __restrict__ counts,
                                                               float* __restrict__ sums, float* __restrict__ loss) {
-  constexpr int kThreads = 1024;
-  __shared__ float s_sum[kThreads / 64][128];
+  __shared__ float s_sum[THREADS / 64][128];
   __shared__ int32_t s_cnt[129];
   __shared__ double s_total[128];
-  route_tokens<T, EPL, kThreads>(a, ids, p, s_sum, s_cnt);
+  route_tokens<T, EPL, THREADS>(a, ids, p, s_sum, s_cnt);
   const int e = threadIdx.x;
   if (e < a.experts) {
     double total = 0.0;
-    for (int w = 0; w < kThreads / 64; ++w) total += s_sum[w][e];
+    for (int w = 0; w < THREADS / 64; ++w) total += s_sum[w][e];
     if constexpr (ALONE) s_total[e] = total;
     else part_sum[(int64_t)blockIdx.x * a.experts + e] = (float)total;
   }
@@ -318,7 +325,7 @@ using namespace mx;
 
 extern "C" size_t mx_moe_route_workspace_size(int64_t tokens, int64_t experts, int64_t top_k) {
   if (!route_shape(tokens, experts, top_k) || tokens <= kRouteAlone) return 0;
-  return (size_t)hmin(cdiv(tokens, 64), kRouteGroups) * (2 * experts + 1) * 4;
+  return (size_t)route_groups(tokens) * (2 * experts + 1) * 4;
 }
 
 #define MX_ROUTE_WIDTH(CALL, T)            \
@@ -346,21 +353,28 @@ extern "C" int mx_moe_route(const void* logits, int dtype, int64_t ld, const uin
   }
   const RouteArgs a{logits, ld, tokens, mask, (int)experts, (int)top_k, renormalize};
   const hipStream_t st = as_stream(stream);
-  const int groups = (int)hmin(cdiv(tokens, 64), kRouteGroups);
+  const int groups = (int)route_groups(tokens);
+  const bool half = route_threads(tokens) == 512;
   float* part = static_cast<float*>(workspace);
   int32_t* cnt = reinterpret_cast<int32_t*>(part + (need ? groups * experts : 0));
-#define MX_ROUTE(T, EPL)                                                                                       \
-  do {                                                                                                         \
-    if (need) {                                                                                                \
-      k_route<T, EPL, false><<<groups, 1024, 0, st>>>(a, ids, weights, part, cnt, counts, sums, loss);         \
-      k_route_sum<EPL><<<1, 1024, 0, st>>>(part, cnt, groups, (int)experts, (int)top_k, counts, sums, loss);    \
-    } else {                                                                                                   \
-      k_route<T, EPL, true><<<1, 1024, 0, st>>>(a, ids, weights, part, cnt, counts, sums, loss);               \
-    }                                                                                                          \
+#define MX_ROUTE_TOKENS(T, EPL, THREADS)                                                                        \
+  do {                                                                                                          \
+    if (need)                                                                                                   \
+      k_route<T, EPL, THREADS, false><<<groups, THREADS, 0, st>>>(a, ids, weights, part, cnt, counts, sums, loss); \
+    else                                                                                                        \
+      k_route<T, EPL, THREADS, true><<<1, THREADS, 0, st>>>(a, ids, weights, part, cnt, counts, sums, loss);     \
+  } while (0)
+#define MX_ROUTE(T, EPL)                                                                                          \
+  do {                                                                                                            \
+    if (half) MX_ROUTE_TOKENS(T, EPL, 512);                                                                       \
+    else MX_ROUTE_TOKENS(T, EPL, 1024);                                                                           \
+    if (need)                                                                                                     \
+      k_route_sum<EPL><<<1, 1024, 0, st>>>(part, cnt, groups, (int)experts, (int)top_k, counts, sums, loss);       \
   } while (0)
   if (dtype == MX_F32) MX_ROUTE_WIDTH(MX_ROUTE, float);
   else MX_ROUTE_WIDTH(MX_ROUTE, uint16_t);
 #undef MX_ROUTE
+#undef MX_ROUTE_TOKENS
   return launch_status();
 }
 

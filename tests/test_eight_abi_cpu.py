@@ -140,7 +140,7 @@ def test_gate_validation(L):
 
 def test_router_validation(L):
     size = L.mx_moe_route_workspace_size
-    assert size(256, 8, 2) == size(-1, 8, 2) == size(10000, 0, 1) == size(10000, 129, 1) == size(10000, 8, 9) == size(10000, 32, 17) == 0
+    assert size(16, 8, 2) == size(-1, 8, 2) == size(10000, 0, 1) == size(10000, 129, 1) == size(10000, 8, 9) == size(10000, 32, 17) == 0
     need = size(10000, 8, 2)
     assert need > 0
 

@@ -19,7 +19,8 @@ pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
 SIZES = [(1, 1, 1), (1, 2, 2), (3, 8, 2), (16, 16, 16), (17, 17, 3), (24, 32, 4), (65, 33, 1), (100, 128, 8), (256, 5, 4),
-         (257, 60, 6), (300, 64, 8), (4100, 100, 2), (1000, 128, 16)]
+         (257, 60, 6), (300, 64, 8), (4100, 100, 2), (1000, 128, 16),
+         (33, 128, 8), (64, 30, 3), (8192, 12, 2), (8193, 70, 3)]
 
 
 def inputs(rng, tokens, experts, dtype, ties=False):
