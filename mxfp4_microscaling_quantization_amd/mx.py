@@ -905,15 +905,16 @@ def _check_matrix8(m, what: str, cols=None):
     codes, scales = m
     if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise ValueError(f"{what}: codes and scales are uint8")
-    if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0]:
+    shape, blocks = codes.shape, scales.shape
+    if len(shape) != 2 or len(blocks) != 2 or shape[0] != blocks[0]:
         raise ValueError(f"{what}: codes [rows, cols] and scales [rows, blocks] must have the same rows")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{what}: codes and scales must be contiguous")
-    ld, scale_ld = codes.shape[1], scales.shape[1]
+    (rows, ld), scale_ld = shape, blocks[1]
     cols = ld if cols is None else cols
     if ld % 16 or ld < cols or scale_ld % 4 or scale_ld * 128 < cols:
         raise ValueError(f"{what}: rows of {ld} codes and {scale_ld} scales do not hold {cols} columns")
-    return codes.shape[0], ld, scale_ld
+    return rows, ld, scale_ld
 
 
 def quantize8(x: torch.Tensor, axis=MX_ROW, stream=None):
