@@ -423,8 +423,8 @@ int mx_gemv_grouped(const void* x, int x_dtype, int64_t ldx, int64_t x_rows, con
  * exponent bits of bias 7, three mantissa bits, largest value 448) and scales
  * [rows][scale_ld] (E8M0), one byte per 128 columns; the last block of a row may be
  * shorter.  ld >= cols rounded up to a multiple of 16, ld % 16 == 0, ld <= 2^23; the bytes
- * from cols up to that multiple are 0.  scale_ld >= 4 ceil(cols / 512), scale_ld % 4 == 0;
- * the quantizers fill the last dword of a row with 0.  Any rows and cols.
+ * from cols up to that multiple are 0.  scale_ld >= 4 ceil(cols / 512), scale_ld % 4 == 0,
+ * scale_ld <= 2^23; the quantizers fill the last dword of a row with 0.  Any rows and cols.
  * A block's scale is the smallest 2^e, e >= -127, with max|v| <= 448 2^e (e = -127 for a
  * block of zeros); an element's code is the E4M3 value nearest to v 2^-e, ties to even, with
  * v's sign.  A block holding NaN or Inf gets scale byte 0xFF and zero codes.  Blocks are

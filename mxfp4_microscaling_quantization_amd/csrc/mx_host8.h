@@ -10,12 +10,13 @@ inline int64_t blocks8(int64_t n) { return cdiv(n, 128); }
 inline int64_t scale8_pitch(int64_t n) { return cdiv(n, 512) * 4; }  // whole dwords of bytes
 inline bool float_type(int t) { return t == MX_F32 || t == MX_BF16; }
 constexpr int64_t kMax8 = (int64_t)1 << 31;       // rows and columns are below this
-constexpr int64_t kMaxAxis8 = (int64_t)1 << 23;   // contraction axes: 256 rows span less than 2^31 bytes
+constexpr int64_t kMaxAxis8 = (int64_t)1 << 23;   // contraction axes and pitches: 256 rows span less than 2^31 bytes
 
-// A [rows, cols] 8-bit matrix at these pitches.
+// A [rows, cols] 8-bit matrix at these pitches.  A product keeps offsets within 256 rows of codes and of scales in
+// 32 bits.
 inline bool matrix8(int64_t cols, int64_t ld, int64_t scale_ld) {
   return ld >= round16(cols) && ld % 16 == 0 && ld <= kMaxAxis8 && scale_ld >= scale8_pitch(cols) &&
-         scale_ld % 4 == 0 && scale_ld < kMax8;
+         scale_ld % 4 == 0 && scale_ld <= kMaxAxis8;
 }
 
 int quant8_row_impl(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t cols, uint8_t* codes,

@@ -160,6 +160,44 @@ def test_router_validation(L):
     assert bwd(T=0, x=None, d=None) == mx.MX_OK
 
 
+PITCHES = [(1 << 23) + 4, 16843012, (1 << 31) - 4]     # 16843012: from there on 255 rows span 2^32 bytes
+
+
+@pytest.mark.parametrize("pitch", PITCHES)
+def test_scale_pitches_past_2_23_are_refused(L, pitch):
+    """256 scale rows span less than 2^31 bytes, as 256 code rows do: a product's offsets within a tile have 32
+    bits.  Every call that takes a scale pitch, with no output, so that none could be launched."""
+    def product(lsa=4, lsb=4):
+        return L.mx_gemm8(GOOD, 64, GOOD, lsa, GOOD, 64, GOOD, lsb, 300, 300, 64, 1.0, None, 0, 300, None, 0, None)
+
+    def rows(sld=4):
+        return L.mx_quantize8(GOOD, 0, 40, 5, 40, 0, None, 48, None, sld, None)
+
+    def both(sld=4, sldt=4):
+        return L.mx_quantize8_dual(GOOD, 0, 40, 5, 40, 0, None, 48, None, sld, None, 16, None, sldt, None)
+
+    def again(sld=4, sldt=4):
+        return L.mx_requantize8(GOOD, 48, GOOD, sld, 5, 40, None, 16, None, sldt, None)
+
+    def values(sld=4):
+        return L.mx_dequantize8(GOOD, 48, GOOD, sld, 5, 40, None, 0, 40, None)
+
+    def gate(ksld=4):
+        return L.mx_glu(GOOD, 0, 64, None, 3, 32, 0, None, 1, 32, GOOD, 32, GOOD, ksld, None)
+
+    def gate8(sld=4):
+        return L.mx_glu_quantize8(GOOD, 0, 64, None, 3, 32, 0, None, 32, None, sld, None, 0, None, 0, None)
+
+    def gradient(ksld=4):
+        return L.mx_glu_bwd(GOOD, 1, 32, GOOD, 32, GOOD, ksld, None, 3, 32, 1, None, 0, 64, None)
+
+    for call, names in ((product, ("lsa", "lsb")), (rows, ("sld",)), (both, ("sld", "sldt")), (again, ("sld", "sldt")),
+                        (values, ("sld",)), (gate, ("ksld",)), (gate8, ("sld",)), (gradient, ("ksld",))):
+        for name in names:
+            assert call(**{name: 1 << 23}) == mx.MX_ERR_NULL, (call.__name__, name)     # the shape is taken
+            assert call(**{name: pitch}) == mx.MX_ERR_SHAPE, (call.__name__, name)
+
+
 def u8(*shape):
     return torch.zeros(shape, dtype=torch.uint8)
 
