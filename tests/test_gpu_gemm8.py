@@ -133,6 +133,48 @@ def test_scales_that_are_nan_and_extreme(M):
     check(mx.gemm8(dev(a), dev(b), out_dtype=torch.bfloat16), want, mag, K, "bf16")
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 20, 130), (7, 40, 300), (20, 33, 1200), (40, 50, 640), (64, 8200, 400), (70, 40, 1200),
+                                   (130, 140, 8192), (3900, 3850, 1300)])
+def test_a_nan_scale_over_codes_of_every_value(M, N, K):
+    """Scale byte 0xFF over codes that are not 0 (a caller's own matrix; the quantizers write zeros there): its row
+    of A or of B (a column of C) is NaN, every other output as without it, bit for bit.  By rows, in tiles, in slices
+    and in tiles of 256, with the byte in the first, a middle and the last block of 128."""
+    rng = np.random.default_rng(M + N + K)
+    a, b = matrix(rng, M, K), matrix(rng, N, K)
+    first, last = 0, -(-K // 128) - 1
+    rows, cols = {0: last, M // 2: first, M - 1: last // 2}, {0: first, N // 2: last, N - 1: last // 2}
+    for y_type in ("f32", "bf16"):
+        plain = mx.gemm8(dev(a), dev(b), out_dtype=torch_type(y_type))
+        assert torch.isfinite(plain).all()
+        for of_a, of_b in ((rows, {}), ({}, cols), (rows, cols)):
+            x, y = (a[0], a[1].copy()), (b[0], b[1].copy())
+            for q, which in ((x, of_a), (y, of_b)):
+                for r, block in which.items():
+                    q[1][r, block] = 255
+                    assert q[0][r, 128 * block:128 * block + 128].any()
+            got = mx.gemm8(dev(x), dev(y), out_dtype=torch_type(y_type))
+            nan = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+            nan[list(of_a)] = True
+            nan[:, list(of_b)] = True
+            assert torch.equal(torch.isnan(got), nan), (y_type, len(of_a), len(of_b))
+            assert torch.equal(got[~nan], plain[~nan])
+
+
+def test_a_nan_scale_over_one_code():
+    """Each code but NaN, and zeros, alone under 0xFF."""
+    codes = np.zeros((256, 16), np.uint8)
+    codes[:, 0] = np.arange(256)
+    codes[127, 0] = codes[255, 0] = 1
+    scales = np.full((256, 1), 255, np.uint8)
+    rng = np.random.default_rng(0)
+    b = matrix(rng, 40, 16)
+    for rows in (slice(0, 256), slice(0, 64), slice(64, 128), slice(250, 256)):
+        for y_type in ("f32", "bf16"):
+            a = dev((codes[rows], scales[rows]))
+            assert torch.isnan(mx.gemm8(a, dev(b), out_dtype=torch_type(y_type))).all()
+            assert torch.isnan(mx.gemm8(dev(b), a, out_dtype=torch_type(y_type))).all()
+
+
 def test_empty_sizes():
     e = lambda r, c: torch.zeros((r, c), dtype=torch.uint8, device=DEV)  # noqa: E731
     out = torch.full((3, 5), 7.0, device=DEV)
