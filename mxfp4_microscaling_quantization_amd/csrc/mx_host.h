@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/mx.h"
+#include "mx_int.h"
 
 namespace mx {
 
@@ -19,14 +20,11 @@ inline int launch_status() {
 
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Split-K plan of a GEMM: n chunks of kchunk K-values (the last may be shorter).
 struct SplitPlan {
   int n;
   int64_t kchunk;
 };
-inline int64_t hmin(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // Compute units of the current device (queried once per device; 256 if the
 // runtime cannot tell).

@@ -133,8 +133,11 @@ def test_scales_that_are_nan_and_extreme(M):
     check(mx.gemm8(dev(a), dev(b), out_dtype=torch.bfloat16), want, mag, K, "bf16")
 
 
+NAN_SCALES_SLICED, NAN_SCALES_BIG = [(130, 140, 8192)], [(3900, 3850, 1300)]   # a CPU test looks at their kernels
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 20, 130), (7, 40, 300), (20, 33, 1200), (40, 50, 640), (64, 8200, 400), (70, 40, 1200),
-                                   (130, 140, 8192), (3900, 3850, 1300)])
+                                   *NAN_SCALES_SLICED, *NAN_SCALES_BIG])
 def test_a_nan_scale_over_codes_of_every_value(M, N, K):
     """Scale byte 0xFF over codes that are not 0 (a caller's own matrix; the quantizers write zeros there): its row
     of A or of B (a column of C) is NaN, every other output as without it, bit for bit.  By rows, in tiles, in slices
