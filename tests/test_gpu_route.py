@@ -167,3 +167,71 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def lanes(experts):
+    """Experts of a lane: 16 lanes hold a token."""
+    return 1 if experts <= 16 else 2 if experts <= 32 else 4 if experts <= 64 else 8
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,dtype,renormalize", [
+    (70000, 32, 4, torch.float32, True), (70001, 128, 8, torch.bfloat16, False), (66000, 7, 2, torch.float32, False),
+    (140000, 60, 6, torch.bfloat16, True)])
+def test_many_masked_tokens_in_loops(tokens, experts, top_k, dtype, renormalize):
+    """More tokens than 256 workgroups hold at once, forward and backward, some masked: every row.
+
+    The kernel's own chains set the bounds, with u, d as above and L experts a lane.  An exponential is off by (4 + d) u,
+    a row's sum by L + 3 roundings more, so a softmax term by (2 d + L + 12) u of it.  A lane adds one token a pass,
+    passes = tokens / (256 * 64), two exchanges follow, the workgroup's sum and the whole are rounded once each and
+    added in float64 between: (2 d + L + 16 + passes) u of sums, and of the loss, whose counts are exact.  A weight
+    divided by the sum of its choices: (2 d + top_k + 9) u.  (A pass left out of sums would be 64 / tokens = 9e-4 of
+    them, 15000 u.)"""
+    g = torch.Generator(device=DEV).manual_seed(tokens)
+    x = (3 * torch.randn((tokens, experts), generator=g, device=DEV)).to(dtype)
+    mask = torch.rand(tokens, generator=g, device=DEV) < 0.8
+    x[:, experts // 2] = float("-inf")            # an expert that is closed
+    x[11:tokens:1000] = float("-inf")             # tokens without any
+    part = mask & (x > float("-inf")).any(dim=1)
+    v = torch.where(part[:, None], x.double(), float("-inf"))
+    x[~mask] = float("nan")                       # a masked token's logits are not looked at
+    s = torch.softmax(torch.where(part[:, None], v, 0.0), dim=1) * part[:, None]
+    finite = torch.where(v > float("-inf"), v, float("nan"))[part]
+    d = float((v[part].max(dim=1).values - torch.nan_to_num(finite, nan=float("inf")).min(dim=1).values).max())
+    term = 2 * d + lanes(experts) + 12
+    order = torch.sort(v, dim=1, descending=True, stable=True)
+    choice = order.indices[:, :top_k]
+    there = order.values[:, :top_k] > float("-inf")
+    weight = torch.gather(s, 1, choice) * there
+    share = weight.sum(dim=1, keepdim=True) if renormalize else torch.ones((tokens, 1), dtype=torch.float64, device=DEV)
+    share = torch.where(part[:, None], share, 1.0)
+    n, slots = int(part.sum()), torch.bincount(choice[there], minlength=experts)
+
+    ids, p, counts, sums, loss = mx.moe_route(x, top_k, renormalize, mask)
+    assert torch.equal(ids.long(), torch.where(there, choice, -1))
+    assert torch.equal(counts.long(), torch.cat((slots, torch.tensor([n], device=DEV))))
+    want = weight / share
+    assert torch.all((p.double() - want).abs() <= (2 * d + top_k + 9 if renormalize else term) * U * want)
+    passes = -(-tokens // (256 * 64))
+    want = s.sum(dim=0)
+    assert passes > 4 and torch.all((sums.double() - want).abs() <= (term + 4 + passes) * U * want)
+    want = experts * float((slots.double() * want).sum()) / (n * n * top_k)
+    assert abs(float(loss) - want) <= (term + 4 + passes) * U * want
+
+    dp = torch.randn((tokens, top_k), generator=g, device=DEV)
+    dp = torch.where(there, dp, float("nan"))     # nor at the gradients of slots left out
+    value = torch.where(there, dp.double(), 0.0)
+    for dloss in (None, 0.7 * n):                 # the loss's gradients as large as the weights'
+        d_loss = None if dloss is None else torch.full((1,), dloss, device=DEV)
+        G0 = (0.0 if dloss is None else float(d_loss)) * experts * slots.double() / (n * n * top_k)
+        inner = (weight / share * value).sum(dim=1, keepdim=True) * renormalize
+        bound = (weight / share * value.abs()).sum(dim=1, keepdim=True) * renormalize
+        G = G0.expand(tokens, experts).scatter_add(1, choice, torch.where(there, (value - inner) / share, 0.0))
+        A = G0.expand(tokens, experts).scatter_add(1, choice, torch.where(there, (value.abs() + bound) / share, 0.0))
+        want = s * (G - (s * G).sum(dim=1, keepdim=True))
+        mag = s * (A + (s * A).sum(dim=1, keepdim=True))
+        got = mx.moe_route_bwd(x, ids, counts, dp, d_loss, renormalize, mask)
+        step = STEP["bf16" if dtype == torch.bfloat16 else "f32"]
+        tol = 8 * (experts + top_k + d + 8) * U * mag + step * want.abs() + 2.0 ** -130
+        bad = ~((got.double() - want).abs() <= tol)
+        assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+        assert not got[~part].any()
