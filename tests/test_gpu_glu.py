@@ -8,6 +8,8 @@ sum is off by at most 24 u s (1 + |g|).  g Phi(g): erfc within 8 steps (16 u); i
 of itself, moves erfc(y) by 2 y^2 2u = 2 g^2 u at most; so (20 + 4 g^2) u of the value, and the same of
 both terms of the derivative.  The rounding to the output type adds 2^-24 or 2^-8 of the value.  2^-115
 covers factors below the normal range."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -181,3 +183,40 @@ def test_empty_sizes():
     for rows, cols in ((0, 32), (3, 0)):
         h, kept = mx.glu(torch.zeros((rows, 2 * cols), device=DEV), checkpoint=True)
         assert h.shape == (rows, cols) and mx.glu_bwd(h, kept).shape == (rows, 2 * cols)
+
+
+# The normal distribution is a fit: Phi(-a) = e^(-a^2/2) t Q(t), t = 1 / (1 + 0.35 a), Q of degree 8.  With its float32
+# coefficients it is 1 u off (Q in float64 against erfc over a <= 15); Horner's nine roundings, each carried through the
+# steps behind it, are 3 u of Q (Q's and its partial sums' sizes over t in [0.16, 1]); t is off by one rounding and a
+# reciprocal within a step (3 u), which t Q(t), of condition 2.3 at most, makes 7 u; the exponential within 2 steps (4 u),
+# the rest of a^2 brought into it 1 u; two products 2 u.  In all 18 u of Phi(-a), and at most that of 1 - Phi(-a) >= 1/2
+# with its own rounding: 20 u with the product by g.  The square's rounding, which the kernel takes back, would be
+# g^2 / 2 u: 84 u at 13.  Below 2^-126 the exponential may be anything from 0 on, times t Q(t) g < 1/2.
+NORMAL, BELOW = 20 * U, 2.0 ** -127
+
+
+def test_normal_distribution_in_both_tails():
+    """g Phi(g) within a bound that does not grow with g, at half a million gates of every mantissa."""
+    rng = np.random.default_rng(3)
+    g = np.concatenate((rng.uniform(0, 14, 300000), rng.uniform(9, 13.5, 150000), np.ldexp(rng.uniform(1, 2, 50000),
+                                                                                        rng.integers(-30, 3, 50000))))
+    g = np.concatenate((g, -g)).astype(np.float32).astype(np.float64).reshape(-1, 1000)
+    z = np.concatenate((g, np.ones_like(g)), axis=1)
+    want = O.glu(z, O.GELU)
+    within(mx.glu(to_dev_f32(z), O.GELU), want, NORMAL * np.abs(want) + BELOW)
+
+
+def test_slope_of_every_gate_that_a_checkpoint_holds():
+    """Phi(g) + g phi(g) at each E4M3 value under scales from 2^-24 to 2^5: both terms within the same 20 u (the
+    density's: exponential 5 u, constant, two products); an exponential below 2^-126 comes with a factor 0.4 g < 8."""
+    v = O.E4M3[:127]
+    g = np.concatenate([np.r_[s * v, 0.0] * 2.0 ** e for e in range(-24, 6) for s in (1, -1)])[None]
+    z = np.concatenate((g, np.ones_like(g)), axis=1)
+    _, kept = mx.glu(to_dev_f32(z), O.GELU, checkpoint=True)
+    same(kept, O.quantize8(z.reshape(2, -1)), "checkpoint")
+    assert np.array_equal(O.dequantize8(*O.quantize8(g)), g)
+    dz = mx.glu_bwd(to_dev_f32(np.ones_like(g)), kept, O.GELU)
+    want = O.glu_bwd(np.ones_like(g), g, np.ones_like(g), O.GELU)
+    phi = 0.5 * np.vectorize(math.erfc)(-g / math.sqrt(2))
+    terms = phi + np.abs(g) * np.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+    within(dz, want, np.concatenate((NORMAL * terms, NORMAL * np.abs(want[:, g.shape[1]:])), axis=1) + 16 * BELOW)
