@@ -363,12 +363,7 @@ __device__ __forceinline__ void tile8(const Gemm8Args& g, int block, int blocks,
   };
 
   v16f acc[W][W];
-#pragma unroll
-  for (int a = 0; a < W; ++a)
-#pragma unroll
-    for (int b = 0; b < W; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+  clear8(acc);
 
   // Fragments: both 64-halves of the rows of A, of this step and the next, and of two B tiles.  Half h of a
   // row's 128 bytes: chunks 4 h + 2 lh and the next.
@@ -401,12 +396,6 @@ __device__ __forceinline__ void tile8(const Gemm8Args& g, int block, int blocks,
       y[t] = s[(T + wn + t * 32 + lr) * 4];
     }
   };
-  auto barrier = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-
   // Prologue, in the order of the steps: scales, step 0 but for its last B tiles; those and A of step 1;
   // the first B tiles of step 1.
   issue_scales(0, true);
@@ -418,7 +407,7 @@ __device__ __forceinline__ void tile8(const Gemm8Args& g, int block, int blocks,
   for (int i = 0; i < kSecond; ++i) issue_one(1, LA + i, Maybe8{});
   if (KT > 1) wait_vm<2 * (NB - 1) + kFirst + kSecond>();
   else wait_vm<0>();
-  barrier();
+  barrier8();
   read_scales(0, sa, sb);
 #pragma unroll
   for (int i = 0; i < 4 * W; ++i) read_a(std::integral_constant<int, 0>{}, 0, i);
@@ -434,14 +423,14 @@ __device__ __forceinline__ void tile8(const Gemm8Args& g, int block, int blocks,
     if constexpr (b == 0) {  // B tiles 1 .. W/2 of this step have landed
       if (sure || p + 1 < KT) wait_vm<kFirst + kSecond>();
       else wait_vm<2 * (W - NB)>();
-      barrier();
+      barrier8();
       issue_scales((p >> 2) + 1, (p & 3) == 0 && p + 4 < KT);
     }
     if constexpr (b == W / 2) {  // the other B tiles, A and B tile 0 of the next step have landed
       if (sure || p + 2 < KT) wait_vm<2 * (NB - 1) + kFirst>();
       else if (p + 1 < KT) wait_vm<2 * (NB - 1) + 2 * (W - NB)>();
       else wait_vm<0>();
-      barrier();
+      barrier8();
     }
     if constexpr (b == W - 1) read_scales(p + 1, na, nb);
     constexpr int kReads = second ? 4 + 8 : 4;  // of this turn
