@@ -481,7 +481,8 @@ int mx_gemm8(const uint8_t* a_codes, int64_t lda, const uint8_t* a_scales, int64
  *   Y = Q(X) Q(W)^T;  dX = Q(dY) Q(W);  dW = Q^T(dY) Q^T(Q(X))^T (straight-through)
  * with Q(X), Q(dY) in 1x128 blocks along the contraction, Q(W) in 128x128 tiles, and Q^T the
  * 128x1 blocks along the rows.  X [M, K], W [N, K], Y, dY [M, N]; each with a type and rows
- * ld* elements apart of its own; dw is float32.  The forward writes y and what the backward
+ * ld* elements apart of its own; dw is float32.  A bf16 y or dx takes the 8-bit matrix
+ * instructions, a float32 one exact products, as mx_gemm8's C.  The forward writes y and what the backward
  * takes: the 8-bit checkpoint of X (xq_codes [M][K16], xq_scales [M][4 ceil(K/512)]; K16: K
  * rounded up to a multiple of 16), and the weight in both layouts (wq_codes [N][K16],
  * wq_scales [N][4 ceil(K/512)], wt_codes [K][N16], wt_scales [K][4 ceil(N/512)]).  wt_codes

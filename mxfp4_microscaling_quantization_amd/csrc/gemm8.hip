@@ -12,8 +12,8 @@
 // float32 sum.
 //
 // Many rows are bound by the matrix units at the clock that power leaves (1.7 GHz in the 8-bit loop):
-// 8192x14336x4096, bf16 360 to 375 us (2.6 PFLOP/s; its loop without loads and LDS reads 322);
-// 4096x4096x4096 56 us, float32 106 (1.3 PFLOP/s).  Few rows are bound by reading B: one row of 14336x4096
+// 8192x14336x4096, bf16 360 to 380 us (2.6 PFLOP/s; its loop without loads and LDS reads 322);
+// 4096x4096x4096 55 to 61 us, float32 106 to 111 (1.25 PFLOP/s).  Few rows are bound by reading B: one row of 14336x4096
 // 12 us (4.9 TB/s).
 //
 // Per lane an operand is 32 bytes of one row: row (lane % 32), k [32 (lane / 32), + 32) of the 64 of
@@ -930,8 +930,9 @@ static int launch_tiles(Gemm8Args g, int64_t whole, hipStream_t st) {
 template <int XD, int NT, typename TY>
 static int launch_rows(const Gemm8Args& g, hipStream_t st) {
   // The waves of a workgroup share K: as many as leave room for two workgroups a compute unit, or for one
-  // where there are no more workgroups than units or half the room takes one wave (47 rows of 14336x4096 by
-  // one wave 27 us, by three 24.5; 17 rows by two waves 14.0, by four 15.5).
+  // where there are no more workgroups than units or half the room takes one wave.  14336x4096, weights from HBM
+  // and, second, the same ones each time: 47 rows float32 by one wave 25.3 and 24.5 us, by three 24.0 and 21.3,
+  // bf16 18.0 and 16.2, and 19.9 and 15.9; 17 rows bf16 by two waves 14.5 and 12.7, by four 16.0 and 13.1.
   const int64_t tiles = cdiv(g.N, 16 * NT), steps = cdiv(g.K, 128), units = cdiv(steps, 4);
   constexpr int64_t kLds = 160 * 1024, kWave = rows8_lds(XD, NT);
   const int64_t room = tiles > device_cu_count() && kLds / 2 >= 2 * kWave ? kLds / 2 : kLds;

@@ -18,11 +18,13 @@ struct Plan8 {
 
 // What a product takes in tiles of 256 (one workgroup a compute unit) and of 128 (two), by rounds of
 // workgroups over 256 compute units, in us: a round's own cost and that of 1024 values of K.  Measured,
-// bf16 C: 4096^3 60 us in tiles of 256, 72 in tiles of 128; 12608x1536x384 37 and 22; 6000x3000x1024 47 and
+// bf16 C: 4096^3 55 to 61 us in tiles of 256, 72 in tiles of 128; 12608x1536x384 37 and 22; 6000x3000x1024 47 and
 // 36; 4093x2880x5760 68 and 85; float32 C: 4096^3 106 and 124, 5760x2880x4096 197 and 135 (125 with slices).
 // The last tiles of 128, behind the full rounds, are sliced along K if that costs less: one or two workgroups a
 // compute unit take step1 and step2 for 128 values of K (`few` times that where one or two rows of tiles read B
-// for the first time), the launch that adds the slices up kSum8, a slice of a tile written and read kPart8.
+// for the first time; not for one or two columns of tiles: there A is the long operand, which the launch before has
+// just written, and 14336 rows of 128x4096 take 19.0 us, 128 rows of 14336x4096 unsliced 29.2), the launch that adds
+// the slices up kSum8, a slice of a tile written and read kPart8.
 // Measured, unsliced and in slices of n: float32 C: 36 tiles of K 12608 86 us,
 // (n 5) 27.6, (7) 27.0, (9) 34; 100 of 4096 31.6, (2) 27.2, (4) 28.1; 196 of 2048 20.0, (2) 28.5; 512 + 17 of
 // 4096 135, (8) 124; bf16 C: 36 of 12608 54, (5) 20.3, (7) 21.2; 100 of 4096 18.1, (2) 19.5; 512 + 17 of 4096

@@ -7,7 +7,8 @@
 // One read of z gives h -- in float32, bf16, or already as the packed 4-bit or 8-bit operand of
 // the next product -- and the checkpoint: the 8-bit matrix of the rows' halves, 2 1/64 bytes a
 // column of h instead of the 4 or 8 of z.  16 lanes hold 128 columns of a half, 8 values a lane,
-// so the blocks' maxima are rotations within the 16.  All of it is bound by HBM.
+// so the blocks' maxima are rotations within the 16.  All of it is bound by HBM: 65536x2880, float32 z, as MXFP4
+// operand 320 us (5.0 TB/s), with the checkpoint 399; bf16 z 205 (4.2) and 274, GELU 224 and 294.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

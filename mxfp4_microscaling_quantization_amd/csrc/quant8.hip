@@ -5,10 +5,11 @@
 // Everything that has columns goes through a 128x128 tile a workgroup: rows and columns come from
 // one read (the two operands that a gradient dY gives, the two layouts of a weight).  All of it
 // moves bytes and computes little: HBM bandwidth bounds it (a large copy moves 4.8 TB/s, read and
-// written).  8192x8192, bf16 and float32: rows 32 and 55 us (6.2 TB/s: three or five parts in six are
-// reads), columns 32 and 66, both 49 and 82 (5.5 and 4.9), a weight's tiles in both layouts 47 and 80,
+// written).  8192x8192, bf16 and float32: rows 32 and 55 us (6.2 TB/s: two parts in three or four in five
+// are reads), columns 32 and 66, both 49 and 82 (5.5 and 4.9), a weight's tiles in both layouts 47 and 80,
 // the codes' second quantization 30 (4.5).  Rows that do not start at 16 bytes load twice as much a
-// run: 8192x8191 takes 64 and 118 us by rows, 74 and 130 both ways.
+// run: 8192x8191 takes 64 and 118 us by rows, 74 and 130 both ways.  Values back from the codes: 31
+// and 99 us (6.5 and 3.4 TB/s; one part in three or in five is reads).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

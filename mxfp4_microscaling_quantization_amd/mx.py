@@ -966,7 +966,10 @@ def dequantize8(q, cols=None, out_dtype=torch.float32, stream=None):
 
 
 def gemm8(a, b, alpha=1.0, out=None, out_dtype=torch.float32, workspace=None, stream=None):
-    """alpha A B^T [M, N] of two 8-bit matrices (codes, scales), A [M, K] and B [N, K]."""
+    """alpha A B^T [M, N] of two 8-bit matrices (codes, scales), A [M, K] and B [N, K].  A float32 result
+    sums exact products; a bf16 one takes the 8-bit matrix instructions, which add eight neighbouring products
+    with 13 bits below the largest (2^-10 of their magnitudes at most, 2e-5 of the result's norm on normal
+    operands): where large terms cancel, ask for float32."""
     M, lda, lsa = _check_matrix8(a, "a")
     N, ldb, lsb = _check_matrix8(b, "b")
     if lda != ldb:
@@ -993,7 +996,8 @@ def _check_exact8(m, what: str, rows: int, cols: int) -> None:
 def linear8_fwd(x: torch.Tensor, w, out=None, out_dtype=torch.float32, backward=True, workspace=None, stream=None):
     """(y, xq, wq) of the 8-bit linear layer: y = Q(x) Q(w)^T [M, N] of x [M, K] and w [N, K] (float32 or
     bf16), xq the 8-bit checkpoint of x, wq = (codes, scales, codes_t, scales_t) the weight's tiles in both
-    layouts (the first alone without `backward`).  w may be such a wq of an earlier call."""
+    layouts (the first alone without `backward`).  w may be such a wq of an earlier call.  A bf16 y is summed
+    as a bf16 gemm8."""
     M, K = x.shape
     quantized = not isinstance(w, torch.Tensor)
     if quantized:
@@ -1026,7 +1030,8 @@ def linear8_fwd(x: torch.Tensor, w, out=None, out_dtype=torch.float32, backward=
 
 
 def linear8_bwd(dy: torch.Tensor, xq, wq, M, N, K, dx_dtype=torch.float32, workspace=None, stream=None):
-    """(dx [M, K] of dx_dtype, dw [N, K] float32) of linear8_fwd, given dy [M, N] and what it kept."""
+    """(dx [M, K] of dx_dtype, dw [N, K] float32) of linear8_fwd, given dy [M, N] and what it kept.  A bf16 dx is
+    summed as a bf16 gemm8."""
     if tuple(dy.shape) != (M, N):
         raise ValueError(f"dy must be [{M}, {N}], not {tuple(dy.shape)}")
     if len(wq) != 4:
